@@ -1,7 +1,9 @@
 /*
- * moe.h — C ABI of one rank's MoE expert-layer forward on an AMD Instinct
- * MI355X (gfx950): router top-k, token dispatch, grouped expert GEMM with
- * SwiGLU, and the weighted combine.
+ * moe.h — C ABI of one rank's MoE expert layer on an AMD Instinct MI355X
+ * (gfx950): router top-k, token dispatch, grouped expert GEMM with SwiGLU, and
+ * the weighted combine, with their gradients; and what stands around the
+ * experts: residual add and layer norm, the experts in 8-bit integers, and the
+ * gradient norm with clipping.
  *
  * Sources of the operations (page title, then section):
  *   [EP] "Paralelismo de especialistas" (transformers v5.23.0 docs, pt), with
@@ -324,6 +326,128 @@ moe_status moe_grouped_gemm_backward_saved(const moe_shape* s, moe_dtype dt, con
 moe_status moe_route_topk_backward(const moe_shape* s, const int32_t* topk_idx,
                                    const float* topk_w, const float* d_topk_w, float* d_logits,
                                    hipStream_t stream);
+
+/* ------------------------------------------------------- around the experts
+ * The calls below take 16-byte aligned tensors (MOE_EINVAL otherwise) unless
+ * they say less, and no two of the buffers one call writes may overlap. */
+
+/* Residual add and layer norm of T rows of d elements, the step between one
+ * block's output and the next block's input:
+ *     s    = x + residual, rounded to dt (s = x without a residual)
+ *     mean = sum(s) / d,  rstd = 1 / sqrt(sum((s - mean)^2) / d + eps)
+ *     y    = (s - mean) * rstd * weight + bias
+ * Statistics and arithmetic in fp32; y rounded once.
+ *   x        [T, d] dt, read only.
+ *   residual [T, d] dt, read only, or NULL.
+ *   weight   [d] wdt, bias [d] wdt or NULL; wdt is dt or MOE_F32.
+ *   y        [T, d] dt, written. May be x or residual.
+ *   sum      [T, d] dt, written when residual is given (then required, ignored
+ *            otherwise). May be x or residual, not y.
+ *   mean, rstd [T] fp32, written (4-byte aligned).
+ * A row with an infinity or NaN gets NaN. Uses s->T and s->d only (E, k and the
+ * local range are not looked at). MOE_EINVAL for eps negative or not finite;
+ * MOE_EUNSUPPORTED for d > 32768 or wdt = MOE_BF16 with dt = MOE_F32. */
+moe_status moe_layer_norm(const moe_shape* s, moe_dtype dt, const void* x, const void* residual,
+                          moe_dtype wdt, const void* weight, const void* bias, float eps,
+                          void* y, void* sum, float* mean, float* rstd, hipStream_t stream);
+
+/* Bytes of device workspace moe_layer_norm_backward needs (0 when T = 0): fp32
+ * column sums of up to 512 groups of rows. */
+size_t moe_layer_norm_backward_workspace_bytes(const moe_shape* s);
+
+/* Gradient of moe_layer_norm. With h = (s - mean) * rstd and g = weight * d_y:
+ *     d_x      = rstd * (g - sum(g) / d - h * sum(g * h) / d) + d_s
+ *     d_weight = sum over rows of d_y * h,  d_bias = sum over rows of d_y
+ *   d_y  [T, d] dt, read only: gradient of y.
+ *   sum  [T, d] dt, read only: the forward's s (x without a residual).
+ *   weight, mean, rstd: as for the forward.
+ *   d_s  [T, d] dt, read only, or NULL: the gradient that reaches s on other
+ *        ways (the residual stream), added in fp32 before the rounding.
+ *   d_x  [T, d] dt, written: the gradient of s, which is that of x and that of
+ *        the residual. May be d_y or d_s.
+ *   d_weight [d] wdt, written; d_bias [d] wdt, written, or NULL. Zero when T = 0.
+ *   workspace moe_layer_norm_backward_workspace_bytes(s) bytes.
+ * Column sums are added in a fixed order: the same inputs give the same bits.
+ * Errors as moe_layer_norm. */
+moe_status moe_layer_norm_backward(const moe_shape* s, moe_dtype dt, const void* d_y, const void* sum,
+                                   moe_dtype wdt, const void* weight, const float* mean,
+                                   const float* rstd, const void* d_s, void* d_x, void* d_weight,
+                                   void* d_bias, void* workspace, hipStream_t stream);
+
+/* Experts in 8-bit integers. A row a (an activation row, or an output channel's
+ * weights) is held as codes q and one fp32 scale:
+ *     scale = max(max|a| / 127, 2^-126),  q = rint(a * (1 / scale)),  |q| <= 127
+ * (1 / scale rounded to fp32). A row with an infinity or NaN gets scale NaN and
+ * codes 0, so that every product with it is NaN.
+ * Codes of a matrix of R rows over K are stored in K-blocks of 64:
+ * [ceil(K / 64)][R][64] int8, zero past column K. */
+
+/* Expert weights to 8-bit integers, once before serving.
+ *   w_gate_up [E_loc, d, 2*d_ff] dt, w_down [E_loc, d_ff, d] dt, read only.
+ *   q_gate_up [E_loc][ceil(d / 64)][2*d_ff][64] int8, written;
+ *   scale_gate_up [E_loc, 2*d_ff] fp32, written;
+ *   q_down [E_loc][ceil(d_ff / 64)][d][64] int8, written; scale_down [E_loc, d] fp32, written.
+ * Uses s->d, d_ff, e_begin, e_end. MOE_EUNSUPPORTED for d or d_ff > 65536. */
+moe_status moe_quantize_experts(const moe_shape* s, moe_dtype dt, const void* w_gate_up,
+                                const void* w_down, void* q_gate_up, float* scale_gate_up,
+                                void* q_down, float* scale_down, hipStream_t stream);
+
+/* Bytes of device workspace moe_grouped_gemm_int8 needs (0 when T = 0): codes and
+ * scales of N_max rows of x and of h, and h. */
+size_t moe_grouped_gemm_int8_workspace_bytes(const moe_shape* s);
+
+/* moe_grouped_gemm_gather in 8-bit integers: for each local expert e with rows R,
+ * the rows of x are quantised while they are gathered through perm, then
+ *     [G | U]_R = (q_x @ q_gate_up[e]) * scale_x * scale_gate_up[e]
+ *     H_R = silu(G) * U, rounded to bf16 and quantised row by row
+ *     Y_R = (q_h @ q_down[e]) * scale_h * scale_down[e], rounded to bf16
+ * with exact int32 sums and fp32 scales.
+ *   x [T, d] bf16, perm, offsets: as for moe_grouped_gemm_gather.
+ *   q_gate_up, scale_gate_up, q_down, scale_down: from moe_quantize_experts (or laid out alike).
+ *   y [N_max, d] bf16, written: rows [0, N_loc).
+ *   workspace moe_grouped_gemm_int8_workspace_bytes(s) bytes; contents on entry do
+ *            not matter. Calls that overlap on one workspace race.
+ * MOE_EUNSUPPORTED unless dt = MOE_BF16 and d and d_ff are at most 65536. */
+moe_status moe_grouped_gemm_int8(const moe_shape* s, moe_dtype dt, const void* x, const int32_t* perm,
+                                 const int32_t* offsets, const void* q_gate_up,
+                                 const float* scale_gate_up, const void* q_down,
+                                 const float* scale_down, void* y, void* workspace,
+                                 hipStream_t stream);
+
+/* The gradient norm over a list of tensors, and clipping to it. A list is a HOST
+ * array of n entries, read before the call returns. Tensors are dense, of any
+ * length (0 included) and aligned to their elements only; types may be mixed.
+ *     norm  = sqrt(sum over all tensors of g^2)   (fp64 sums, rounded to fp32 once)
+ *     out_i = g_i * min(1, max_norm / (norm + 1e-6))   (fp32, rounded once)
+ * An infinite norm scales by 0 (infinite elements become NaN), a NaN norm makes
+ * every element NaN. The order of the sums is fixed: the same list gives the same
+ * bits. A list without elements has norm 0. */
+typedef struct {
+  void* data;    /* device pointer, aligned to the element */
+  int64_t numel; /* elements, >= 0 (data may be NULL when 0) */
+  moe_dtype dt;
+} moe_tensor;
+
+/* Bytes of device workspace moe_grad_norm and moe_clip_grad_norm need for a list of n tensors. */
+size_t moe_grad_norm_workspace_bytes(int32_t n);
+
+/* The norm alone, to be joined with other ranks' before moe_clip_grads.
+ *   norm [1] fp32, written.   workspace: 8-byte aligned. */
+moe_status moe_grad_norm(const moe_tensor* grads, int32_t n, float* norm, void* workspace,
+                         hipStream_t stream);
+
+/* Scales by a norm in device memory (norm [1] fp32, read only).
+ *   out: a list of n tensors of the same lengths and types to write to, or NULL to
+ *   scale in place. An entry may be its own gradient. In place, tensors are not
+ *   touched when the factor is 1.
+ * MOE_EINVAL if max_norm is negative or not finite, if two written tensors
+ * overlap, or if a written tensor overlaps a gradient other than its own or its own in part. */
+moe_status moe_clip_grads(const moe_tensor* grads, const moe_tensor* out, int32_t n, const float* norm,
+                          float max_norm, hipStream_t stream);
+
+/* moe_grad_norm, then moe_clip_grads with that norm. Same arguments and errors. */
+moe_status moe_clip_grad_norm(const moe_tensor* grads, const moe_tensor* out, int32_t n, float max_norm,
+                              float* norm, void* workspace, hipStream_t stream);
 
 #ifdef __cplusplus
 }

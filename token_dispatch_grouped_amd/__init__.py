@@ -1,4 +1,4 @@
-"""MI355X (gfx950) MoE expert-layer forward on one rank's share: Python binding.
+"""MI355X (gfx950) MoE expert layer on one rank's share: Python binding.
 
 Thin ctypes marshalling over libmoe.so (include/moe.h). Every step of the path
 runs in the library's HIP kernels; PyTorch only provides device memory and the
@@ -52,6 +52,14 @@ class moe_shape(ctypes.Structure):
     ]
 
 
+class moe_tensor(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("dt", ctypes.c_int),
+    ]
+
+
 _libs: dict = {}
 _debug = os.environ.get("MOE_DEBUG", "") not in ("", "0")
 
@@ -96,6 +104,17 @@ def _load():
             "moe_grouped_gemm_gather_save": (ctypes.c_int, [S, ctypes.c_int, P, P, P, P, P, P, P, P, P, P]),
             "moe_grouped_gemm_backward_saved": (ctypes.c_int,
                                                 [S, ctypes.c_int, P, P, P, P, P, P, P, P, P, P, P, P, P]),
+            "moe_layer_norm": (ctypes.c_int, [S, ctypes.c_int, P, P, ctypes.c_int, P, P, ctypes.c_float, P, P, P, P, P]),
+            "moe_layer_norm_backward_workspace_bytes": (SZ, [S]),
+            "moe_layer_norm_backward": (ctypes.c_int,
+                                        [S, ctypes.c_int, P, P, ctypes.c_int, P, P, P, P, P, P, P, P, P]),
+            "moe_quantize_experts": (ctypes.c_int, [S, ctypes.c_int, P, P, P, P, P, P, P]),
+            "moe_grouped_gemm_int8_workspace_bytes": (SZ, [S]),
+            "moe_grouped_gemm_int8": (ctypes.c_int, [S, ctypes.c_int, P, P, P, P, P, P, P, P, P, P]),
+            "moe_grad_norm_workspace_bytes": (SZ, [I32]),
+            "moe_grad_norm": (ctypes.c_int, [P, I32, P, P, P]),
+            "moe_clip_grads": (ctypes.c_int, [P, P, I32, P, ctypes.c_float, P]),
+            "moe_clip_grad_norm": (ctypes.c_int, [P, P, I32, ctypes.c_float, P, P, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -186,6 +205,50 @@ def _want(t, name: str, dtype=None, shape=None, min_rows=None):
                                  f"got {list(got)}")
         elif got != tuple(shape):
             raise ValueError(f"{name} must have shape {list(shape)}, got {list(got)}")
+
+
+class _On:
+    """Where a call runs: the tensors' GPU, on `stream` or that GPU's current
+    stream. As a context it makes both current, so that memory allocated inside
+    belongs to that stream; tensors that come from another stream are recorded on
+    it, so that freeing them early does not hand their memory out while the call
+    still runs. `_dev` has checked the tensors first."""
+
+    def __init__(self, stream, *ts):
+        torch = _torch()
+        ts = [t for t in ts if t is not None]
+        dev = ts[0].device
+        for t in ts:
+            if t.device != dev:
+                raise ValueError(f"every tensor must be on one GPU, got {dev} and {t.device}")
+        current = torch.cuda.current_stream(dev)
+        self.stream = current if stream is None else stream
+        if self.stream.device != dev:
+            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {dev}")
+        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
+        self.ctx = None
+        if self.stream != current:
+            for t in ts:
+                t.record_stream(self.stream)
+        if self.stream != current or dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+def _aligned(**named):
+    """The calls around the experts move 16-byte vectors from every tensor's first element."""
+    for name, t in named.items():
+        if t is not None and t.data_ptr() % 16:
+            raise ValueError(f"{name} must start at a 16-byte boundary")
 
 
 def _act_dtypes():
@@ -468,11 +531,15 @@ def combine(y, pair_pos, topk_w, T: int, k: int, E: int, e_begin: int, e_end: in
 
 
 def layer(x, logits, w_gate_up, w_down, k: int, e_begin: int, e_end: int, stream=None, fused: bool = False,
-          save: bool = False) -> dict:
+          save: bool = False, norm=None) -> dict:
     """The whole forward of one rank: route -> dispatch -> grouped GEMM -> combine.
     With `fused`, the dispatch writes indices only and the GEMM gathers the rows.
     With `save` (fused path), the gate/up pre-activations are kept in the result
-    as "gu", for layer_backward to use instead of recomputing them."""
+    as "gu", for layer_backward to use instead of recomputing them.
+    With `norm` = (weight, bias or None, eps), out is added to the residual x and
+    normalised (layer_norm): the result has "sum" = x + out, "normed", "mean" and
+    "rstd" as well. On a rank that holds a share of the experts, out is a partial
+    sum over ranks: join the ranks' first and call layer_norm then."""
     torch = _torch()
     T = x.shape[0]
     if logits.dim() != 2 or logits.shape[0] != T:
@@ -480,6 +547,7 @@ def layer(x, logits, w_gate_up, w_down, k: int, e_begin: int, e_end: int, stream
     E = logits.shape[1]
     if save and not fused:
         raise ValueError("save needs the fused path")
+    _check_layer_norm_arg(norm, E, e_begin, e_end)
     idx, w = route_topk(logits, k, stream=stream)
     disp = dispatch(x, idx, E, e_begin, e_end, stream=stream, gather=not fused)
     gu = None
@@ -492,8 +560,26 @@ def layer(x, logits, w_gate_up, w_down, k: int, e_begin: int, e_end: int, stream
     else:
         h, y = grouped_gemm(disp.x_perm, disp.offsets, w_gate_up, w_down, T, k, E, e_begin, e_end, stream=stream)
     out = combine(y, disp.pair_pos, w, T, k, E, e_begin, e_end, stream=stream)
-    return dict(idx=idx, w=w, counts=disp.counts, offsets=disp.offsets, perm=disp.perm,
-                pair_pos=disp.pair_pos, x_perm=disp.x_perm, h=h, y=y, out=out, gu=gu)
+    res = dict(idx=idx, w=w, counts=disp.counts, offsets=disp.offsets, perm=disp.perm,
+               pair_pos=disp.pair_pos, x_perm=disp.x_perm, h=h, y=y, out=out, gu=gu)
+    return _with_norm(res, x, E, e_begin, e_end, norm, stream)
+
+
+def _check_layer_norm_arg(norm, E: int, e_begin: int, e_end: int):
+    if norm is None:
+        return
+    if len(norm) != 3:
+        raise ValueError("norm must be (weight, bias or None, eps)")
+    if (e_begin, e_end) != (0, E):
+        raise ValueError(f"norm needs the whole layer output; experts [{e_begin}, {e_end}) of {E} give a partial sum")
+
+
+def _with_norm(res: dict, x, E: int, e_begin: int, e_end: int, norm, stream) -> dict:
+    if norm is not None:
+        weight, bias, eps = norm
+        res["normed"], res["sum"], res["mean"], res["rstd"] = layer_norm(res["out"], weight, bias, eps, residual=x,
+                                                                         stream=stream)
+    return res
 
 
 # ----------------------------------------------------------------------------- backward
@@ -633,15 +719,340 @@ def route_topk_backward(topk_idx, topk_w, d_topk_w, E: int, d_logits=None, strea
     return d_logits
 
 
-def layer_backward(x, w_gate_up, w_down, fwd: dict, d_out, k: int, e_begin: int, e_end: int, stream=None) -> dict:
+def layer_backward(x, w_gate_up, w_down, fwd: dict, d_out, k: int, e_begin: int, e_end: int, stream=None,
+                   norm=None, d_sum=None) -> dict:
     """The whole backward of one rank, given the forward's dict (from layer()):
     combine -> experts -> row gather -> router softmax. The gate/up
-    pre-activations come from the forward's "gu" when it kept them."""
+    pre-activations come from the forward's "gu" when it kept them.
+    With the forward's `norm`, d_out is the gradient of "normed" (and d_sum, if
+    given, that of "sum"): the result has "d_norm_weight", "d_norm_bias" (None
+    without a bias) and "d_sum", the gradient of x + out. d_x is then still the
+    gradient through the experts alone; x's whole gradient adds d_sum (the
+    residual) and what comes through the logits."""
     T = x.shape[0]
     E = fwd["counts"].shape[0]
+    extra = {}
+    if norm is not None:
+        if "sum" not in fwd:
+            raise ValueError("the forward was run without norm")
+        weight, bias, _ = norm
+        d_out, d_nw, d_nb = layer_norm_backward(d_out, fwd["sum"], weight, fwd["mean"], fwd["rstd"], d_s=d_sum,
+                                                bias=bias is not None, stream=stream)
+        extra = dict(d_sum=d_out, d_norm_weight=d_nw, d_norm_bias=d_nb)
+    elif d_sum is not None:
+        raise ValueError("d_sum needs norm")
     d_y, d_w = combine_backward(d_out, fwd["y"], fwd["pair_pos"], fwd["w"], T, k, E, e_begin, e_end, stream=stream)
     d_x_perm, d_wgu, d_wdn = grouped_gemm_backward(x, fwd["perm"], fwd["offsets"], w_gate_up, w_down, fwd["h"], d_y,
                                                    k, E, e_begin, e_end, stream=stream, gu=fwd.get("gu"))
     d_x = dispatch_backward(d_x_perm, fwd["pair_pos"], T, k, E, e_begin, e_end, stream=stream)
     d_logits = route_topk_backward(fwd["idx"], fwd["w"], d_w, E, stream=stream)
-    return dict(d_y=d_y, d_w=d_w, d_x_perm=d_x_perm, d_w_gate_up=d_wgu, d_w_down=d_wdn, d_x=d_x, d_logits=d_logits)
+    return dict(d_y=d_y, d_w=d_w, d_x_perm=d_x_perm, d_w_gate_up=d_wgu, d_w_down=d_wdn, d_x=d_x, d_logits=d_logits,
+                **extra)
+
+
+# ----------------------------------------------------------------------------- residual add and layer norm
+
+def _norm_params(x, weight, bias, name_d: int):
+    torch = _torch()
+    _want(weight, "weight", (x.dtype, torch.float32), (name_d,))
+    if bias is not None:
+        _want(bias, "bias", weight.dtype, (name_d,))
+
+
+def _rows(x, name: str):
+    _want(x, name, _act_dtypes())
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [T, d], got {list(x.shape)}")
+    return int(x.shape[0]), int(x.shape[1])
+
+
+def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s=None, mean=None, rstd=None,
+               stream=None):
+    """(y, s, mean, rstd): s = x + residual (x itself without one), normalised to
+    y = (s - mean) * rstd * weight + bias, with fp32 statistics [T]. weight and
+    bias [d] are of x's dtype or fp32. y may be x or residual, and so may s."""
+    torch = _torch()
+    T, d = _rows(x, "x")
+    _norm_params(x, weight, bias, d)
+    if residual is not None:
+        _want(residual, "residual", x.dtype, (T, d))
+    elif s is not None:
+        raise ValueError("s is written only with a residual")
+    for name, t in (("y", y), ("s", s)):
+        if t is not None:
+            _want(t, name, x.dtype, (T, d))
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _want(t, name, torch.float32, (T,))
+    _dev(x, weight, bias, residual, y, s, mean, rstd)
+    _aligned(x=x, weight=weight, bias=bias, residual=residual, y=y, s=s)
+    sh = shape(T, d, 8, 1, 1, 0, 1)
+    with _On(stream, x, weight, bias, residual, y, s, mean, rstd) as h:
+        if y is None:
+            y = torch.empty_like(x)
+        if residual is not None and s is None:
+            s = torch.empty_like(x)
+        if mean is None:
+            mean = torch.empty(T, dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        _check(_load().moe_layer_norm(ctypes.byref(sh), _dtype_code(x), _ptr(x), _ptr(residual), _dtype_code(weight),
+                                      _ptr(weight), _ptr(bias), eps, _ptr(y), _ptr(s), _ptr(mean), _ptr(rstd), h),
+               "moe_layer_norm")
+    return y, x if residual is None else s, mean, rstd
+
+
+def layer_norm_backward_workspace_bytes(T: int, d: int) -> int:
+    sh = shape(T, d, 8, 1, 1, 0, 1)
+    return int(_load().moe_layer_norm_backward_workspace_bytes(ctypes.byref(sh)))
+
+
+def layer_norm_backward(d_y, s, weight, mean, rstd, d_s=None, bias: bool = True, d_x=None, d_weight=None, d_bias=None,
+                        workspace=None, stream=None):
+    """(d_x, d_weight, d_bias): the gradient of layer_norm, given the forward's s,
+    mean and rstd. d_s, the gradient that reaches s on other ways, is added to
+    d_x. Without `bias`, d_bias is None. d_x may be d_y or d_s."""
+    torch = _torch()
+    T, d = _rows(d_y, "d_y")
+    _want(s, "s", d_y.dtype, (T, d))
+    _norm_params(d_y, weight, None, d)
+    _want(mean, "mean", torch.float32, (T,))
+    _want(rstd, "rstd", torch.float32, (T,))
+    for name, t in (("d_s", d_s), ("d_x", d_x)):
+        if t is not None:
+            _want(t, name, d_y.dtype, (T, d))
+    for name, t in (("d_weight", d_weight), ("d_bias", d_bias)):
+        if t is not None:
+            _want(t, name, weight.dtype, (d,))
+    if d_bias is not None and not bias:
+        raise ValueError("d_bias is written only with bias")
+    ws_bytes = layer_norm_backward_workspace_bytes(T, d)
+    if workspace is not None:
+        _want(workspace, "workspace", torch.uint8)
+        if workspace.numel() < ws_bytes:
+            raise ValueError(f"workspace must hold at least {ws_bytes} bytes, got {workspace.numel()}")
+    _dev(d_y, s, weight, mean, rstd, d_s, d_x, d_weight, d_bias, workspace)
+    _aligned(d_y=d_y, s=s, weight=weight, d_s=d_s, d_x=d_x, d_weight=d_weight, d_bias=d_bias, workspace=workspace)
+    sh = shape(T, d, 8, 1, 1, 0, 1)
+    with _On(stream, d_y, s, weight, mean, rstd, d_s, d_x, d_weight, d_bias, workspace) as h:
+        if d_x is None:
+            d_x = torch.empty_like(d_y)
+        if d_weight is None:
+            d_weight = torch.empty_like(weight)
+        if d_bias is None and bias:
+            d_bias = torch.empty_like(weight)
+        if workspace is None and ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=d_y.device)
+        _check(_load().moe_layer_norm_backward(ctypes.byref(sh), _dtype_code(d_y), _ptr(d_y), _ptr(s),
+                                               _dtype_code(weight), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(d_s),
+                                               _ptr(d_x), _ptr(d_weight), _ptr(d_bias), _ptr(workspace), h),
+               "moe_layer_norm_backward")
+    return d_x, d_weight, d_bias
+
+
+# ----------------------------------------------------------------------------- experts in 8-bit integers
+
+@dataclass
+class Int8Experts:
+    """The local experts' weights as 8-bit codes in K-blocks of 64 with one fp32
+    scale per output channel: w_gate_up int8 [E_loc, ceil(d / 64), 2 * d_ff, 64],
+    gate_up_scale [E_loc, 2 * d_ff], w_down int8 [E_loc, ceil(d_ff / 64), d, 64],
+    down_scale [E_loc, d]. Weight [e, k, n] is w[e, k // 64, n, k % 64] * scale[e, n]."""
+    w_gate_up: object
+    gate_up_scale: object
+    w_down: object
+    down_scale: object
+
+
+def _kblocks(k: int) -> int:
+    return (k + 63) // 64
+
+
+def _want_int8_experts(experts: Int8Experts, d: int, e_loc: int) -> int:
+    """Checks the quantised experts against the activations; returns d_ff."""
+    torch = _torch()
+    sc = experts.gate_up_scale
+    _want(sc, "gate_up_scale", torch.float32)
+    if sc.dim() != 2 or sc.shape[0] != e_loc or sc.shape[1] % 2:
+        raise ValueError(f"gate_up_scale must be [{e_loc}, 2 * d_ff], got {list(sc.shape)}")
+    d_ff = int(sc.shape[1]) // 2
+    _want(experts.w_gate_up, "w_gate_up", torch.int8, (e_loc, _kblocks(d), 2 * d_ff, 64))
+    _want(experts.w_down, "w_down", torch.int8, (e_loc, _kblocks(d_ff), d, 64))
+    _want(experts.down_scale, "down_scale", torch.float32, (e_loc, d))
+    return d_ff
+
+
+def quantize_experts(w_gate_up, w_down, out: Int8Experts | None = None, stream=None) -> Int8Experts:
+    """The experts' weights (w_gate_up [E_loc, d, 2 * d_ff], w_down [E_loc, d_ff, d])
+    as 8-bit codes, one scale per output channel: once, before serving."""
+    torch = _torch()
+    _want(w_down, "w_down", _act_dtypes())
+    if w_down.dim() != 3:
+        raise ValueError(f"w_down must be [E_loc, d_ff, d], got {list(w_down.shape)}")
+    e_loc, d_ff, d = (int(v) for v in w_down.shape)
+    _want(w_gate_up, "w_gate_up", w_down.dtype, (e_loc, d, 2 * d_ff))
+    if out is not None:
+        _want_int8_experts(out, d, e_loc)
+    mine = () if out is None else (out.w_gate_up, out.gate_up_scale, out.w_down, out.down_scale)
+    _dev(w_gate_up, w_down, *mine)
+    _aligned(w_gate_up=w_gate_up, w_down=w_down)
+    if out is not None:
+        _aligned(out_gate_up=out.w_gate_up, out_down=out.w_down)
+    s = shape(0, d, d_ff, max(e_loc, 1), 1, 0, e_loc)
+    dev = w_down.device
+    with _On(stream, w_gate_up, w_down, *mine) as h:
+        if out is None:
+            out = Int8Experts(torch.empty((e_loc, _kblocks(d), 2 * d_ff, 64), dtype=torch.int8, device=dev),
+                              torch.empty((e_loc, 2 * d_ff), dtype=torch.float32, device=dev),
+                              torch.empty((e_loc, _kblocks(d_ff), d, 64), dtype=torch.int8, device=dev),
+                              torch.empty((e_loc, d), dtype=torch.float32, device=dev))
+        _check(_load().moe_quantize_experts(ctypes.byref(s), _dtype_code(w_down), _ptr(w_gate_up), _ptr(w_down),
+                                            _ptr(out.w_gate_up), _ptr(out.gate_up_scale), _ptr(out.w_down),
+                                            _ptr(out.down_scale), h), "moe_quantize_experts")
+    return out
+
+
+def grouped_gemm_int8_workspace_bytes(T: int, d: int, d_ff: int, E: int, k: int, e_begin: int, e_end: int) -> int:
+    s = shape(T, d, d_ff, E, k, e_begin, e_end)
+    return int(_load().moe_grouped_gemm_int8_workspace_bytes(ctypes.byref(s)))
+
+
+def grouped_gemm_int8(x, perm, offsets, experts: Int8Experts, k: int, E: int, e_begin: int, e_end: int, y=None,
+                      workspace=None, stream=None):
+    """y [N_max, d]: the local experts' SwiGLU FFN in 8-bit integers, on rows of x
+    (bf16) quantised as they are gathered through perm."""
+    torch = _torch()
+    _range(E, k, e_begin, e_end)
+    _want(x, "x", torch.bfloat16)
+    T, d = _rows(x, "x")
+    n_max = _n_max(T, k, e_begin, e_end)
+    _want(perm, "perm", torch.int32, (T * k,))
+    _want(offsets, "offsets", torch.int32, (E + 1,))
+    d_ff = _want_int8_experts(experts, d, e_end - e_begin)
+    if y is not None:
+        _want(y, "y", x.dtype, (n_max, d), min_rows=n_max)
+    s = shape(T, d, d_ff, E, k, e_begin, e_end)
+    ws_bytes = int(_load().moe_grouped_gemm_int8_workspace_bytes(ctypes.byref(s)))
+    if workspace is not None:
+        _want(workspace, "workspace", torch.uint8)
+        if workspace.numel() < ws_bytes:
+            raise ValueError(f"workspace must hold at least {ws_bytes} bytes, got {workspace.numel()}")
+    wgu, sgu, wdn, sdn = experts.w_gate_up, experts.gate_up_scale, experts.w_down, experts.down_scale
+    _dev(x, perm, offsets, wgu, sgu, wdn, sdn, y, workspace)
+    _aligned(x=x, w_gate_up=wgu, w_down=wdn, y=y, workspace=workspace)
+    with _On(stream, x, perm, offsets, wgu, sgu, wdn, sdn, y, workspace) as h:
+        if y is None:
+            y = torch.empty((n_max, d), dtype=x.dtype, device=x.device)
+        if workspace is None and ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+        _check(_load().moe_grouped_gemm_int8(ctypes.byref(s), _dtype_code(x), _ptr(x), _ptr(perm), _ptr(offsets),
+                                             _ptr(wgu), _ptr(sgu), _ptr(wdn), _ptr(sdn), _ptr(y), _ptr(workspace), h),
+               "moe_grouped_gemm_int8")
+    return y
+
+
+def layer_int8(x, logits, experts: Int8Experts, k: int, e_begin: int, e_end: int, stream=None, norm=None) -> dict:
+    """layer() for serving, with the experts in 8-bit integers: route -> dispatch
+    (indices) -> grouped_gemm_int8 -> combine, and with `norm` the residual add
+    and layer norm."""
+    T = x.shape[0]
+    if logits.dim() != 2 or logits.shape[0] != T:
+        raise ValueError(f"logits must be [T={T}, E], got {list(logits.shape)}")
+    E = logits.shape[1]
+    _check_layer_norm_arg(norm, E, e_begin, e_end)
+    idx, w = route_topk(logits, k, stream=stream)
+    disp = dispatch(x, idx, E, e_begin, e_end, stream=stream, gather=False)
+    y = grouped_gemm_int8(x, disp.perm, disp.offsets, experts, k, E, e_begin, e_end, stream=stream)
+    out = combine(y, disp.pair_pos, w, T, k, E, e_begin, e_end, stream=stream)
+    res = dict(idx=idx, w=w, counts=disp.counts, offsets=disp.offsets, perm=disp.perm, pair_pos=disp.pair_pos, y=y,
+               out=out)
+    return _with_norm(res, x, E, e_begin, e_end, norm, stream)
+
+
+# ----------------------------------------------------------------------------- gradient norm and clipping
+
+def _tensor_list(ts, name: str):
+    """The host array of a list of gradients, after checking them."""
+    torch = _torch()
+    if torch.is_tensor(ts):
+        raise TypeError(f"{name} must be a list of tensors")
+    ts = list(ts)
+    if not ts:
+        raise ValueError(f"{name} is empty")
+    arr = (moe_tensor * len(ts))()
+    for i, t in enumerate(ts):
+        _want(t, f"{name}[{i}]", _act_dtypes())
+        arr[i] = moe_tensor(t.data_ptr(), t.numel(), _dtype_code(t))
+    return ts, arr
+
+
+def grad_norm_workspace_bytes(n: int) -> int:
+    return int(_load().moe_grad_norm_workspace_bytes(n))
+
+
+def _norm_buffers(ts, norm, workspace):
+    torch = _torch()
+    if norm is not None:
+        _want(norm, "norm", torch.float32, (1,))
+    need = grad_norm_workspace_bytes(len(ts))
+    if workspace is not None:
+        _want(workspace, "workspace", torch.uint8)
+        if workspace.numel() < need or workspace.data_ptr() % 8:
+            raise ValueError(f"workspace must hold at least {need} bytes at an 8-byte boundary")
+    return need
+
+
+def _clip_out(ts, out):
+    if out is None:
+        return [], None
+    out, arr = _tensor_list(out, "out")
+    if len(out) != len(ts):
+        raise ValueError(f"out must hold {len(ts)} tensors, got {len(out)}")
+    for i, (o, t) in enumerate(zip(out, ts)):
+        _want(o, f"out[{i}]", t.dtype, tuple(t.shape))
+    return out, arr
+
+
+def grad_norm(grads, norm=None, workspace=None, stream=None):
+    """norm [1] fp32: the 2-norm over a list of gradients (bf16 or fp32, dense, any
+    length and alignment), summed in fp64."""
+    torch = _torch()
+    ts, arr = _tensor_list(grads, "grads")
+    need = _norm_buffers(ts, norm, workspace)
+    _dev(*ts, norm, workspace)
+    with _On(stream, *ts, norm, workspace) as h:
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device=ts[0].device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=ts[0].device)
+        _check(_load().moe_grad_norm(arr, len(ts), _ptr(norm), _ptr(workspace), h), "moe_grad_norm")
+    return norm
+
+
+def clip_grads(grads, norm, max_norm: float, out=None, stream=None) -> None:
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)) for a norm [1] fp32
+    in device memory, in place or into the tensors of `out`."""
+    torch = _torch()
+    ts, arr = _tensor_list(grads, "grads")
+    outs, out_arr = _clip_out(ts, out)
+    _want(norm, "norm", torch.float32, (1,))
+    _dev(*ts, *outs, norm)
+    with _On(stream, *ts, *outs, norm) as h:
+        _check(_load().moe_clip_grads(arr, out_arr, len(ts), _ptr(norm), max_norm, h), "moe_clip_grads")
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, norm=None, workspace=None, stream=None):
+    """grad_norm, then clip_grads with it; returns the norm [1] before clipping."""
+    torch = _torch()
+    ts, arr = _tensor_list(grads, "grads")
+    outs, out_arr = _clip_out(ts, out)
+    need = _norm_buffers(ts, norm, workspace)
+    _dev(*ts, *outs, norm, workspace)
+    with _On(stream, *ts, *outs, norm, workspace) as h:
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device=ts[0].device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=ts[0].device)
+        _check(_load().moe_clip_grad_norm(arr, out_arr, len(ts), max_norm, _ptr(norm), _ptr(workspace), h),
+               "moe_clip_grad_norm")
+    return norm

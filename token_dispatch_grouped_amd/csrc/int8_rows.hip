@@ -1,0 +1,203 @@
+// Quantisation to 8-bit integers for the experts' products: activation rows with
+// one scale per row (dynamic, taken from the row itself), weights with one scale
+// per output channel (once, before serving).
+//
+//   scale = max(max|a| / 127, 2^-126),  q = rint(a * (1 / scale))
+//
+// so a = q * scale to within half a step, a row of zeros gives q = 0, and no
+// division by zero or overflow of 1 / scale can occur. A row (or channel) that
+// holds an infinity or a NaN gets scale = NaN and q = 0: every product with it is
+// NaN, as it would be in floating point.
+//
+// Both operands of the products are kept in K-blocks of 64: block kb of a matrix
+// of R rows holds [R][64] bytes, columns 64 kb .. 64 kb + 63 of every row, zero
+// past the last column. A K = 64 stage of a tile is then one contiguous run.
+// Everything here is bound by HBM: a row is read once and its codes written once.
+#include "row_group.h"
+
+namespace moe {
+namespace {
+
+using namespace rows;
+
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
+
+__device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
+
+// scale and 1 / scale from the largest absolute value's bits (as unsigned
+// integers these order like the values, infinities and NaN above all others)
+__device__ __forceinline__ void scale_of(uint32_t amax_bits, float* scale, float* inv) {
+  if (amax_bits >= 0x7F800000u) {
+    *scale = __uint_as_float(0x7FC00000u);
+    *inv = 0.f;
+  } else {
+    *scale = fmaxf(__uint_as_float(amax_bits) / 127.f, kMinScale);
+    *inv = 1.f / *scale;
+  }
+}
+
+__device__ __forceinline__ uint32_t code(float f, float inv) {
+  // inv = 0 marks a row without finite scale
+  return inv == 0.f ? 0u : static_cast<uint32_t>(static_cast<int>(rintf(f * inv))) & 0xFFu;
+}
+
+__device__ __forceinline__ uint2 codes8(const float* f, float inv) {
+  uint2 o;
+  o.x = code(f[0], inv) | code(f[1], inv) << 8 | code(f[2], inv) << 16 | code(f[3], inv) << 24;
+  o.y = code(f[4], inv) | code(f[5], inv) << 8 | code(f[6], inv) << 16 | code(f[7], inv) << 24;
+  return o;
+}
+
+template <int G>
+constexpr int block_threads() { return G > 256 ? G : 256; }
+
+// Rows [0, N_loc) of the local segment: row r is row perm[seg0 + r] / k of src
+// (perm != nullptr: the dispatch's row gather) or row r. G threads per row, VPT
+// vectors of 8 bf16 per thread; the row's K-blocks are filled up with zeros.
+template <int G, int VPT>
+__global__ __launch_bounds__(block_threads<G>()) void quantize_rows_kernel(
+    const uint4* __restrict__ src, const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets,
+    uint8_t* __restrict__ q, float* __restrict__ scale, int e_begin, int e_end, int k, int64_t T, int cols_vec,
+    int kblocks, int64_t n_max) {
+  constexpr int kRows = block_threads<G>() / G;
+  __shared__ uint32_t lds[G > kWave ? G / kWave : 1];
+  const int seg0 = offsets[e_begin];
+  const int64_t n_loc = min(static_cast<int64_t>(offsets[e_end] - seg0), n_max);
+  const int li = static_cast<int>(threadIdx.x) % G;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < n_loc;
+       r0 += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int64_t r = r0 + threadIdx.x / G;
+    const bool live = r < n_loc;
+    const int64_t from = !live ? 0 : perm != nullptr ? perm[seg0 + r] / k : r;
+    const int n = live && (perm == nullptr || (from >= 0 && from < T)) ? cols_vec : 0;
+    uint4 v[VPT];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * G + li;
+      v[i] = c < n ? src[from * cols_vec + c] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float f[8];
+      Vec16<true>::unpack(v[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = Max::apply(top, abs_bits(f[j]));
+    }
+    top = group_reduce<G, Max>(top, lds);
+    float sc, inv;
+    scale_of(top, &sc, &inv);
+    if (live && li == 0) scale[r] = sc;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * G + li;
+      if (live && c < kblocks * 8) {
+        float f[8];
+        Vec16<true>::unpack(v[i], f);
+        *reinterpret_cast<uint2*>(q + (static_cast<int64_t>(c >> 3) * n_max + r) * 64 + (c & 7) * 8) = codes8(f, inv);
+      }
+    }
+  }
+}
+
+// Weights [K, N] of each expert (row-major, N-contiguous) to codes in K-blocks
+// [K / 64][N][64] with one scale per channel. A workgroup takes 64 channels of an
+// expert: a pass for the channels' largest values, then a pass that turns 64 x 64
+// blocks through LDS.
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize_weights_kernel(const void* __restrict__ w, uint8_t* __restrict__ q,
+                                                               float* __restrict__ scale, int K, int N) {
+  __shared__ uint32_t tops[4][64];
+  __shared__ float invs[64];
+  __shared__ uint32_t turn[64][17];  // [channel][16 words of 4 codes + 1]
+  const int tiles = (N + 63) / 64;
+  const int64_t e = blockIdx.x / tiles;
+  const int n0 = static_cast<int>(blockIdx.x % tiles) * 64;
+  const int lane = lane_id(), wv = static_cast<int>(threadIdx.x) / kWave;
+  const int n = n0 + lane;
+  auto at = [&](int k) -> float {
+    const int64_t i = (e * K + k) * N + n;
+    return BF16 ? bf16_to_f32(static_cast<const uint16_t*>(w)[i]) : static_cast<const float*>(w)[i];
+  };
+  uint32_t top = 0;
+  if (n < N)
+#pragma unroll 8
+    for (int k = wv; k < K; k += 4) top = Max::apply(top, abs_bits(at(k)));
+  tops[wv][lane] = top;
+  __syncthreads();
+  if (wv == 0) {
+    for (int i = 1; i < 4; ++i) top = Max::apply(top, tops[i][lane]);
+    float sc, inv;
+    scale_of(top, &sc, &inv);
+    invs[lane] = inv;
+    if (n < N) scale[e * N + n] = sc;
+  }
+  __syncthreads();
+  const float inv = invs[lane];
+  const int kblocks = (K + 63) / 64;
+  for (int kb = 0; kb < kblocks; ++kb) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int kw = wv * 4 + j;  // word kw: rows 64 kb + 4 kw ..
+      uint32_t word = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int k = kb * 64 + kw * 4 + b;
+        if (n < N && k < K) word |= code(at(k), inv) << (8 * b);
+      }
+      turn[lane][kw] = word;
+    }
+    __syncthreads();
+    uint32_t* out = reinterpret_cast<uint32_t*>(q) + ((e * kblocks + kb) * static_cast<int64_t>(N) + n0) * 16;
+    for (int i = threadIdx.x; i < 64 * 16; i += 256)
+      if (n0 + i / 16 < N) out[i] = turn[i / 16][i % 16];
+    __syncthreads();
+  }
+}
+
+template <int G, int VPT>
+hipError_t launch_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale, int e_begin,
+                       int e_end, int k, int64_t T, int cols, int64_t n_max, hipStream_t stream) {
+  constexpr int kRows = block_threads<G>() / G;
+  const int64_t blocks = (n_max + kRows - 1) / kRows;
+  hipLaunchKernelGGL((quantize_rows_kernel<G, VPT>), dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)),
+                     dim3(block_threads<G>()), 0, stream, static_cast<const uint4*>(src), perm, offsets,
+                     static_cast<uint8_t*>(q), scale, e_begin, e_end, k, T, cols / 8, (cols + 63) / 64, n_max);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int int8_kblocks(int K) { return (K + 63) / 64; }
+
+int64_t int8_max_k() { return 65536; }
+
+hipError_t launch_quantize_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale,
+                                int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max,
+                                hipStream_t stream) {
+  const int vec = int8_kblocks(cols) * 8;  // the padded row, in vectors of 8 elements
+#define MOE_QROWS(G, VPT) \
+  return launch_rows<G, VPT>(src, perm, offsets, q, scale, e_begin, e_end, k, T, cols, n_max, stream)
+  if (vec <= 64) MOE_QROWS(64, 1);
+  if (vec <= 256) MOE_QROWS(64, 4);
+  if (vec <= 512) MOE_QROWS(64, 8);
+  if (vec <= 1024) MOE_QROWS(256, 4);
+  if (vec <= 2048) MOE_QROWS(256, 8);
+  if (vec <= 4096) MOE_QROWS(1024, 4);
+  MOE_QROWS(1024, 8);
+#undef MOE_QROWS
+}
+
+hipError_t launch_quantize_weights(const void* w, void* q, float* scale, int e_loc, int K, int N, bool bf16,
+                                   hipStream_t stream) {
+  const unsigned blocks = static_cast<unsigned>(e_loc) * static_cast<unsigned>((N + 63) / 64);
+  if (bf16)
+    hipLaunchKernelGGL(quantize_weights_kernel<true>, dim3(blocks), dim3(256), 0, stream, w, static_cast<uint8_t*>(q),
+                       scale, K, N);
+  else
+    hipLaunchKernelGGL(quantize_weights_kernel<false>, dim3(blocks), dim3(256), 0, stream, w, static_cast<uint8_t*>(q),
+                       scale, K, N);
+  return hipGetLastError();
+}
+
+}  // namespace moe

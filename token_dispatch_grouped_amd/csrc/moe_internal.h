@@ -130,4 +130,35 @@ hipError_t launch_combine_backward(const void* d_out, const void* y, const int32
 hipError_t launch_route_topk_backward(const int32_t* idx, const float* w, const float* d_w, float* d_logits,
                                       int64_t T, int E, int k, hipStream_t stream);
 
+// Residual add and layer norm (r, b may be null; s is written only with r), and its gradient (ds, db may be null;
+// ws: layer_norm_backward_workspace_bytes)
+int64_t layer_norm_max_d();
+hipError_t launch_layer_norm(const void* x, const void* r, const void* w, const void* b, float eps, void* y, void* s,
+                             float* mean, float* rstd, int64_t T, int d, bool bf16, bool wbf16, hipStream_t stream);
+size_t layer_norm_backward_workspace_bytes(int64_t T, int d);
+hipError_t launch_layer_norm_backward(const void* dy, const void* s, const void* w, const float* mean,
+                                      const float* rstd, const void* ds, void* dx, void* dw, void* db, void* ws,
+                                      int64_t T, int d, bool bf16, bool wbf16, hipStream_t stream);
+
+// Quantised matrices are stored in K-blocks of 64: [int8_kblocks(K)][rows][64] bytes
+int int8_kblocks(int K);
+int64_t int8_max_k();  // int32 sums of 127 * 127 * K, and rows held in registers
+// the local rows (through perm, or in order with perm == nullptr) as codes and scales
+hipError_t launch_quantize_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale,
+                                int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max, hipStream_t stream);
+// [e_loc, K, N] weights as codes [e_loc][int8_kblocks(K)][N][64] and scales [e_loc, N]
+hipError_t launch_quantize_weights(const void* w, void* q, float* scale, int e_loc, int K, int N, bool bf16,
+                                   hipStream_t stream);
+// C[rows, N] (bf16) = A @ W_e per local expert, with swiglu silu(gate) * up of W_e's 2 N channels
+hipError_t launch_grouped_gemm_int8(const void* a, const float* a_scale, const void* w, const float* w_scale, void* c,
+                                    const int32_t* offsets, int e_begin, int e_loc, int K, int N, int64_t n_max,
+                                    bool swiglu, hipStream_t stream);
+
+size_t grad_norm_workspace_bytes(int n);
+hipError_t launch_grad_norm(const moe_tensor* t, int n, float* norm, void* ws, hipStream_t stream);
+hipError_t launch_clip_grads(const moe_tensor* t, const moe_tensor* out, int n, const float* norm, float max_norm,
+                             hipStream_t stream);
+hipError_t launch_clip_grad_norm(const moe_tensor* t, const moe_tensor* out, int n, float max_norm, float* norm,
+                                 void* ws, hipStream_t stream);
+
 }  // namespace moe
