@@ -18,6 +18,7 @@ for finding bad input, not for graph capture or timing.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -151,9 +152,16 @@ def _check(status: int, where: str) -> None:
 
 # ----------------------------------------------------------------------------- torch helpers
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported by the first call that needs it."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t):
@@ -207,48 +215,62 @@ def _want(t, name: str, dtype=None, shape=None, min_rows=None):
             raise ValueError(f"{name} must have shape {list(shape)}, got {list(got)}")
 
 
-class _On:
-    """Where a call runs: the tensors' GPU, on `stream` or that GPU's current
-    stream. As a context it makes both current, so that memory allocated inside
-    belongs to that stream; tensors that come from another stream are recorded on
-    it, so that freeing them early does not hand their memory out while the call
-    still runs. `_dev` has checked the tensors first."""
-
-    def __init__(self, stream, *ts):
-        torch = _torch()
-        ts = [t for t in ts if t is not None]
-        dev = ts[0].device
-        for t in ts:
-            if t.device != dev:
-                raise ValueError(f"every tensor must be on one GPU, got {dev} and {t.device}")
-        current = torch.cuda.current_stream(dev)
-        self.stream = current if stream is None else stream
-        if self.stream.device != dev:
-            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {dev}")
-        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
-        self.ctx = None
-        if self.stream != current:
-            for t in ts:
-                t.record_stream(self.stream)
-        if self.stream != current or dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.stream(self.stream)
-
+class _SameStream:
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
+        return self
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
         return False
 
 
-def _aligned(**named):
-    """The calls around the experts move 16-byte vectors from every tensor's first element."""
-    for name, t in named.items():
-        if t is not None and t.data_ptr() % 16:
-            raise ValueError(f"{name} must start at a 16-byte boundary")
+_SAME = _SameStream()
+
+
+def _place(stream, ts):
+    """Where a call on the GPU tensors `ts` runs: (stream handle, context), on
+    `stream` or their GPU's current stream. The context makes both the GPU and the
+    stream current, so that memory allocated inside belongs to that stream. Tensors
+    that come from another stream are recorded on it, so that freeing them early
+    does not hand their memory out while the call still runs."""
+    torch = _torch()
+    index = ts[0].get_device()
+    for t in ts:
+        if t.get_device() != index:
+            raise ValueError(f"every tensor must be on one GPU, got {ts[0].device} and {t.device}")
+    if stream is None and index == torch.cuda.current_device():
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
+        return (raw(index) if raw else torch.cuda.current_stream(index).cuda_stream), _SAME
+    dev = ts[0].device
+    current = torch.cuda.current_stream(dev)
+    if stream is None:
+        stream = current
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    if stream != current:
+        for t in ts:
+            t.record_stream(stream)
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _ready(stream, vectors, others=()):
+    """_place after checking that every tensor (None: not given) is dense and on the
+    GPU, and that `vectors`, which move in 16-byte pieces, start at such a boundary."""
+    ts = [t for t in vectors if t is not None]
+    for t in ts:
+        if not t.is_cuda or not t.is_contiguous():
+            _dev(t)
+        if t.data_ptr() & 15:
+            raise ValueError(f"a tensor of shape {list(t.shape)} does not start at a 16-byte boundary")
+    for t in others:
+        if t is not None:
+            if not t.is_cuda or not t.is_contiguous():
+                _dev(t)
+            ts.append(t)
+    return _place(stream, ts)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _act_dtypes():
@@ -784,10 +806,9 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t is not None:
             _want(t, name, torch.float32, (T,))
-    _dev(x, weight, bias, residual, y, s, mean, rstd)
-    _aligned(x=x, weight=weight, bias=bias, residual=residual, y=y, s=s)
-    sh = shape(T, d, 8, 1, 1, 0, 1)
-    with _On(stream, x, weight, bias, residual, y, s, mean, rstd) as h:
+    h, ctx = _ready(stream, (x, weight, bias, residual, y, s), (mean, rstd))
+    sh = moe_shape(T, d, 8, 1, 1, 0, 1)
+    with ctx:
         if y is None:
             y = torch.empty_like(x)
         if residual is not None and s is None:
@@ -796,9 +817,9 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s
             mean = torch.empty(T, dtype=torch.float32, device=x.device)
         if rstd is None:
             rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-        _check(_load().moe_layer_norm(ctypes.byref(sh), _dtype_code(x), _ptr(x), _ptr(residual), _dtype_code(weight),
-                                      _ptr(weight), _ptr(bias), eps, _ptr(y), _ptr(s), _ptr(mean), _ptr(rstd), h),
-               "moe_layer_norm")
+        _check(_load().moe_layer_norm(ctypes.byref(sh), _dtype_code(x), x.data_ptr(), _addr(residual),
+                                      _dtype_code(weight), weight.data_ptr(), _addr(bias), eps, y.data_ptr(), _addr(s),
+                                      mean.data_ptr(), rstd.data_ptr(), h), "moe_layer_norm")
     return y, x if residual is None else s, mean, rstd
 
 
@@ -826,15 +847,14 @@ def layer_norm_backward(d_y, s, weight, mean, rstd, d_s=None, bias: bool = True,
             _want(t, name, weight.dtype, (d,))
     if d_bias is not None and not bias:
         raise ValueError("d_bias is written only with bias")
-    ws_bytes = layer_norm_backward_workspace_bytes(T, d)
+    sh = moe_shape(T, d, 8, 1, 1, 0, 1)
+    ws_bytes = _load().moe_layer_norm_backward_workspace_bytes(ctypes.byref(sh))
     if workspace is not None:
         _want(workspace, "workspace", torch.uint8)
         if workspace.numel() < ws_bytes:
             raise ValueError(f"workspace must hold at least {ws_bytes} bytes, got {workspace.numel()}")
-    _dev(d_y, s, weight, mean, rstd, d_s, d_x, d_weight, d_bias, workspace)
-    _aligned(d_y=d_y, s=s, weight=weight, d_s=d_s, d_x=d_x, d_weight=d_weight, d_bias=d_bias, workspace=workspace)
-    sh = shape(T, d, 8, 1, 1, 0, 1)
-    with _On(stream, d_y, s, weight, mean, rstd, d_s, d_x, d_weight, d_bias, workspace) as h:
+    h, ctx = _ready(stream, (d_y, s, weight, d_s, d_x, d_weight, d_bias, workspace), (mean, rstd))
+    with ctx:
         if d_x is None:
             d_x = torch.empty_like(d_y)
         if d_weight is None:
@@ -843,10 +863,10 @@ def layer_norm_backward(d_y, s, weight, mean, rstd, d_s=None, bias: bool = True,
             d_bias = torch.empty_like(weight)
         if workspace is None and ws_bytes:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=d_y.device)
-        _check(_load().moe_layer_norm_backward(ctypes.byref(sh), _dtype_code(d_y), _ptr(d_y), _ptr(s),
-                                               _dtype_code(weight), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(d_s),
-                                               _ptr(d_x), _ptr(d_weight), _ptr(d_bias), _ptr(workspace), h),
-               "moe_layer_norm_backward")
+        _check(_load().moe_layer_norm_backward(ctypes.byref(sh), _dtype_code(d_y), d_y.data_ptr(), s.data_ptr(),
+                                               _dtype_code(weight), weight.data_ptr(), mean.data_ptr(),
+                                               rstd.data_ptr(), _addr(d_s), d_x.data_ptr(), d_weight.data_ptr(),
+                                               _addr(d_bias), _addr(workspace), h), "moe_layer_norm_backward")
     return d_x, d_weight, d_bias
 
 
@@ -894,13 +914,10 @@ def quantize_experts(w_gate_up, w_down, out: Int8Experts | None = None, stream=N
     if out is not None:
         _want_int8_experts(out, d, e_loc)
     mine = () if out is None else (out.w_gate_up, out.gate_up_scale, out.w_down, out.down_scale)
-    _dev(w_gate_up, w_down, *mine)
-    _aligned(w_gate_up=w_gate_up, w_down=w_down)
-    if out is not None:
-        _aligned(out_gate_up=out.w_gate_up, out_down=out.w_down)
+    h, ctx = _ready(stream, (w_gate_up, w_down, *mine[::2]), mine[1::2])
     s = shape(0, d, d_ff, max(e_loc, 1), 1, 0, e_loc)
     dev = w_down.device
-    with _On(stream, w_gate_up, w_down, *mine) as h:
+    with ctx:
         if out is None:
             out = Int8Experts(torch.empty((e_loc, _kblocks(d), 2 * d_ff, 64), dtype=torch.int8, device=dev),
                               torch.empty((e_loc, 2 * d_ff), dtype=torch.float32, device=dev),
@@ -931,22 +948,22 @@ def grouped_gemm_int8(x, perm, offsets, experts: Int8Experts, k: int, E: int, e_
     d_ff = _want_int8_experts(experts, d, e_end - e_begin)
     if y is not None:
         _want(y, "y", x.dtype, (n_max, d), min_rows=n_max)
-    s = shape(T, d, d_ff, E, k, e_begin, e_end)
-    ws_bytes = int(_load().moe_grouped_gemm_int8_workspace_bytes(ctypes.byref(s)))
+    s = moe_shape(T, d, d_ff, E, k, e_begin, e_end)
+    ws_bytes = _load().moe_grouped_gemm_int8_workspace_bytes(ctypes.byref(s))
     if workspace is not None:
         _want(workspace, "workspace", torch.uint8)
         if workspace.numel() < ws_bytes:
             raise ValueError(f"workspace must hold at least {ws_bytes} bytes, got {workspace.numel()}")
     wgu, sgu, wdn, sdn = experts.w_gate_up, experts.gate_up_scale, experts.w_down, experts.down_scale
-    _dev(x, perm, offsets, wgu, sgu, wdn, sdn, y, workspace)
-    _aligned(x=x, w_gate_up=wgu, w_down=wdn, y=y, workspace=workspace)
-    with _On(stream, x, perm, offsets, wgu, sgu, wdn, sdn, y, workspace) as h:
+    h, ctx = _ready(stream, (x, wgu, wdn, y, workspace), (perm, offsets, sgu, sdn))
+    with ctx:
         if y is None:
             y = torch.empty((n_max, d), dtype=x.dtype, device=x.device)
         if workspace is None and ws_bytes:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
-        _check(_load().moe_grouped_gemm_int8(ctypes.byref(s), _dtype_code(x), _ptr(x), _ptr(perm), _ptr(offsets),
-                                             _ptr(wgu), _ptr(sgu), _ptr(wdn), _ptr(sdn), _ptr(y), _ptr(workspace), h),
+        _check(_load().moe_grouped_gemm_int8(ctypes.byref(s), MOE_BF16, x.data_ptr(), perm.data_ptr(),
+                                             offsets.data_ptr(), wgu.data_ptr(), sgu.data_ptr(), wdn.data_ptr(),
+                                             sdn.data_ptr(), y.data_ptr(), _addr(workspace), h),
                "moe_grouped_gemm_int8")
     return y
 
@@ -972,29 +989,50 @@ def layer_int8(x, logits, experts: Int8Experts, k: int, e_begin: int, e_end: int
 # ----------------------------------------------------------------------------- gradient norm and clipping
 
 def _tensor_list(ts, name: str):
-    """The host array of a list of gradients, after checking them."""
+    """A list of gradients after checking its types, and their lengths and dtype codes."""
     torch = _torch()
     if torch.is_tensor(ts):
         raise TypeError(f"{name} must be a list of tensors")
     ts = list(ts)
     if not ts:
         raise ValueError(f"{name} is empty")
-    arr = (moe_tensor * len(ts))()
-    for i, t in enumerate(ts):
-        _want(t, f"{name}[{i}]", _act_dtypes())
-        arr[i] = moe_tensor(t.data_ptr(), t.numel(), _dtype_code(t))
-    return ts, arr
+    codes = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+    try:
+        kinds = [codes[t.dtype] for t in ts]
+    except KeyError:
+        for i, t in enumerate(ts):
+            _want(t, f"{name}[{i}]", _act_dtypes())
+        raise
+    return ts, [t.numel() for t in ts], kinds
+
+
+def _host_list(ts, numels, kinds):
+    """The host array of moe_tensor (address, length and dtype code, eight bytes each) as a C pointer."""
+    flat = [0] * (3 * len(ts))
+    flat[::3] = [t.data_ptr() for t in ts]
+    flat[1::3] = numels
+    flat[2::3] = kinds
+    return array.array("q", flat)
+
+
+def _list_ready(stream, ts, *others):
+    """_place for a list of gradients (aligned to their elements only) and its buffers."""
+    all_ = ts + [t for t in others if t is not None]
+    for t in all_:
+        if not t.is_cuda or not t.is_contiguous():
+            _dev(t)
+    return _place(stream, all_)
 
 
 def grad_norm_workspace_bytes(n: int) -> int:
     return int(_load().moe_grad_norm_workspace_bytes(n))
 
 
-def _norm_buffers(ts, norm, workspace):
+def _norm_buffers(n: int, norm, workspace) -> int:
     torch = _torch()
     if norm is not None:
         _want(norm, "norm", torch.float32, (1,))
-    need = grad_norm_workspace_bytes(len(ts))
+    need = grad_norm_workspace_bytes(n)
     if workspace is not None:
         _want(workspace, "workspace", torch.uint8)
         if workspace.numel() < need or workspace.data_ptr() % 8:
@@ -1004,28 +1042,31 @@ def _norm_buffers(ts, norm, workspace):
 
 def _clip_out(ts, out):
     if out is None:
-        return [], None
-    out, arr = _tensor_list(out, "out")
+        return []
+    out = list(out)
     if len(out) != len(ts):
         raise ValueError(f"out must hold {len(ts)} tensors, got {len(out)}")
     for i, (o, t) in enumerate(zip(out, ts)):
-        _want(o, f"out[{i}]", t.dtype, tuple(t.shape))
-    return out, arr
+        if o.dtype is not t.dtype or o.shape != t.shape:
+            _want(o, f"out[{i}]", t.dtype, tuple(t.shape))
+    return out
 
 
 def grad_norm(grads, norm=None, workspace=None, stream=None):
     """norm [1] fp32: the 2-norm over a list of gradients (bf16 or fp32, dense, any
     length and alignment), summed in fp64."""
     torch = _torch()
-    ts, arr = _tensor_list(grads, "grads")
-    need = _norm_buffers(ts, norm, workspace)
-    _dev(*ts, norm, workspace)
-    with _On(stream, *ts, norm, workspace) as h:
+    ts, numels, kinds = _tensor_list(grads, "grads")
+    need = _norm_buffers(len(ts), norm, workspace)
+    h, ctx = _list_ready(stream, ts, norm, workspace)
+    src = _host_list(ts, numels, kinds)
+    with ctx:
         if norm is None:
             norm = torch.empty(1, dtype=torch.float32, device=ts[0].device)
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=ts[0].device)
-        _check(_load().moe_grad_norm(arr, len(ts), _ptr(norm), _ptr(workspace), h), "moe_grad_norm")
+        _check(_load().moe_grad_norm(src.buffer_info()[0], len(ts), norm.data_ptr(), workspace.data_ptr(), h),
+               "moe_grad_norm")
     return norm
 
 
@@ -1033,26 +1074,31 @@ def clip_grads(grads, norm, max_norm: float, out=None, stream=None) -> None:
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)) for a norm [1] fp32
     in device memory, in place or into the tensors of `out`."""
     torch = _torch()
-    ts, arr = _tensor_list(grads, "grads")
-    outs, out_arr = _clip_out(ts, out)
+    ts, numels, kinds = _tensor_list(grads, "grads")
+    outs = _clip_out(ts, out)
     _want(norm, "norm", torch.float32, (1,))
-    _dev(*ts, *outs, norm)
-    with _On(stream, *ts, *outs, norm) as h:
-        _check(_load().moe_clip_grads(arr, out_arr, len(ts), _ptr(norm), max_norm, h), "moe_clip_grads")
+    h, ctx = _list_ready(stream, ts + outs, norm)
+    src = _host_list(ts, numels, kinds)
+    dst = _host_list(outs, numels, kinds) if outs else None
+    with ctx:
+        _check(_load().moe_clip_grads(src.buffer_info()[0], dst.buffer_info()[0] if outs else None, len(ts),
+                                      norm.data_ptr(), max_norm, h), "moe_clip_grads")
 
 
 def clip_grad_norm(grads, max_norm: float, out=None, norm=None, workspace=None, stream=None):
     """grad_norm, then clip_grads with it; returns the norm [1] before clipping."""
     torch = _torch()
-    ts, arr = _tensor_list(grads, "grads")
-    outs, out_arr = _clip_out(ts, out)
-    need = _norm_buffers(ts, norm, workspace)
-    _dev(*ts, *outs, norm, workspace)
-    with _On(stream, *ts, *outs, norm, workspace) as h:
+    ts, numels, kinds = _tensor_list(grads, "grads")
+    outs = _clip_out(ts, out)
+    need = _norm_buffers(len(ts), norm, workspace)
+    h, ctx = _list_ready(stream, ts + outs, norm, workspace)
+    src = _host_list(ts, numels, kinds)
+    dst = _host_list(outs, numels, kinds) if outs else None
+    with ctx:
         if norm is None:
             norm = torch.empty(1, dtype=torch.float32, device=ts[0].device)
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=ts[0].device)
-        _check(_load().moe_clip_grad_norm(arr, out_arr, len(ts), max_norm, _ptr(norm), _ptr(workspace), h),
-               "moe_clip_grad_norm")
+        _check(_load().moe_clip_grad_norm(src.buffer_info()[0], dst.buffer_info()[0] if outs else None, len(ts),
+                                          max_norm, norm.data_ptr(), workspace.data_ptr(), h), "moe_clip_grad_norm")
     return norm
