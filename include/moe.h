@@ -392,8 +392,9 @@ moe_status moe_quantize_experts(const moe_shape* s, moe_dtype dt, const void* w_
                                 const void* w_down, void* q_gate_up, float* scale_gate_up,
                                 void* q_down, float* scale_down, hipStream_t stream);
 
-/* Bytes of device workspace moe_grouped_gemm_int8 needs (0 when T = 0): codes and
- * scales of N_max rows of x and of h, and h. */
+/* Bytes of device workspace moe_grouped_gemm_int8 needs (0 when T = 0): the codes of
+ * N_max rows of x, their scales, h, the codes of h and their scales, then the list of
+ * row tiles, each part at a multiple of 256 bytes. */
 size_t moe_grouped_gemm_int8_workspace_bytes(const moe_shape* s);
 
 /* moe_grouped_gemm_gather in 8-bit integers: for each local expert e with rows R,

@@ -86,10 +86,11 @@ def test_int8_refusals():
     for kw in (dict(dt=F), dict(d=65544), dict(d_ff=65544), dict(E=1025, e_end=1025)):
         assert _int8(**kw) == EUNSUP, kw
     assert _int8(T=0, **{n: NULL for n in names}) == moe.MOE_OK
-    # codes of x, its scales, h, its codes and its scales, each rounded up to 256 bytes
+    # codes of x, its scales, h, its codes and its scales, each rounded up to 256 bytes, and the list of
+    # row tiles: a 256-byte header and 16 bytes a tile
     n = 16 * 2
     assert moe.grouped_gemm_int8_workspace_bytes(16, 72, 136, 8, 2, 0, 8) == \
-        n * 128 + 256 + n * 136 * 2 + n * 192 + 256
+        n * 128 + 256 + n * 136 * 2 + n * 192 + 256 + 512
     assert moe.grouped_gemm_int8_workspace_bytes(0, 72, 136, 8, 2, 0, 8) == 0
 
 

@@ -13,6 +13,7 @@
 // of R rows holds [R][64] bytes, columns 64 kb .. 64 kb + 63 of every row, zero
 // past the last column. A K = 64 stage of a tile is then one contiguous run.
 // Everything here is bound by HBM: a row is read once and its codes written once.
+#include "int8_plan.h"
 #include "row_group.h"
 
 namespace moe {
@@ -53,19 +54,30 @@ constexpr int block_threads() { return G > 256 ? G : 256; }
 
 // Rows [0, N_loc) of the local segment: row r is row perm[seg0 + r] / k of src
 // (perm != nullptr: the dispatch's row gather) or row r. G threads per row, VPT
-// vectors of 8 bf16 per thread; the row's K-blocks are filled up with zeros.
+// vectors of 8 bf16 per thread; the row's K-blocks are filled up with zeros. With
+// `plan`, one more workgroup (the first) lists the tiles of the call's GEMM launches.
 template <int G, int VPT>
 __global__ __launch_bounds__(block_threads<G>()) void quantize_rows_kernel(
     const uint4* __restrict__ src, const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets,
     uint8_t* __restrict__ q, float* __restrict__ scale, int e_begin, int e_end, int k, int64_t T, int cols_vec,
-    int kblocks, int64_t n_max) {
+    int kblocks, int64_t n_max, void* __restrict__ plan, int tall) {
   constexpr int kRows = block_threads<G>() / G;
   __shared__ uint32_t lds[G > kWave ? G / kWave : 1];
+  const int planners = plan != nullptr ? 1 : 0;
+  if (static_cast<int>(blockIdx.x) < planners) {
+    int* count = static_cast<int*>(plan);
+    int8::RowGroup* groups = reinterpret_cast<int8::RowGroup*>(static_cast<char*>(plan) + int8::kPlanHeader);
+    const int e_loc = e_end - e_begin, n = static_cast<int>(n_max);
+    if (tall) int8::plan_tiles<int8::kTallRows, int8::kTallMerge>(offsets, e_begin, e_loc, n, count, groups);
+    else int8::plan_tiles<int8::kShortRows, 0>(offsets, e_begin, e_loc, n, count, groups);
+    return;
+  }
+  const int64_t block = static_cast<int64_t>(blockIdx.x) - planners;
+  const int64_t blocks = static_cast<int64_t>(gridDim.x) - planners;
   const int seg0 = offsets[e_begin];
   const int64_t n_loc = min(static_cast<int64_t>(offsets[e_end] - seg0), n_max);
   const int li = static_cast<int>(threadIdx.x) % G;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < n_loc;
-       r0 += static_cast<int64_t>(gridDim.x) * kRows) {
+  for (int64_t r0 = block * kRows; r0 < n_loc; r0 += blocks * kRows) {
     const int64_t r = r0 + threadIdx.x / G;
     const bool live = r < n_loc;
     const int64_t from = !live ? 0 : perm != nullptr ? perm[seg0 + r] / k : r;
@@ -157,12 +169,13 @@ __global__ __launch_bounds__(256) void quantize_weights_kernel(const void* __res
 
 template <int G, int VPT>
 hipError_t launch_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale, int e_begin,
-                       int e_end, int k, int64_t T, int cols, int64_t n_max, hipStream_t stream) {
+                       int e_end, int k, int64_t T, int cols, int64_t n_max, void* plan, hipStream_t stream) {
   constexpr int kRows = block_threads<G>() / G;
   const int64_t blocks = (n_max + kRows - 1) / kRows;
-  hipLaunchKernelGGL((quantize_rows_kernel<G, VPT>), dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)),
+  hipLaunchKernelGGL((quantize_rows_kernel<G, VPT>), dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536) + (plan != nullptr ? 1u : 0u)),
                      dim3(block_threads<G>()), 0, stream, static_cast<const uint4*>(src), perm, offsets,
-                     static_cast<uint8_t*>(q), scale, e_begin, e_end, k, T, cols / 8, (cols + 63) / 64, n_max);
+                     static_cast<uint8_t*>(q), scale, e_begin, e_end, k, T, cols / 8, (cols + 63) / 64, n_max, plan,
+                     int8_tall(n_max, e_end - e_begin) ? 1 : 0);
   return hipGetLastError();
 }
 
@@ -172,12 +185,19 @@ int int8_kblocks(int K) { return (K + 63) / 64; }
 
 int64_t int8_max_k() { return 65536; }
 
+// Average rows per local expert from which the tall workgroups pay (2880 x 2880, per
+// call of both products: 16 experts of 128 rows short 97 us, tall 108; of 256 rows
+// short 137, tall 137; 8 experts of 1024 rows at 4096 x 14336 short 1424, tall 1280).
+bool int8_tall(int64_t n_max, int e_loc) { return n_max >= int64_t{192} * e_loc; }
+
+size_t int8_plan_bytes(int64_t n_max, int e_loc) { return int8::plan_bytes(n_max, e_loc, int8_tall(n_max, e_loc)); }
+
 hipError_t launch_quantize_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale,
-                                int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max,
+                                int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max, void* plan,
                                 hipStream_t stream) {
   const int vec = int8_kblocks(cols) * 8;  // the padded row, in vectors of 8 elements
 #define MOE_QROWS(G, VPT) \
-  return launch_rows<G, VPT>(src, perm, offsets, q, scale, e_begin, e_end, k, T, cols, n_max, stream)
+  return launch_rows<G, VPT>(src, perm, offsets, q, scale, e_begin, e_end, k, T, cols, n_max, plan, stream)
   if (vec <= 64) MOE_QROWS(64, 1);
   if (vec <= 256) MOE_QROWS(64, 4);
   if (vec <= 512) MOE_QROWS(64, 8);

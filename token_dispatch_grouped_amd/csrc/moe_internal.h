@@ -143,16 +143,20 @@ hipError_t launch_layer_norm_backward(const void* dy, const void* s, const void*
 // Quantised matrices are stored in K-blocks of 64: [int8_kblocks(K)][rows][64] bytes
 int int8_kblocks(int K);
 int64_t int8_max_k();  // int32 sums of 127 * 127 * K, and rows held in registers
-// the local rows (through perm, or in order with perm == nullptr) as codes and scales
+// the local rows (through perm, or in order with perm == nullptr) as codes and scales; with plan (of
+// int8_plan_bytes), the list of row tiles that launch_grouped_gemm_int8 walks is written there too
+bool int8_tall(int64_t n_max, int e_loc);
+size_t int8_plan_bytes(int64_t n_max, int e_loc);
 hipError_t launch_quantize_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale,
-                                int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max, hipStream_t stream);
+                                int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max, void* plan,
+                                hipStream_t stream);
 // [e_loc, K, N] weights as codes [e_loc][int8_kblocks(K)][N][64] and scales [e_loc, N]
 hipError_t launch_quantize_weights(const void* w, void* q, float* scale, int e_loc, int K, int N, bool bf16,
                                    hipStream_t stream);
 // C[rows, N] (bf16) = A @ W_e per local expert, with swiglu silu(gate) * up of W_e's 2 N channels
 hipError_t launch_grouped_gemm_int8(const void* a, const float* a_scale, const void* w, const float* w_scale, void* c,
-                                    const int32_t* offsets, int e_begin, int e_loc, int K, int N, int64_t n_max,
-                                    bool swiglu, hipStream_t stream);
+                                    const void* plan, int e_loc, int K, int N, int64_t n_max, bool swiglu,
+                                    hipStream_t stream);
 
 size_t grad_norm_workspace_bytes(int n);
 hipError_t launch_grad_norm(const moe_tensor* t, int n, float* norm, void* ws, hipStream_t stream);
