@@ -20,6 +20,9 @@
 namespace moe {
 namespace {
 
+using rows::kStreamBytes;
+using rows::load16;
+using rows::store16;
 using rows::Vec16;
 
 constexpr int kThreads = 256;
@@ -74,7 +77,7 @@ __device__ __forceinline__ float load_one(const void* p, int64_t i) {
   return static_cast<const float*>(p)[i];
 }
 
-template <bool BF16>
+template <bool BF16, bool STREAM>
 __device__ __forceinline__ double piece_sumsq(const Entry& e, int64_t p) {
   using V = Vec16<BF16>;
   const PieceSpan<V::kN> span(e, p);
@@ -85,7 +88,7 @@ __device__ __forceinline__ double piece_sumsq(const Entry& e, int64_t p) {
   for (int q = 0; q < kUnroll; ++q) {
     const int c = q * kThreads + static_cast<int>(threadIdx.x);
     const int64_t a = span.first + static_cast<int64_t>(c) * V::kN;
-    v[q] = span.whole(c) ? *reinterpret_cast<const uint4*>(src + a * (16 / V::kN)) : make_uint4(0, 0, 0, 0);
+    v[q] = span.whole(c) ? load16<STREAM>(reinterpret_cast<const uint4*>(src + a * (16 / V::kN))) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int q = 0; q < kUnroll; ++q) {
@@ -112,10 +115,13 @@ __device__ __forceinline__ double piece_sumsq(const Entry& e, int64_t p) {
 
 __device__ __forceinline__ double block_sum(double v, double* lds) { return rows::group_reduce<kThreads, rows::Sum>(v, lds); }
 
+template <bool STREAM>
 __global__ __launch_bounds__(kThreads) void sumsq_kernel(const List l, double* __restrict__ partial) {
   __shared__ double lds[kThreads / kWave];
   double acc = 0.0;
-  for_pieces(l, [&](int i, int64_t p) { acc += l.bf16[i] ? piece_sumsq<true>(l.t[i], p) : piece_sumsq<false>(l.t[i], p); });
+  for_pieces(l, [&](int i, int64_t p) {
+    acc += l.bf16[i] ? piece_sumsq<true, STREAM>(l.t[i], p) : piece_sumsq<false, STREAM>(l.t[i], p);
+  });
   acc = block_sum(acc, lds);
   if (threadIdx.x == 0) partial[blockIdx.x] = acc;
 }
@@ -135,7 +141,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const double* __restrict
   if (threadIdx.x == 0) *norm = v;
 }
 
-template <bool BF16>
+template <bool BF16, bool STREAM>
 __device__ __forceinline__ void piece_scale(const Entry& e, int64_t p, float coef) {
   using V = Vec16<BF16>;
   const PieceSpan<V::kN> span(e, p);
@@ -148,7 +154,7 @@ __device__ __forceinline__ void piece_scale(const Entry& e, int64_t p, float coe
   for (int q = 0; q < kUnroll; ++q) {
     const int c = q * kThreads + static_cast<int>(threadIdx.x);
     const int64_t a = span.first + static_cast<int64_t>(c) * V::kN;
-    v[q] = span.whole(c) ? *reinterpret_cast<const uint4*>(src + a * (16 / V::kN)) : make_uint4(0, 0, 0, 0);
+    v[q] = span.whole(c) ? load16<STREAM>(reinterpret_cast<const uint4*>(src + a * (16 / V::kN))) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int q = 0; q < kUnroll; ++q) {
@@ -161,7 +167,7 @@ __device__ __forceinline__ void piece_scale(const Entry& e, int64_t p, float coe
       for (int i = 0; i < V::kN; ++i) f[i] *= coef;
       const uint4 o = V::pack(f);
       if (same) {
-        *reinterpret_cast<uint4*>(dst + a * (16 / V::kN)) = o;
+        store16<STREAM>(reinterpret_cast<uint4*>(dst + a * (16 / V::kN)), o);
       } else {
         const uint32_t w[4] = {o.x, o.y, o.z, o.w};
         for (int i = 0; i < V::kN; ++i) {
@@ -182,6 +188,7 @@ __device__ __forceinline__ void piece_scale(const Entry& e, int64_t p, float coe
 
 // partial != nullptr: the norm is taken from n partial sums (and written by the
 // first workgroup of the first launch); else it is read from *norm.
+template <bool STREAM>
 __global__ __launch_bounds__(kThreads) void clip_kernel(const List l, const double* __restrict__ partial, int n,
                                                         float* norm, int write_norm, float max_norm) {
   __shared__ double lds[kThreads / kWave];
@@ -192,8 +199,8 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(const List l, const doub
   const float coef = c >= 1.f ? 1.f : c;
   for_pieces(l, [&](int i, int64_t p) {
     if (coef == 1.f && l.t[i].src == l.t[i].dst) return;  // times one, in place
-    if (l.bf16[i]) piece_scale<true>(l.t[i], p, coef);
-    else piece_scale<false>(l.t[i], p, coef);
+    if (l.bf16[i]) piece_scale<true, STREAM>(l.t[i], p, coef);
+    else piece_scale<false, STREAM>(l.t[i], p, coef);
   });
 }
 
@@ -222,13 +229,23 @@ unsigned list_blocks(const List& l) {
   return static_cast<unsigned>(p < 1 ? 1 : p < kNormBlocks ? p : kNormBlocks);
 }
 
-hipError_t sum_squares(const moe_tensor* t, int n, double* partial, int* count, hipStream_t stream) {
+// Whether a list is streamed past the caches. The reading pass then runs at 6.9 TB/s instead of
+// 6.1 (2.8 GB of bf16: 412 us against 463) and the clip takes 1445 us instead of 1555; a list
+// that fits finds its gradients in the caches in the second pass (32 MB: 18 us against 22).
+bool stream_list(const moe_tensor* t, int n, int sides) {
+  int64_t bytes = 0;
+  for (int i = 0; i < n; ++i) bytes += t[i].numel * (t[i].dt == MOE_BF16 ? 2 : 4);
+  return bytes * sides > kStreamBytes;
+}
+
+hipError_t sum_squares(const moe_tensor* t, int n, bool big, double* partial, int* count, hipStream_t stream) {
   *count = 0;
   for (int i0 = 0; i0 < n;) {
     List l;
     i0 += fill(&l, t, nullptr, i0, n);
     const unsigned blocks = list_blocks(l);
-    hipLaunchKernelGGL(sumsq_kernel, dim3(blocks), dim3(kThreads), 0, stream, l, partial + *count);
+    if (big) hipLaunchKernelGGL(sumsq_kernel<true>, dim3(blocks), dim3(kThreads), 0, stream, l, partial + *count);
+    else hipLaunchKernelGGL(sumsq_kernel<false>, dim3(blocks), dim3(kThreads), 0, stream, l, partial + *count);
     *count += static_cast<int>(blocks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -236,15 +253,19 @@ hipError_t sum_squares(const moe_tensor* t, int n, double* partial, int* count, 
   return hipSuccess;
 }
 
-hipError_t scale_all(const moe_tensor* t, const moe_tensor* out, int n, const double* partial, int count, float* norm,
+hipError_t scale_all(const moe_tensor* t, const moe_tensor* out, int n, bool big, const double* partial, int count, float* norm,
                      float max_norm, hipStream_t stream) {
   int i0 = 0;
   do {
     List l;
     const int first = i0 == 0;
     i0 += fill(&l, t, out, i0, n);
-    hipLaunchKernelGGL(clip_kernel, dim3(list_blocks(l)), dim3(kThreads), 0, stream, l, partial, count, norm, first,
-                       max_norm);
+    if (big)
+      hipLaunchKernelGGL(clip_kernel<true>, dim3(list_blocks(l)), dim3(kThreads), 0, stream, l, partial, count, norm,
+                         first, max_norm);
+    else
+      hipLaunchKernelGGL(clip_kernel<false>, dim3(list_blocks(l)), dim3(kThreads), 0, stream, l, partial, count, norm,
+                         first, max_norm);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   } while (i0 < n);
@@ -260,7 +281,7 @@ size_t grad_norm_workspace_bytes(int n) {
 
 hipError_t launch_grad_norm(const moe_tensor* t, int n, float* norm, void* ws, hipStream_t stream) {
   int count = 0;
-  hipError_t e = sum_squares(t, n, static_cast<double*>(ws), &count, stream);
+  hipError_t e = sum_squares(t, n, stream_list(t, n, 1), static_cast<double*>(ws), &count, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(kThreads), 0, stream, static_cast<const double*>(ws), count, norm);
   return hipGetLastError();
@@ -268,15 +289,16 @@ hipError_t launch_grad_norm(const moe_tensor* t, int n, float* norm, void* ws, h
 
 hipError_t launch_clip_grads(const moe_tensor* t, const moe_tensor* out, int n, const float* norm, float max_norm,
                              hipStream_t stream) {
-  return scale_all(t, out, n, nullptr, 0, const_cast<float*>(norm), max_norm, stream);
+  return scale_all(t, out, n, stream_list(t, n, out == t ? 1 : 2), nullptr, 0, const_cast<float*>(norm), max_norm, stream);
 }
 
 hipError_t launch_clip_grad_norm(const moe_tensor* t, const moe_tensor* out, int n, float max_norm, float* norm,
                                  void* ws, hipStream_t stream) {
   int count = 0;
-  const hipError_t e = sum_squares(t, n, static_cast<double*>(ws), &count, stream);
+  const bool big = stream_list(t, n, out == t ? 1 : 2);
+  const hipError_t e = sum_squares(t, n, big, static_cast<double*>(ws), &count, stream);
   if (e != hipSuccess) return e;
-  return scale_all(t, out, n, static_cast<const double*>(ws), count, norm, max_norm, stream);
+  return scale_all(t, out, n, big, static_cast<const double*>(ws), count, norm, max_norm, stream);
 }
 
 }  // namespace moe

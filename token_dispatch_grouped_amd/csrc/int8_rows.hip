@@ -62,7 +62,8 @@ __global__ __launch_bounds__(block_threads<G>()) void quantize_rows_kernel(
     uint8_t* __restrict__ q, float* __restrict__ scale, int e_begin, int e_end, int k, int64_t T, int cols_vec,
     int kblocks, int64_t n_max, void* __restrict__ plan, int tall) {
   constexpr int kRows = block_threads<G>() / G;
-  __shared__ uint32_t lds[G > kWave ? G / kWave : 1];
+  __shared__ uint32_t lds[2][G > kWave ? G / kWave : 1];
+  int turn = 0;
   const int planners = plan != nullptr ? 1 : 0;
   if (static_cast<int>(blockIdx.x) < planners) {
     int* count = static_cast<int*>(plan);
@@ -96,7 +97,8 @@ __global__ __launch_bounds__(block_threads<G>()) void quantize_rows_kernel(
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = Max::apply(top, abs_bits(f[j]));
     }
-    top = group_reduce<G, Max>(top, lds);
+    top = group_reduce<G, Max>(top, lds[turn]);
+    turn ^= 1;
     float sc, inv;
     scale_of(top, &sc, &inv);
     if (live && li == 0) scale[r] = sc;

@@ -23,20 +23,18 @@ namespace {
 
 using namespace rows;
 
-constexpr int kMaxRowThreads = 1024;
-
 template <int G>
 constexpr int block_threads() { return G > 256 ? G : 256; }
 
-// G threads per row, VPT vectors per thread.
-template <bool BF16, bool WBF16, int G, int VPT>
+// G threads per row, VPT vectors per thread. STREAM: the rows do not fit the caches.
+template <bool BF16, bool WBF16, int G, int VPT, bool STREAM>
 __global__ __launch_bounds__(block_threads<G>()) void layer_norm_kernel(
     const uint4* x, const uint4* r, const void* __restrict__ w, const void* __restrict__ b, float eps, uint4* y,
     uint4* s, float* __restrict__ mean, float* __restrict__ rstd, int64_t T, int row_vec) {
   using V = Vec16<BF16>;
-  const float d = static_cast<float>(row_vec * V::kN);
   constexpr int kRows = block_threads<G>() / G;  // rows per workgroup
-  __shared__ float lds[G > kWave ? G / kWave : 1];
+  __shared__ float lds[2][G > kWave ? G / kWave : 1];
+  const float d = static_cast<float>(row_vec * V::kN);
   const int li = static_cast<int>(threadIdx.x) % G;
   // the bound is the same for every group of a workgroup, so barriers inside are uniform
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < T; t0 += static_cast<int64_t>(gridDim.x) * kRows) {
@@ -47,14 +45,14 @@ __global__ __launch_bounds__(block_threads<G>()) void layer_norm_kernel(
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
       const int c = q * G + li;
-      v[q] = c < n ? x[base + c] : make_uint4(0, 0, 0, 0);
+      v[q] = c < n ? load16<STREAM>(x + base + c) : make_uint4(0, 0, 0, 0);
     }
     if (r != nullptr) {
       uint4 u[VPT];
 #pragma unroll
       for (int q = 0; q < VPT; ++q) {
         const int c = q * G + li;
-        u[q] = c < n ? r[base + c] : make_uint4(0, 0, 0, 0);
+        u[q] = c < n ? load16<STREAM>(r + base + c) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int q = 0; q < VPT; ++q) {
@@ -65,7 +63,7 @@ __global__ __launch_bounds__(block_threads<G>()) void layer_norm_kernel(
 #pragma unroll
         for (int i = 0; i < V::kN; ++i) f[i] += g[i];
         v[q] = V::pack(f);
-        if (c < n) s[base + c] = v[q];
+        if (c < n) store16<STREAM>(s + base + c, v[q]);
       }
     }
     float sum = 0.f;
@@ -76,7 +74,7 @@ __global__ __launch_bounds__(block_threads<G>()) void layer_norm_kernel(
 #pragma unroll
       for (int i = 0; i < V::kN; ++i) sum += f[i];
     }
-    const float m = group_reduce<G, Sum>(sum, lds) / d;  // a quotient: a constant row's mean is that constant
+    const float m = group_reduce<G, Sum>(sum, lds[0]) / d;  // a quotient: a constant row's mean is that constant
     float var = 0.f;
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
@@ -86,7 +84,7 @@ __global__ __launch_bounds__(block_threads<G>()) void layer_norm_kernel(
       for (int i = 0; i < V::kN; ++i) p = fmaf(f[i] - m, f[i] - m, p);
       var += q * G + li < n ? p : 0.f;
     }
-    const float rs = 1.f / sqrtf(group_reduce<G, Sum>(var, lds) / d + eps);
+    const float rs = 1.f / sqrtf(group_reduce<G, Sum>(var, lds[1]) / d + eps);
     if (n != 0 && li == 0) {
       mean[t] = m;
       rstd[t] = rs;
@@ -104,7 +102,7 @@ __global__ __launch_bounds__(block_threads<G>()) void layer_norm_kernel(
           const float h = (f[i] - m) * rs;
           f[i] = b != nullptr ? fmaf(h, wf[i], bf[i]) : h * wf[i];
         }
-        y[base + c] = V::pack(f);
+        store16<STREAM>(y + base + c, V::pack(f));
       }
     }
   }
@@ -113,71 +111,114 @@ __global__ __launch_bounds__(block_threads<G>()) void layer_norm_kernel(
 // The gradient. Workgroups walk rows with a fixed stride and keep their columns'
 // sums of dy * h and dy in registers; each leaves one fp32 row of both in
 // `partial` [gridDim.x][2][d], added in a fixed order by the kernel below (no
-// atomics: the same bits every time).
-template <bool BF16, bool WBF16, int G, int VPT>
+// atomics: the same bits every time). There are only two workgroups per CU (more
+// would leave more partial rows), so each asks for its next row before it reduces
+// the present one.
+template <bool BF16, int VPT>
+struct GradRow {
+  uint4 s[VPT], dy[VPT], ds[VPT];
+  float mean, rstd;
+};
+
+template <bool BF16, bool WBF16, int G, int VPT, bool STREAM>
 __global__ __launch_bounds__(block_threads<G>()) void layer_norm_backward_kernel(
     const uint4* dy, const uint4* __restrict__ s, const void* __restrict__ w, const float* __restrict__ mean,
     const float* __restrict__ rstd, const uint4* ds, uint4* dx, float* __restrict__ partial, int64_t T, int row_vec,
     float inv_d) {
   using V = Vec16<BF16>;
   constexpr int kRows = block_threads<G>() / G;
-  __shared__ float lds[G > kWave ? G / kWave : 1];
+  // the next row and the weights stay in registers where there is room for them
+  constexpr bool kAhead = G <= 512;
+  __shared__ float lds[2][G > kWave ? 2 * G / kWave : 1];
   __shared__ float cols[kRows > 1 ? 2 * G * VPT * V::kN : 1];  // the groups' column sums, joined
   const int li = static_cast<int>(threadIdx.x) % G;
+  using Row = GradRow<BF16, VPT>;
+  auto fetch = [&](Row& o, int64_t t) {
+    const int n = t < T ? row_vec : 0;
+    const int64_t base = t * row_vec;
+    o.mean = n ? mean[t] : 0.f;
+    o.rstd = n ? rstd[t] : 0.f;
+#pragma unroll
+    for (int q = 0; q < VPT; ++q) {
+      const int c = q * G + li;
+      o.s[q] = c < n ? load16<STREAM>(s + base + c) : make_uint4(0, 0, 0, 0);
+      o.dy[q] = c < n ? load16<STREAM>(dy + base + c) : make_uint4(0, 0, 0, 0);
+      o.ds[q] = ds != nullptr && c < n ? load16<STREAM>(ds + base + c) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  float wr[kAhead ? VPT : 1][V::kN];
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int q = 0; q < VPT; ++q)
+      if (q * G + li < row_vec) load_params<V::kN, WBF16>(w, q * G + li, wr[q]);
+  }
+  auto weights = [&](int q, float* wf) {
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < V::kN; ++i) wf[i] = wr[q][i];
+    } else {
+      load_params<V::kN, WBF16>(w, q * G + li, wf);
+    }
+  };
   float aw[VPT][V::kN], ab[VPT][V::kN];
 #pragma unroll
   for (int q = 0; q < VPT; ++q)
 #pragma unroll
     for (int i = 0; i < V::kN; ++i) aw[q][i] = ab[q][i] = 0.f;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < T; t0 += static_cast<int64_t>(gridDim.x) * kRows) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
+  Row row, next;
+  if (kAhead && first < T) fetch(next, first + threadIdx.x / G);
+  int turn = 0;
+  // the bound is the same for every group of a workgroup, so barriers inside are uniform
+  for (int64_t t0 = first; t0 < T; t0 += stride) {
     const int64_t t = t0 + threadIdx.x / G;
     const int n = t < T ? row_vec : 0;
     const int64_t base = t * row_vec;
-    const float m = n ? mean[t] : 0.f, rs = n ? rstd[t] : 0.f;
-    uint4 vs[VPT], vd[VPT];
-#pragma unroll
-    for (int q = 0; q < VPT; ++q) {
-      const int c = q * G + li;
-      vs[q] = c < n ? s[base + c] : make_uint4(0, 0, 0, 0);
-      vd[q] = c < n ? dy[base + c] : make_uint4(0, 0, 0, 0);
+    if constexpr (kAhead) {
+      row = next;
+      if (t0 + stride < T) fetch(next, t + stride);
+    } else {
+      fetch(row, t);
     }
-    float c1 = 0.f, c2 = 0.f;
+    const float m = row.mean, rs = row.rstd;
+    float c12[2] = {0.f, 0.f};
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
-      const int c = q * G + li;
-      if (c < n) {
+      if (q * G + li < n) {
         float f[V::kN], g[V::kN], wf[V::kN];
-        V::unpack(vs[q], f);
-        V::unpack(vd[q], g);
-        load_params<V::kN, WBF16>(w, c, wf);
+        V::unpack(row.s[q], f);
+        V::unpack(row.dy[q], g);
+        weights(q, wf);
 #pragma unroll
         for (int i = 0; i < V::kN; ++i) {
           const float h = (f[i] - m) * rs, gw = g[i] * wf[i];
-          c1 += gw;
-          c2 = fmaf(gw, h, c2);
+          c12[0] += gw;
+          c12[1] = fmaf(gw, h, c12[1]);
           aw[q][i] = fmaf(g[i], h, aw[q][i]);
           ab[q][i] += g[i];
         }
       }
     }
-    c1 = group_reduce<G, Sum>(c1, lds) * inv_d;
-    c2 = group_reduce<G, Sum>(c2, lds) * inv_d;
+    group_reduce<G, Sum>(c12, lds[turn]);
+    turn ^= 1;
+    const float c1 = c12[0] * inv_d, c2 = c12[1] * inv_d;
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
       const int c = q * G + li;
       if (c < n) {
         float f[V::kN], g[V::kN], wf[V::kN], e[V::kN];
-        V::unpack(vs[q], f);
-        V::unpack(vd[q], g);
-        load_params<V::kN, WBF16>(w, c, wf);
-        if (ds != nullptr) V::unpack(ds[base + c], e);
+        V::unpack(row.s[q], f);
+        V::unpack(row.dy[q], g);
+        V::unpack(row.ds[q], e);
+        weights(q, wf);
 #pragma unroll
         for (int i = 0; i < V::kN; ++i) {
           const float h = (f[i] - m) * rs;
           const float o = rs * (fmaf(g[i], wf[i], -c1) - h * c2);
           f[i] = ds != nullptr ? o + e[i] : o;
         }
-        dx[base + c] = V::pack(f);
+        store16<STREAM>(dx + base + c, V::pack(f));
       }
     }
   }
@@ -256,15 +297,27 @@ unsigned row_blocks(int64_t T, int64_t most) {
 
 constexpr int kBackwardBlocks = 512;  // partial rows at most
 
-// f(G, VPT) for a row of row_vec vectors
-#define MOE_ROW_SHAPES(F)          \
-  if (row_vec <= 16) F(16, 1);     \
-  else if (row_vec <= 32) F(32, 1); \
-  else if (row_vec <= 64) F(64, 1); \
+// F(G, VPT) for a row of row_vec vectors
+#define MOE_NORM_SHAPES(F)           \
+  if (row_vec <= 16) F(16, 1);       \
+  else if (row_vec <= 32) F(32, 1);  \
+  else if (row_vec <= 64) F(64, 1);  \
   else if (row_vec <= 128) F(64, 2); \
   else if (row_vec <= 256) F(256, 1); \
   else if (row_vec <= 512) F(256, 2); \
   else if (row_vec <= 1024) F(256, 4); \
+  else if (row_vec <= 2048) F(1024, 2); \
+  else if (row_vec <= 4096) F(1024, 4); \
+  else F(1024, 8)
+
+#define MOE_NORM_BWD_SHAPES(F)       \
+  if (row_vec <= 16) F(16, 1);       \
+  else if (row_vec <= 32) F(32, 1);  \
+  else if (row_vec <= 64) F(64, 1);  \
+  else if (row_vec <= 128) F(64, 2); \
+  else if (row_vec <= 256) F(256, 1); \
+  else if (row_vec <= 512) F(512, 1); \
+  else if (row_vec <= 1024) F(512, 2); \
   else if (row_vec <= 2048) F(1024, 2); \
   else if (row_vec <= 4096) F(1024, 4); \
   else F(1024, 8)
@@ -277,21 +330,28 @@ hipError_t launch_layer_norm(const void* x, const void* r, const void* w, const 
                              float* mean, float* rstd, int64_t T, int d, bool bf16, bool wbf16, hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const int row_vec = bf16 ? d / 8 : d / 4;
-#define MOE_NORM(B, W, G, VPT)                                                                                   \
-  hipLaunchKernelGGL((layer_norm_kernel<B, W, G, VPT>), dim3(row_blocks<G>(T, int64_t{1} << 30)),                \
+  const bool big = T * d * (bf16 ? 2 : 4) * (r != nullptr ? 4 : 2) > kStreamBytes;
+#define MOE_NORM_S(B, W, G, VPT, S)                                                                              \
+  hipLaunchKernelGGL((layer_norm_kernel<B, W, G, VPT, S>), dim3(row_blocks<G>(T, int64_t{1} << 30)),             \
                      dim3(block_threads<G>()), 0, stream, static_cast<const uint4*>(x),                          \
                      static_cast<const uint4*>(r), w, b, eps, static_cast<uint4*>(y), static_cast<uint4*>(s),    \
                      mean, rstd, T, row_vec)
+#define MOE_NORM(B, W, G, VPT)                 \
+  do {                                         \
+    if (big) MOE_NORM_S(B, W, G, VPT, true);   \
+    else MOE_NORM_S(B, W, G, VPT, false);      \
+  } while (0)
 #define MOE_NORM_BB(G, VPT) MOE_NORM(true, true, G, VPT)
 #define MOE_NORM_BF(G, VPT) MOE_NORM(true, false, G, VPT)
 #define MOE_NORM_FF(G, VPT) MOE_NORM(false, false, G, VPT)
-  if (bf16 && wbf16) { MOE_ROW_SHAPES(MOE_NORM_BB); }
-  else if (bf16) { MOE_ROW_SHAPES(MOE_NORM_BF); }
-  else { MOE_ROW_SHAPES(MOE_NORM_FF); }
+  if (bf16 && wbf16) { MOE_NORM_SHAPES(MOE_NORM_BB); }
+  else if (bf16) { MOE_NORM_SHAPES(MOE_NORM_BF); }
+  else { MOE_NORM_SHAPES(MOE_NORM_FF); }
 #undef MOE_NORM_BB
 #undef MOE_NORM_BF
 #undef MOE_NORM_FF
 #undef MOE_NORM
+#undef MOE_NORM_S
   return hipGetLastError();
 }
 
@@ -308,23 +368,28 @@ hipError_t launch_layer_norm_backward(const void* dy, const void* s, const void*
   float* partial = static_cast<float*>(ws);
   unsigned blocks = 0;
   if (T > 0) {
-#define MOE_NORM_BWD(B, W, G, VPT)                                                                                \
-  do {                                                                                                            \
-    blocks = row_blocks<G>(T, kBackwardBlocks);                                                                   \
-    hipLaunchKernelGGL((layer_norm_backward_kernel<B, W, G, VPT>), dim3(blocks), dim3(block_threads<G>()), 0,     \
-                       stream, static_cast<const uint4*>(dy), static_cast<const uint4*>(s), w, mean, rstd,        \
-                       static_cast<const uint4*>(ds), static_cast<uint4*>(dx), partial, T, row_vec, inv_d);       \
+    const bool big = T * d * (bf16 ? 2 : 4) * (ds != nullptr ? 4 : 3) > kStreamBytes;
+#define MOE_NORM_BWD_S(B, W, G, VPT, S)                                                                           \
+  hipLaunchKernelGGL((layer_norm_backward_kernel<B, W, G, VPT, S>), dim3(blocks), dim3(block_threads<G>()), 0,    \
+                     stream, static_cast<const uint4*>(dy), static_cast<const uint4*>(s), w, mean, rstd,          \
+                     static_cast<const uint4*>(ds), static_cast<uint4*>(dx), partial, T, row_vec, inv_d)
+#define MOE_NORM_BWD(B, W, G, VPT)                   \
+  do {                                               \
+    blocks = row_blocks<G>(T, kBackwardBlocks);      \
+    if (big) MOE_NORM_BWD_S(B, W, G, VPT, true);     \
+    else MOE_NORM_BWD_S(B, W, G, VPT, false);        \
   } while (0)
 #define MOE_NORM_BWD_BB(G, VPT) MOE_NORM_BWD(true, true, G, VPT)
 #define MOE_NORM_BWD_BF(G, VPT) MOE_NORM_BWD(true, false, G, VPT)
 #define MOE_NORM_BWD_FF(G, VPT) MOE_NORM_BWD(false, false, G, VPT)
-    if (bf16 && wbf16) { MOE_ROW_SHAPES(MOE_NORM_BWD_BB); }
-    else if (bf16) { MOE_ROW_SHAPES(MOE_NORM_BWD_BF); }
-    else { MOE_ROW_SHAPES(MOE_NORM_BWD_FF); }
+    if (bf16 && wbf16) { MOE_NORM_BWD_SHAPES(MOE_NORM_BWD_BB); }
+    else if (bf16) { MOE_NORM_BWD_SHAPES(MOE_NORM_BWD_BF); }
+    else { MOE_NORM_BWD_SHAPES(MOE_NORM_BWD_FF); }
 #undef MOE_NORM_BWD_BB
 #undef MOE_NORM_BWD_BF
 #undef MOE_NORM_BWD_FF
 #undef MOE_NORM_BWD
+#undef MOE_NORM_BWD_S
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

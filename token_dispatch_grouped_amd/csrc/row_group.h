@@ -49,6 +49,31 @@ struct Vec16<false> {
   }
 };
 
+// A 16-byte vector, with STREAM past the caches (data that is too large to be found there again).
+template <bool STREAM>
+__device__ __forceinline__ uint4 load16(const uint4* p) {
+  if constexpr (STREAM) {
+    const i32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(p));
+    return make_uint4(static_cast<uint32_t>(v.x), static_cast<uint32_t>(v.y), static_cast<uint32_t>(v.z),
+                      static_cast<uint32_t>(v.w));
+  } else {
+    return *p;
+  }
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(uint4* p, const uint4& v) {
+  if constexpr (STREAM) {
+    const i32x4_t d = {static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w)};
+    __builtin_nontemporal_store(d, reinterpret_cast<i32x4_t*>(p));
+  } else {
+    *p = v;
+  }
+}
+
+// Bytes of one call from which its tensors are streamed: the memory-side cache holds 256 MB, so
+// a call that moves more finds little of its data there again, and neither does the next one.
+constexpr int64_t kStreamBytes = int64_t{256} << 20;
+
 // kN consecutive parameters (N = 8 or 4) from vector c of a bf16 or fp32 array
 template <int N, bool BF16>
 __device__ __forceinline__ void load_params(const void* p, int c, float* f) {
@@ -70,24 +95,37 @@ struct Max {
   __device__ static T apply(T a, T b) { return a > b ? a : b; }
 };
 
-// Reduction of one value per thread over a group of G threads (a power of two);
-// every thread gets the result, which is the same bits in each and does not
-// depend on timing. For G > 64 the group is the workgroup, `lds` holds G / 64
-// values and is free again when the call returns.
-template <int G, typename Op, typename T>
-__device__ __forceinline__ T group_reduce(T v, T* lds) {
+// Reduction of N values per thread over a group of G threads (a power of two); every
+// thread gets the results, which are the same bits in each and do not depend on
+// timing. For G > 64 the group is the workgroup and `lds` holds N * G / 64 values:
+// it must not be the buffer of the call before (which a slower wave may still read),
+// so callers alternate between two.
+template <int G, typename Op, int N, typename T>
+__device__ __forceinline__ void group_reduce(T (&v)[N], T* lds) {
 #pragma unroll
-  for (int off = (G < kWave ? G : kWave) / 2; off > 0; off >>= 1) v = Op::apply(v, __shfl_xor(v, off));
+  for (int off = (G < kWave ? G : kWave) / 2; off > 0; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = Op::apply(v[i], __shfl_xor(v[i], off));
   if constexpr (G > kWave) {
     constexpr int kW = G / kWave;
-    if (lane_id() == 0) lds[threadIdx.x / kWave] = v;
-    __syncthreads();
-    v = lds[0];
+    if (lane_id() == 0)
 #pragma unroll
-    for (int i = 1; i < kW; ++i) v = Op::apply(v, lds[i]);
+      for (int i = 0; i < N; ++i) lds[i * kW + threadIdx.x / kWave] = v[i];
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = lds[i * kW];
+#pragma unroll
+      for (int w = 1; w < kW; ++w) v[i] = Op::apply(v[i], lds[i * kW + w]);
+    }
   }
-  return v;
+}
+
+template <int G, typename Op, typename T>
+__device__ __forceinline__ T group_reduce(T v, T* lds) {
+  T a[1] = {v};
+  group_reduce<G, Op, 1, T>(a, lds);
+  return a[0];
 }
 
 }  // namespace rows
