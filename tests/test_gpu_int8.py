@@ -30,6 +30,7 @@ if not torch.cuda.is_available():  # pragma: no cover
 import token_dispatch_grouped_amd as moe  # noqa: E402
 
 U = 2.0 ** -24
+FEW = 64  # tokens up to which the codes may never reach the workspace
 
 
 def _np(t):
@@ -83,12 +84,13 @@ def _check(w, x, logits, experts):
     xq, xs, h, hq, hs = _parts(ws, w.n_max, w.d, w.d_ff)
     x32 = x.float().cpu().numpy()[tok]
     want_q, want_s = oa.quantize(x32)
-    np.testing.assert_array_equal(_np(xq)[:, :n_loc], oa.kblocks(want_q))
-    _equal_scales(_np(xs)[:n_loc], want_s)
     h_got = g.to_f64(h)[:n_loc]
     hq_want, hs_want = oa.quantize(h_got.astype(np.float32))
-    np.testing.assert_array_equal(_np(hq)[:, :n_loc], oa.kblocks(hq_want))
-    _equal_scales(_np(hs)[:n_loc], hs_want)
+    if w.T > FEW:  # a few tokens' codes stay on the chip
+        np.testing.assert_array_equal(_np(xq)[:, :n_loc], oa.kblocks(want_q))
+        _equal_scales(_np(xs)[:n_loc], want_s)
+        np.testing.assert_array_equal(_np(hq)[:, :n_loc], oa.kblocks(hq_want))
+        _equal_scales(_np(hs)[:n_loc], hs_want)
     wgu, sgu = oa.from_kblocks(_np(experts.w_gate_up), w.d), _np(experts.gate_up_scale)
     wdn, sdn = oa.from_kblocks(_np(experts.w_down), w.d_ff), _np(experts.down_scale)
     y_got = g.to_f64(y)
@@ -131,6 +133,10 @@ CASES = [
     W("i8_all_of_k", 40, 64, 520, 8, 8, 0, 8, "bf16", 69),
     W("i8_wide_k", 20, 2056, 4104, 4, 2, 0, 2, "bf16", 70),     # rows of 256-thread groups
     W("i8_wider_k", 6, 64, 8712, 2, 1, 0, 2, "bf16", 71),       # rows of 1024-thread groups
+    W("i8_few", 16, 200, 328, 32, 4, 8, 16, "bf16", 77),        # a few tokens, two rows per expert
+    W("i8_few_many_rows", 64, 136, 72, 64, 1, 0, 64, "bf16", 78, 3.0),  # skewed: several row tiles of one expert
+    W("i8_few_wide", 8, 512, 2056, 64, 4, 0, 64, "bf16", 79),   # enough channels for the wide workgroups
+    W("i8_few_long_k", 1, 64, 8712, 2, 1, 0, 2, "bf16", 80),    # more of a row than its threads hold
     W("i8_stages", 260, 448, 192, 2, 1, 0, 2, "bf16", 72),      # 7 and 3 K stages
 ]
 

@@ -233,10 +233,10 @@ def _place(stream, ts):
     that come from another stream are recorded on it, so that freeing them early
     does not hand their memory out while the call still runs."""
     torch = _torch()
-    index = ts[0].get_device()
-    for t in ts:
-        if t.get_device() != index:
-            raise ValueError(f"every tensor must be on one GPU, got {ts[0].device} and {t.device}")
+    devices = set(map(torch.Tensor.get_device, ts))
+    if len(devices) > 1:
+        raise ValueError(f"every tensor must be on one GPU, got GPUs {sorted(devices)}")
+    index = devices.pop()
     if stream is None and index == torch.cuda.current_device():
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
         return (raw(index) if raw else torch.cuda.current_stream(index).cuda_stream), _SAME
@@ -1003,13 +1003,13 @@ def _tensor_list(ts, name: str):
         for i, t in enumerate(ts):
             _want(t, f"{name}[{i}]", _act_dtypes())
         raise
-    return ts, [t.numel() for t in ts], kinds
+    return ts, list(map(torch.Tensor.numel, ts)), kinds
 
 
 def _host_list(ts, numels, kinds):
     """The host array of moe_tensor (address, length and dtype code, eight bytes each) as a C pointer."""
     flat = [0] * (3 * len(ts))
-    flat[::3] = [t.data_ptr() for t in ts]
+    flat[::3] = map(_torch().Tensor.data_ptr, ts)
     flat[1::3] = numels
     flat[2::3] = kinds
     return array.array("q", flat)
@@ -1018,9 +1018,8 @@ def _host_list(ts, numels, kinds):
 def _list_ready(stream, ts, *others):
     """_place for a list of gradients (aligned to their elements only) and its buffers."""
     all_ = ts + [t for t in others if t is not None]
-    for t in all_:
-        if not t.is_cuda or not t.is_contiguous():
-            _dev(t)
+    if min(map(_torch().Tensor.get_device, all_)) < 0 or not all(map(_torch().Tensor.is_contiguous, all_)):
+        _dev(*all_)
     return _place(stream, all_)
 
 

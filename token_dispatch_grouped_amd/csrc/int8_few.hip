@@ -1,0 +1,211 @@
+// The experts' FFN in 8-bit integers for a few tokens (single-token decoding): two
+// launches, each quantising its own rows.
+//
+//   gate/up: rows of x (through perm) -> codes in LDS; H = silu(G) * U (bf16)
+//   down:    rows of H -> codes in LDS; Y (bf16)
+//
+// With a handful of rows the weights are streamed once for almost no arithmetic, so
+// what counts is bytes in flight and launches. A workgroup takes up to 16 rows of an
+// expert and 16 * FRAGS weight channels over all of K; its four waves take a quarter of
+// K each and ask for their weights, straight into registers, before anything else.
+// While those are on their way the workgroup quantises its rows (each workgroup of an
+// expert does so again: a few KB from L2 next to its 100 KB of weights).
+// v_mfma_i32_16x16x64_i8: 16 channels x 64 K values of the K-blocked weights are one
+// contiguous KB, lane L's 16 bytes at (L & 15) * 64 + (L >> 4) * 16. Integer sums are
+// exact, so the quarters of K are joined in any order with the same bits.
+#include "int8_code.h"
+#include "gemm_common.h"
+
+namespace moe {
+namespace {
+
+using namespace int8;
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kRows = 16;
+constexpr int kHeld = 4;    // vectors of a row a thread holds between its two passes
+constexpr int kMaxCodes = 48 * 1024;
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+__host__ __device__ constexpr int code_stride(int kblocks) { return kblocks * 64 + 16; }  // rows fall into different banks
+
+// FRAGS 16-channel blocks of a workgroup (SwiGLU: half gate, half up), AHEAD K-blocks that
+// a wave has in flight; three waves per SIMD.
+template <bool SWIGLU, int FRAGS, int AHEAD>
+__global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
+    const uint4* __restrict__ src, const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets,
+    const uint8_t* __restrict__ w, const float* __restrict__ w_scale, __bf16* __restrict__ out, int e_begin, int k,
+    int64_t T, int cols_vec, int kblocks, int N, int64_t n_max) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  __shared__ i32x4 part[kWaves * FRAGS * kWave];
+  __shared__ float scales[kRows];
+  __shared__ uint32_t tops[2][kWaves];
+  constexpr int NO = SWIGLU ? FRAGS / 2 : FRAGS;
+  const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid / kWave);
+  const int e = blockIdx.y;
+  const int seg0 = offsets[e_begin];
+  const int start = static_cast<int>(min(static_cast<int64_t>(offsets[e_begin + e] - seg0), n_max));
+  const int end = static_cast<int>(min(static_cast<int64_t>(offsets[e_begin + e + 1] - seg0), n_max));
+  const int r0 = start + static_cast<int>(blockIdx.z) * kRows;
+  if (r0 >= end) return;
+  const int R = min(kRows, end - r0);
+  const int n0 = static_cast<int>(blockIdx.x) * 16 * NO;
+  const int64_t channels = SWIGLU ? 2 * static_cast<int64_t>(N) : N;
+  const uint8_t* we = w + e * channels * kblocks * 64;
+
+  // this wave's quarter of K, its first weights in flight
+  const int lo = kblocks * wv / kWaves, hi = kblocks * (wv + 1) / kWaves;
+  uint32_t off[FRAGS];
+#pragma unroll
+  for (int f = 0; f < FRAGS; ++f) {
+    const int col = min(n0 + 16 * (f % NO) + (lane & 15), N - 1);  // channels past N are read again and not stored
+    off[f] = static_cast<uint32_t>(col + (f >= NO ? N : 0)) * 64u + static_cast<uint32_t>(lane >> 4) * 16u;
+  }
+  i32x4 b[AHEAD][FRAGS];
+  auto load = [&](int kb0) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (kb0 + u < hi) {
+        const uint8_t* p = we + (kb0 + u) * channels * 64;
+#pragma unroll
+        for (int f = 0; f < FRAGS; ++f)
+          b[u][f] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p + off[f]));
+      }
+  };
+  load(lo);
+  __builtin_amdgcn_sched_barrier(0);
+
+  // the rows' codes, a row at a time by all threads
+  const int stride = code_stride(kblocks);
+  for (int r = 0; r < R; ++r) {
+    int64_t from = r0 + r;
+    if (perm != nullptr) from = perm[seg0 + r0 + r] / k;
+    const int n = perm == nullptr || (from >= 0 && from < T) ? cols_vec : 0;
+    const uint4* row = src + from * cols_vec;
+    uint4 v[kHeld];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int c = i * kThreads + tid;
+      v[i] = c < n ? row[c] : make_uint4(0, 0, 0, 0);
+    }
+    for (int c = kHeld * kThreads + tid; c < n; c += kThreads) top = rows::Max::apply(top, amax8(row[c]));
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) top = rows::Max::apply(top, amax8(v[i]));
+    top = rows::group_reduce<kThreads, rows::Max>(top, tops[r & 1]);
+    float sc, inv;
+    scale_of(top, &sc, &inv);
+    if (tid == 0) scales[r] = sc;
+    char* codes = smem + r * stride;
+    auto put = [&](int c, const uint4& a) {
+      float f[8];
+      rows::Vec16<true>::unpack(a, f);
+      *reinterpret_cast<uint2*>(codes + c * 8) = codes8(f, inv);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int c = i * kThreads + tid;
+      if (c < kblocks * 8) put(c, v[i]);  // zeros past the last column
+    }
+    for (int c = kHeld * kThreads + tid; c < kblocks * 8; c += kThreads)
+      put(c, c < n ? row[c] : make_uint4(0, 0, 0, 0));
+  }
+  __syncthreads();
+
+  // lanes of rows past the last read the last row's codes; their sums are not stored
+  const char* mine = smem + min(lane & 15, R - 1) * stride + (lane >> 4) * 16;
+  i32x4 acc[FRAGS];
+#pragma unroll
+  for (int f = 0; f < FRAGS; ++f) acc[f] = i32x4{0, 0, 0, 0};
+  for (int kb0 = lo; kb0 < hi; kb0 += AHEAD) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (kb0 + u < hi) {
+        const i32x4 a = *reinterpret_cast<const i32x4*>(mine + (kb0 + u) * 64);
+#pragma unroll
+        for (int f = 0; f < FRAGS; ++f) acc[f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b[u][f], acc[f], 0, 0, 0);
+      }
+    if (kb0 + AHEAD < hi) load(kb0 + AHEAD);
+  }
+#pragma unroll
+  for (int f = 0; f < FRAGS; ++f) part[(wv * FRAGS + f) * kWave + lane] = acc[f];
+  __syncthreads();
+
+  // a thread per element of a 16 x 16 block: lane l's element j of a block is row (l >> 4) * 4 + j, channel l & 15
+  const int j = wv, row = (lane >> 4) * 4 + j;
+  auto sum = [&](int f) {
+    int s = 0;
+#pragma unroll
+    for (int q = 0; q < kWaves; ++q) s += reinterpret_cast<const int*>(part)[((q * FRAGS + f) * kWave + lane) * 4 + j];
+    return static_cast<float>(s);
+  };
+  if (row < R) {
+    const float* se = w_scale + e * channels;
+    const float sa = scales[row];
+#pragma unroll
+    for (int f = 0; f < NO; ++f) {
+      const int col = n0 + 16 * f + (lane & 15);
+      if (col < N) {
+        float v = sum(f) * se[col] * sa;
+        if constexpr (SWIGLU) v = gemm::silu_fast(v) * (sum(f + NO) * se[N + col] * sa);
+        out[static_cast<int64_t>(r0 + row) * N + col] = static_cast<__bf16>(v);
+      }
+    }
+  }
+}
+
+template <bool SWIGLU, int FRAGS, int AHEAD>
+hipError_t launch_one(const void* src, const int32_t* perm, const int32_t* offsets, const void* w,
+                      const float* w_scale, void* out, int e_begin, int e_loc, int k, int64_t T, int K, int N,
+                      int64_t n_max, hipStream_t stream) {
+  constexpr int cols = 16 * (SWIGLU ? FRAGS / 2 : FRAGS);
+  const int kblocks = int8_kblocks(K);
+  const int rows = static_cast<int>(T < kRows ? T : kRows);
+  const dim3 grid(static_cast<unsigned>((N + cols - 1) / cols), static_cast<unsigned>(e_loc),
+                  static_cast<unsigned>((T + kRows - 1) / kRows));
+  hipLaunchKernelGGL((int8_few_kernel<SWIGLU, FRAGS, AHEAD>), grid, dim3(kThreads),
+                     static_cast<unsigned>(rows * code_stride(kblocks)), stream, static_cast<const uint4*>(src), perm,
+                     offsets, static_cast<const uint8_t*>(w), w_scale, static_cast<__bf16*>(out), e_begin, k, T, K / 8,
+                     kblocks, N, n_max);
+  return hipGetLastError();
+}
+
+// Narrow workgroups where wide ones would be fewer than four per CU (one token, 4 of 32 experts of
+// 1000 x 1480: 11.2 us against 13.4; one token, 2 experts of 4096 x 14336: 59.6 against 63.5); the
+// wide ones' longer runs stream better once they fill the chip (32 tokens, 128 experts of 2880 x
+// 2880: 296 us against 342).
+template <bool SWIGLU>
+hipError_t launch_product(const void* src, const int32_t* perm, const int32_t* offsets, const void* w,
+                          const float* w_scale, void* out, int e_begin, int e_loc, int k, int64_t T, int K, int N,
+                          int64_t n_max, hipStream_t stream) {
+  const int wide = 16 * (SWIGLU ? 2 : 4);
+  const int64_t active = n_max < e_loc ? n_max : e_loc;
+  if (active * ((N + wide - 1) / wide) < 4 * device_cu_count())
+    return launch_one<SWIGLU, 2, 6>(src, perm, offsets, w, w_scale, out, e_begin, e_loc, k, T, K, N, n_max, stream);
+  return launch_one<SWIGLU, 4, 4>(src, perm, offsets, w, w_scale, out, e_begin, e_loc, k, T, K, N, n_max, stream);
+}
+
+}  // namespace
+
+// Up to two rows per expert on average and 64 tokens, whose codes fit a workgroup's LDS. Against the
+// staged path (graph replays): one token 11 us for 25, 8 tokens x 4 of 128 experts of 2880 x 2880 107
+// for 120, 32 tokens 289 for 294, 64 tokens (two rows each) 415 for 414, 128 tokens 541 for 476; small
+// experts lose earlier (16 tokens x 2 of 8 experts of 64 x 64, four rows each: 17.5 for 13.9).
+bool int8_few(int64_t T, int k, int E, int d, int d_ff) {
+  const int64_t rows = T < kRows ? T : kRows;
+  return T <= 64 && T * k <= 2 * static_cast<int64_t>(E) &&
+         rows * code_stride(int8_kblocks(d > d_ff ? d : d_ff)) <= kMaxCodes;
+}
+
+hipError_t launch_int8_few(const void* x, const int32_t* perm, const int32_t* offsets, const void* q_gu,
+                           const float* s_gu, const void* q_dn, const float* s_dn, void* h, void* y, int d, int d_ff,
+                           int e_begin, int e_loc, int k, int64_t T, int64_t n_max, hipStream_t stream) {
+  const hipError_t e =
+      launch_product<true>(x, perm, offsets, q_gu, s_gu, h, e_begin, e_loc, k, T, d, d_ff, n_max, stream);
+  if (e != hipSuccess) return e;
+  return launch_product<false>(h, nullptr, offsets, q_dn, s_dn, y, e_begin, e_loc, k, T, d_ff, d, n_max, stream);
+}
+
+}  // namespace moe

@@ -13,41 +13,14 @@
 // of R rows holds [R][64] bytes, columns 64 kb .. 64 kb + 63 of every row, zero
 // past the last column. A K = 64 stage of a tile is then one contiguous run.
 // Everything here is bound by HBM: a row is read once and its codes written once.
+#include "int8_code.h"
 #include "int8_plan.h"
-#include "row_group.h"
 
 namespace moe {
 namespace {
 
 using namespace rows;
-
-constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
-
-__device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
-
-// scale and 1 / scale from the largest absolute value's bits (as unsigned
-// integers these order like the values, infinities and NaN above all others)
-__device__ __forceinline__ void scale_of(uint32_t amax_bits, float* scale, float* inv) {
-  if (amax_bits >= 0x7F800000u) {
-    *scale = __uint_as_float(0x7FC00000u);
-    *inv = 0.f;
-  } else {
-    *scale = fmaxf(__uint_as_float(amax_bits) / 127.f, kMinScale);
-    *inv = 1.f / *scale;
-  }
-}
-
-__device__ __forceinline__ uint32_t code(float f, float inv) {
-  // inv = 0 marks a row without finite scale
-  return inv == 0.f ? 0u : static_cast<uint32_t>(static_cast<int>(rintf(f * inv))) & 0xFFu;
-}
-
-__device__ __forceinline__ uint2 codes8(const float* f, float inv) {
-  uint2 o;
-  o.x = code(f[0], inv) | code(f[1], inv) << 8 | code(f[2], inv) << 16 | code(f[3], inv) << 24;
-  o.y = code(f[4], inv) | code(f[5], inv) << 8 | code(f[6], inv) << 16 | code(f[7], inv) << 24;
-  return o;
-}
+using namespace int8;
 
 template <int G>
 constexpr int block_threads() { return G > 256 ? G : 256; }
@@ -91,12 +64,7 @@ __global__ __launch_bounds__(block_threads<G>()) void quantize_rows_kernel(
       v[i] = c < n ? src[from * cols_vec + c] : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      float f[8];
-      Vec16<true>::unpack(v[i], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = Max::apply(top, abs_bits(f[j]));
-    }
+    for (int i = 0; i < VPT; ++i) top = Max::apply(top, amax8(v[i]));
     top = group_reduce<G, Max>(top, lds[turn]);
     turn ^= 1;
     float sc, inv;

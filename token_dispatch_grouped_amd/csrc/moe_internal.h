@@ -158,6 +158,12 @@ hipError_t launch_grouped_gemm_int8(const void* a, const float* a_scale, const v
                                     const void* plan, int e_loc, int K, int N, int64_t n_max, bool swiglu,
                                     hipStream_t stream);
 
+// The same FFN for a few tokens, in two launches that quantise their own rows (h: n_max rows of d_ff, bf16)
+bool int8_few(int64_t T, int k, int E, int d, int d_ff);
+hipError_t launch_int8_few(const void* x, const int32_t* perm, const int32_t* offsets, const void* q_gu,
+                           const float* s_gu, const void* q_dn, const float* s_dn, void* h, void* y, int d, int d_ff,
+                           int e_begin, int e_loc, int k, int64_t T, int64_t n_max, hipStream_t stream);
+
 size_t grad_norm_workspace_bytes(int n);
 hipError_t launch_grad_norm(const moe_tensor* t, int n, float* norm, void* ws, hipStream_t stream);
 hipError_t launch_clip_grads(const moe_tensor* t, const moe_tensor* out, int n, const float* norm, float max_norm,
