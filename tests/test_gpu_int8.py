@@ -159,6 +159,21 @@ def test_every_row_count():
     np.testing.assert_array_equal(_np(disp.counts), counts)
 
 
+@pytest.mark.parametrize("d,f", [(256, 160), (264, 1352), (1480, 72)])
+def test_every_row_count_of_tall_tiles(d, f):
+    """Many rows per expert: tiles of 256 rows, remainders that ride along (up to 288 rows) or
+    get a tile of their own, whole and halved, and empty and light experts among them."""
+    counts = [256, 0, 257, 288, 289, 300, 512, 544, 545, 1, 384, 600, 40]
+    E, T = len(counts), sum(counts)
+    rng = np.random.default_rng(74)
+    owner = np.repeat(np.arange(E), counts)
+    rng.shuffle(owner)
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    logits[np.arange(T), owner] += 50.0
+    disp, _ = _case(W("i8_tall", T, d, f, E, 1, 0, E, "bf16", 74), logits)
+    np.testing.assert_array_equal(_np(disp.counts), counts)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("e,d,f", [(3, 72, 136), (1, 8, 8), (2, 256, 64), (2, 200, 520)])
 def test_quantized_weights(e, d, f, dt):

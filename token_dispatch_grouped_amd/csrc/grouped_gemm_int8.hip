@@ -55,38 +55,41 @@ __device__ __forceinline__ void mfma_i8_in_vgprs(i32x16_t& c, const i32x4_t& a, 
   asm volatile("v_mfma_i32_32x32x32_i8 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
 }
 
-// H rows of the tile: 32, 64, 128, 256 or 288; 256 weight channels. A 288-row tile is a
-// 256-row tile plus one 32-row block that every wave shares, each computing it against
-// half of its own channel blocks.
-template <int H, int LDS>
+// H rows of the tile: 32, 64, 128, 256 or 288; BN weight channels: 256, or 128 for half of a
+// tall tile. A 288-row tile is a 256-row tile plus one 32-row block that every wave shares,
+// each computing it against half of its own channel blocks (all of its two at BN = 128,
+// where the second wave row's results are the first's and are not stored).
+template <int H, int BN, int LDS>
 struct Layout {
   static constexpr int WM = H >= 64 ? 2 : 1;  // waves along M
   static constexpr int WN = 4 / WM;
   static constexpr int MI = H / WM / 32;      // 32-row blocks per wave (regular part)
-  static constexpr int NI = 256 / WN / 32;    // 32-channel blocks per wave
+  static constexpr int NI = BN / WN / 32;     // 32-channel blocks per wave
   static constexpr int XR = H == 288 ? 1 : 0;
   static constexpr int MX = 2 * XR;           // extra MFMAs per wave and slice
   static constexpr int A_INSTR = H / 16;      // 1 KB loads per activation stage
   static constexpr int A_PER_WAVE = (A_INSTR + 3) / 4;
-  static constexpr int B_PER_WAVE = 4;
+  static constexpr int B_PER_WAVE = BN / 64;
   static constexpr int PER = A_PER_WAVE + B_PER_WAVE;
   static constexpr int READS = MI + XR + NI;
   static constexpr int NMFMA = MX + MI * NI;
-  static constexpr uint32_t A_BYTES = H * kBK, B_BYTES = 256 * kBK;
-  // stages that fit, at most eight (vmcnt counts 63 loads, a wave has PER per stage)
+  static constexpr uint32_t A_BYTES = H * kBK, B_BYTES = BN * kBK;
+  // stages that fit, at most six (vmcnt counts 63 loads, a wave has PER per stage)
   static constexpr int FIT = LDS / static_cast<int>(A_BYTES + B_BYTES);
   static constexpr int NS = FIT < 6 ? FIT : 6;
   static_assert((NS - 2) * PER < 64, "loads in flight are counted in six bits");
+  static_assert(BN == 256 || (BN == 128 && WN == 2), "half-width tiles have two waves along N");
 };
 
 // One tile: rows [row0, row0 + rows_valid) of A (K-blocks of n_rows rows), channels
 // from n0 of the expert's weights. STREAM: no other row tile reads this weight panel.
-template <bool SWIGLU, int H, int LDS, bool STREAM>
+template <bool SWIGLU, int H, int BN, int LDS, bool STREAM>
 __device__ __forceinline__ void gemm_tile(char* smem, const uint8_t* __restrict__ A, const float* __restrict__ a_scale,
                                           const uint8_t* __restrict__ Bexp, const float* __restrict__ b_scale,
                                           uint16_t* __restrict__ C, int row0, int rows_valid, int n0, int ksteps, int N,
                                           int64_t n_rows) {
-  using L = Layout<H, LDS>;
+  using L = Layout<H, BN, LDS>;
+  constexpr int HB = BN / 2;
   constexpr int MI = L::MI, NI = L::NI, WM = L::WM, WN = L::WN, PER = L::PER, NS = L::NS;
   // opaque: the lane's offsets are recomputed for each tile instead of living through the kernel for every height
   const int tid = opaque(static_cast<int>(threadIdx.x));
@@ -115,9 +118,9 @@ __device__ __forceinline__ void gemm_tile(char* smem, const uint8_t* __restrict_
 #pragma unroll
   for (int jj = 0; jj < L::B_PER_WAVE; ++jj) {
     const int r = 16 * (wave * L::B_PER_WAVE + jj) + (lane >> 2);  // row of the weight stage
-    const int c = SWIGLU ? n0 + (r & 127) : n0 + r;
+    const int c = SWIGLU ? n0 + (r & (HB - 1)) : n0 + r;
     // channels past N point past the buffer: zeros, without a fetch
-    b_voff[jj] = c < N ? static_cast<uint32_t>(c + (SWIGLU && r >= 128 ? N : 0)) * 64u + chunk : 0x80000000u;
+    b_voff[jj] = c < N ? static_cast<uint32_t>(c + (SWIGLU && r >= HB ? N : 0)) * 64u + chunk : 0x80000000u;
   }
   const uint8_t* a_tile = A + static_cast<int64_t>(row0) * 64;
   // these threads' row scales, for the epilogue (asked for before the pipeline's loads, so no wait counts them)
@@ -130,9 +133,9 @@ __device__ __forceinline__ void gemm_tile(char* smem, const uint8_t* __restrict_
   // SwiGLU and its up pair, else and slot 1), the blocks that the other wave row does not take.
   constexpr int X1 = SWIGLU ? NI / 2 : 1;
   auto bcol = [&](int ni) {
-    if (L::XR && wm) ni = SWIGLU ? ni ^ 1 : ni ^ 2;
-    if (SWIGLU) return ni < NI / 2 ? wn * (128 / WN) + ni * 32 : 128 + wn * (128 / WN) + (ni - NI / 2) * 32;
-    return wn * (256 / WN) + ni * 32;
+    if (L::XR && wm && BN == 256) ni = SWIGLU ? ni ^ 1 : ni ^ 2;
+    if (SWIGLU) return ni < NI / 2 ? wn * (HB / WN) + ni * 32 : HB + wn * (HB / WN) + (ni - NI / 2) * 32;
+    return wn * (BN / WN) + ni * 32;
   };
   uint32_t a_rd[2], b_rd[2], b_slot[NI];
 #pragma unroll
@@ -321,6 +324,7 @@ __device__ __forceinline__ void gemm_tile(char* smem, const uint8_t* __restrict_
       for (int j = 0; j < 4; ++j) {
         const int r = 4 * r4 + j;
         if (x) {
+          if (BN == 128 && wm != 0) continue;  // the first wave row stores the shared block
           if constexpr (L::XR) {
             if constexpr (SWIGLU) {
               emit(acc_x[0][r], acc_x[1][r], sb[0], sb[NO], sa[j], row4 + j, coff[0]);
@@ -345,6 +349,7 @@ __global__ __launch_bounds__(kThreads, TALL ? 1 : 2) void grouped_gemm_int8_kern
     const uint8_t* __restrict__ A, const float* __restrict__ a_scale, const uint8_t* __restrict__ B,
     const float* __restrict__ b_scale, uint16_t* __restrict__ C, const int* __restrict__ n_row_tiles,
     const RowGroup* __restrict__ groups, int kblocks, int N, int64_t n_max) {
+  // n_row_tiles[0]: all entries, [1]: those of experts with tall tiles (they come first)
   constexpr int LDS = TALL ? kTallLds : kShortLds;
   constexpr int BM = TALL ? int8::kTallRows : int8::kShortRows;
   __shared__ __attribute__((aligned(1024))) char smem[LDS];
@@ -355,32 +360,41 @@ __global__ __launch_bounds__(kThreads, TALL ? 1 : 2) void grouped_gemm_int8_kern
   const int G = gridDim.x, per = G >> 3;
   const bool spread = (G & 7) == 0;
   const int r = xcd_remap(blockIdx.x, G);
+  // The last, partial round: where its tall tiles can be halved and all of it still fits one
+  // round, they are (16 experts of 256 rows, 2880 x 2880: gate/up is 368 tiles on 256 CUs).
+  const int rounds = (total + G - 1) / G, last = total - (rounds - 1) * G;
+  const int tall_last = min(max(uniform(n_row_tiles[1]) * n_tiles - (rounds - 1) * G, 0), last);
+  const int n_split = TALL && last < G && last + tall_last <= G ? tall_last : 0;
   for (int i = 0;; ++i) {
     // Whole rounds give each XCD a contiguous run of tile ids, forward and backward in turn. The
     // last, partial one deals its tiles evenly over the XCDs: each has its own way to HBM, and
     // on 3.5 of the 8 a half-full round took as long as a full one (16 experts of 256 rows,
     // 2880 x 2880: gate/up 98 -> 90 us).
-    int tile;
+    int tile, half = 0;  // half: 0 the whole tile, 1 or 2 its first or second half
     const int rest = total - i * G;
     if (rest >= G) {
       tile = snake_tile(i, r, G);
     } else {
-      int lo = 0, j = r, hi = rest;
+      const int items = rest + n_split;
+      int lo = 0, j = r, hi = items;
       if (spread) {
         const int x = r / per;
-        lo = rest * x / 8;
-        hi = rest * (x + 1) / 8;
+        lo = items * x / 8;
+        hi = items * (x + 1) / 8;
         j = r - x * per;
       }
       if (rest <= 0 || lo + j >= hi) break;
-      tile = i * G + lo + j;
+      const int item = lo + j;
+      tile = i * G + (item < 2 * n_split ? item >> 1 : item - n_split);
+      if (item < 2 * n_split) half = 1 + (item & 1);
     }
     // ids of a group of row tiles of one expert: row tile fastest, then the column block
     const int q = tile / n_tiles;
     const RowGroup g = groups[q];
     const int off = tile - (q - uniform(g.index)) * n_tiles;
     const int in_group = uniform(g.tiles);
-    const int mt = off % in_group, n0 = off / in_group * kOutCols;
+    const int mt = off % in_group, n0 = off / in_group * kOutCols + (half == 2 ? kOutCols / 2 : 0);
+    if (n0 >= N) break;  // the second half of a last column block that has only a first
     const int row0 = uniform(g.row0) + mt * BM;
     const int rows = uniform(g.last) && mt == in_group - 1 ? uniform(g.row_end) - row0 : BM;
     const int e = uniform(g.expert);
@@ -392,16 +406,21 @@ __global__ __launch_bounds__(kThreads, TALL ? 1 : 2) void grouped_gemm_int8_kern
     auto run = [&](auto stream) {
       constexpr bool S = decltype(stream)::value;
       if constexpr (TALL) {
+        if (half) {
+          if (rows > 256)
+            return gemm_tile<SWIGLU, 288, 128, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
+          return gemm_tile<SWIGLU, 256, 128, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
+        }
         if (rows > 256)
-          return gemm_tile<SWIGLU, 288, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
+          return gemm_tile<SWIGLU, 288, 256, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
         if (rows > 128)
-          return gemm_tile<SWIGLU, 256, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
+          return gemm_tile<SWIGLU, 256, 256, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
       }
       if (rows > 64)
-        return gemm_tile<SWIGLU, 128, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
+        return gemm_tile<SWIGLU, 128, 256, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
       if (rows > 32)
-        return gemm_tile<SWIGLU, 64, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
-      return gemm_tile<SWIGLU, 32, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
+        return gemm_tile<SWIGLU, 64, 256, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
+      return gemm_tile<SWIGLU, 32, 256, LDS, S>(smem, A, a_scale, Be, be, C, row0, rows, n0, kblocks, N, n_max);
     };
     if (uniform(g.alone)) run(std::true_type{});
     else run(std::false_type{});

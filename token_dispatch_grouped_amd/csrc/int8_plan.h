@@ -25,7 +25,7 @@ struct alignas(16) RowGroup {
 };
 static_assert(sizeof(RowGroup) == 16, "one 16-byte load");
 
-constexpr size_t kPlanHeader = 256;  // an int: how many entries
+constexpr size_t kPlanHeader = 256;  // two ints: how many entries, and how many are of experts with more than 128 rows
 
 inline int64_t max_row_tiles(int64_t n_max, int e_loc, bool tall) {
   return n_max / (tall ? kTallRows : kShortRows) + (n_max < e_loc ? n_max : e_loc);
@@ -84,8 +84,9 @@ __device__ void plan_tiles(const int32_t* __restrict__ offsets, int e_begin, int
       if (mine > 0) plan_expert<BM, MERGE>(out + at + incl - mine, e, start, rows);
       at += __shfl(incl, kWave - 1);
     }
+    if (cls == 0 && lane == 0) count[1] = at;
   }
-  if (lane == 0) *count = at;
+  if (lane == 0) count[0] = at;
 }
 
 }  // namespace int8
