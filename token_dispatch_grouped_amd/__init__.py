@@ -153,6 +153,7 @@ def _check(status: int, where: str) -> None:
 # ----------------------------------------------------------------------------- torch helpers
 
 _TORCH = None
+_CODES: dict = {}  # torch dtype -> moe_dtype
 
 
 def _torch():
@@ -161,6 +162,7 @@ def _torch():
     if _TORCH is None:
         import torch
         _TORCH = torch
+        _CODES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16})
     return _TORCH
 
 
@@ -234,9 +236,10 @@ def _place(stream, ts):
     does not hand their memory out while the call still runs."""
     torch = _torch()
     devices = set(map(torch.Tensor.get_device, ts))
-    if len(devices) > 1:
-        raise ValueError(f"every tensor must be on one GPU, got GPUs {sorted(devices)}")
     index = devices.pop()
+    if devices or index < 0:
+        _dev(*ts)
+        raise ValueError(f"every tensor must be on one GPU, got GPUs {sorted({index, *devices})}")
     if stream is None and index == torch.cuda.current_device():
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
         return (raw(index) if raw else torch.cuda.current_stream(index).cuda_stream), _SAME
@@ -256,17 +259,18 @@ def _ready(stream, vectors, others=()):
     """_place after checking that every tensor (None: not given) is dense and on the
     GPU, and that `vectors`, which move in 16-byte pieces, start at such a boundary."""
     ts = [t for t in vectors if t is not None]
+    low = 0
     for t in ts:
-        if not t.is_cuda or not t.is_contiguous():
-            _dev(t)
-        if t.data_ptr() & 15:
-            raise ValueError(f"a tensor of shape {list(t.shape)} does not start at a 16-byte boundary")
-    for t in others:
-        if t is not None:
-            if not t.is_cuda or not t.is_contiguous():
-                _dev(t)
-            ts.append(t)
-    return _place(stream, ts)
+        low |= t.data_ptr()
+    n = len(ts)
+    ts += [t for t in others if t is not None]
+    if not all(map(_torch().Tensor.is_contiguous, ts)):
+        _dev(*ts)
+    placed = _place(stream, ts)
+    if low & 15:
+        bad = next(t for t in ts[:n] if t.data_ptr() & 15)
+        raise ValueError(f"a tensor of shape {list(bad.shape)} does not start at a 16-byte boundary")
+    return placed
 
 
 def _addr(t):
@@ -774,18 +778,25 @@ def layer_backward(x, w_gate_up, w_down, fwd: dict, d_out, k: int, e_begin: int,
 
 # ----------------------------------------------------------------------------- residual add and layer norm
 
-def _norm_params(x, weight, bias, name_d: int):
-    torch = _torch()
-    _want(weight, "weight", (x.dtype, torch.float32), (name_d,))
-    if bias is not None:
-        _want(bias, "bias", weight.dtype, (name_d,))
-
-
 def _rows(x, name: str):
-    _want(x, name, _act_dtypes())
-    if x.dim() != 2:
-        raise ValueError(f"{name} must be [T, d], got {list(x.shape)}")
-    return int(x.shape[0]), int(x.shape[1])
+    if x.dtype not in _CODES:
+        _want(x, name, _act_dtypes())
+    size = x.shape
+    if len(size) != 2:
+        raise ValueError(f"{name} must be [T, d], got {list(size)}")
+    return size
+
+
+def _like(t, name: str, dtype, size):
+    """_want of a tensor that may be left out (None)."""
+    if t is not None and (t.dtype is not dtype or t.shape != size):
+        _want(t, name, dtype, tuple(size))
+
+
+def _norm_params(x, weight, bias, d: int):
+    if weight.dtype is not x.dtype or weight.shape != (d,):
+        _want(weight, "weight", (x.dtype, _torch().float32), (d,))
+    _like(bias, "bias", weight.dtype, (d,))
 
 
 def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s=None, mean=None, rstd=None,
@@ -794,18 +805,15 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s
     y = (s - mean) * rstd * weight + bias, with fp32 statistics [T]. weight and
     bias [d] are of x's dtype or fp32. y may be x or residual, and so may s."""
     torch = _torch()
-    T, d = _rows(x, "x")
+    T, d = size = _rows(x, "x")
     _norm_params(x, weight, bias, d)
-    if residual is not None:
-        _want(residual, "residual", x.dtype, (T, d))
-    elif s is not None:
+    if residual is None and s is not None:
         raise ValueError("s is written only with a residual")
-    for name, t in (("y", y), ("s", s)):
-        if t is not None:
-            _want(t, name, x.dtype, (T, d))
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t is not None:
-            _want(t, name, torch.float32, (T,))
+    _like(residual, "residual", x.dtype, size)
+    _like(y, "y", x.dtype, size)
+    _like(s, "s", x.dtype, size)
+    _like(mean, "mean", torch.float32, (T,))
+    _like(rstd, "rstd", torch.float32, (T,))
     h, ctx = _ready(stream, (x, weight, bias, residual, y, s), (mean, rstd))
     sh = moe_shape(T, d, 8, 1, 1, 0, 1)
     with ctx:
@@ -817,8 +825,8 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s
             mean = torch.empty(T, dtype=torch.float32, device=x.device)
         if rstd is None:
             rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-        _check(_load().moe_layer_norm(ctypes.byref(sh), _dtype_code(x), x.data_ptr(), _addr(residual),
-                                      _dtype_code(weight), weight.data_ptr(), _addr(bias), eps, y.data_ptr(), _addr(s),
+        _check(_load().moe_layer_norm(ctypes.byref(sh), _CODES[x.dtype], x.data_ptr(), _addr(residual),
+                                      _CODES[weight.dtype], weight.data_ptr(), _addr(bias), eps, y.data_ptr(), _addr(s),
                                       mean.data_ptr(), rstd.data_ptr(), h), "moe_layer_norm")
     return y, x if residual is None else s, mean, rstd
 
@@ -834,17 +842,17 @@ def layer_norm_backward(d_y, s, weight, mean, rstd, d_s=None, bias: bool = True,
     mean and rstd. d_s, the gradient that reaches s on other ways, is added to
     d_x. Without `bias`, d_bias is None. d_x may be d_y or d_s."""
     torch = _torch()
-    T, d = _rows(d_y, "d_y")
-    _want(s, "s", d_y.dtype, (T, d))
+    T, d = size = _rows(d_y, "d_y")
+    if s is None or mean is None or rstd is None:
+        raise ValueError("s, mean and rstd of the forward are required")
+    _like(s, "s", d_y.dtype, size)
     _norm_params(d_y, weight, None, d)
-    _want(mean, "mean", torch.float32, (T,))
-    _want(rstd, "rstd", torch.float32, (T,))
-    for name, t in (("d_s", d_s), ("d_x", d_x)):
-        if t is not None:
-            _want(t, name, d_y.dtype, (T, d))
-    for name, t in (("d_weight", d_weight), ("d_bias", d_bias)):
-        if t is not None:
-            _want(t, name, weight.dtype, (d,))
+    _like(mean, "mean", torch.float32, (T,))
+    _like(rstd, "rstd", torch.float32, (T,))
+    _like(d_s, "d_s", d_y.dtype, size)
+    _like(d_x, "d_x", d_y.dtype, size)
+    _like(d_weight, "d_weight", weight.dtype, (d,))
+    _like(d_bias, "d_bias", weight.dtype, (d,))
     if d_bias is not None and not bias:
         raise ValueError("d_bias is written only with bias")
     sh = moe_shape(T, d, 8, 1, 1, 0, 1)
@@ -863,8 +871,8 @@ def layer_norm_backward(d_y, s, weight, mean, rstd, d_s=None, bias: bool = True,
             d_bias = torch.empty_like(weight)
         if workspace is None and ws_bytes:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=d_y.device)
-        _check(_load().moe_layer_norm_backward(ctypes.byref(sh), _dtype_code(d_y), d_y.data_ptr(), s.data_ptr(),
-                                               _dtype_code(weight), weight.data_ptr(), mean.data_ptr(),
+        _check(_load().moe_layer_norm_backward(ctypes.byref(sh), _CODES[d_y.dtype], d_y.data_ptr(), s.data_ptr(),
+                                               _CODES[weight.dtype], weight.data_ptr(), mean.data_ptr(),
                                                rstd.data_ptr(), _addr(d_s), d_x.data_ptr(), d_weight.data_ptr(),
                                                _addr(d_bias), _addr(workspace), h), "moe_layer_norm_backward")
     return d_x, d_weight, d_bias
@@ -895,10 +903,12 @@ def _want_int8_experts(experts: Int8Experts, d: int, e_loc: int) -> int:
     _want(sc, "gate_up_scale", torch.float32)
     if sc.dim() != 2 or sc.shape[0] != e_loc or sc.shape[1] % 2:
         raise ValueError(f"gate_up_scale must be [{e_loc}, 2 * d_ff], got {list(sc.shape)}")
-    d_ff = int(sc.shape[1]) // 2
-    _want(experts.w_gate_up, "w_gate_up", torch.int8, (e_loc, _kblocks(d), 2 * d_ff, 64))
-    _want(experts.w_down, "w_down", torch.int8, (e_loc, _kblocks(d_ff), d, 64))
-    _want(experts.down_scale, "down_scale", torch.float32, (e_loc, d))
+    d_ff = sc.shape[1] // 2
+    for t, name, dtype, size in ((experts.w_gate_up, "w_gate_up", torch.int8, (e_loc, _kblocks(d), 2 * d_ff, 64)),
+                                 (experts.w_down, "w_down", torch.int8, (e_loc, _kblocks(d_ff), d, 64)),
+                                 (experts.down_scale, "down_scale", torch.float32, (e_loc, d))):
+        if t is None or t.dtype is not dtype or t.shape != size:
+            _want(t, name, dtype, size)
     return d_ff
 
 
@@ -996,9 +1006,8 @@ def _tensor_list(ts, name: str):
     ts = list(ts)
     if not ts:
         raise ValueError(f"{name} is empty")
-    codes = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
     try:
-        kinds = [codes[t.dtype] for t in ts]
+        kinds = [_CODES[t.dtype] for t in ts]
     except KeyError:
         for i, t in enumerate(ts):
             _want(t, f"{name}[{i}]", _act_dtypes())
@@ -1018,7 +1027,7 @@ def _host_list(ts, numels, kinds):
 def _list_ready(stream, ts, *others):
     """_place for a list of gradients (aligned to their elements only) and its buffers."""
     all_ = ts + [t for t in others if t is not None]
-    if min(map(_torch().Tensor.get_device, all_)) < 0 or not all(map(_torch().Tensor.is_contiguous, all_)):
+    if not all(map(_torch().Tensor.is_contiguous, all_)):
         _dev(*all_)
     return _place(stream, all_)
 
