@@ -40,6 +40,7 @@ import moe_inputs as mi  # noqa: E402
 METRIC = "routed tokens/sec per MoE layer fwd on 1 MI355X; grouped-GEMM % MFMA peak"
 PEAK_BF16_TFLOPS = 2500.0   # MI355X dense bf16 MFMA
 PEAK_FP32_TFLOPS = 157.3    # MI355X fp32 vector
+PEAK_INT8_TOPS = 5000.0     # MI355X dense int8 MFMA
 PEAK_HBM_GBS = 8000.0
 # Sources that decide the grouped GEMM's machine code; a stored traffic figure is
 # reported only while they are unchanged since its counters were taken.
@@ -169,6 +170,11 @@ def main() -> int:
     ap.add_argument("--train", action="store_true",
                     help="a step is the forward and then the backward of the layer (seeded d_out); the "
                          "roofline object then covers moe_grouped_gemm_backward")
+    ap.add_argument("--int8", action="store_true",
+                    help="serve with the experts in 8-bit integers (quantised once, untimed; bf16 workloads): the "
+                         "step's grouped GEMM is moe_grouped_gemm_int8, the quantisation of its rows included")
+    ap.add_argument("--clip-norm", type=float, default=0.0,
+                    help="with --train: a step ends with clip_grad_norm of the weight gradients to this norm")
     ap.add_argument("--graph", action="store_true",
                     help="record one step in a HIP graph and time graph replays (the GEMM roofline "
                          "then comes from an eager pass after the timed replays)")
@@ -252,8 +258,23 @@ def main() -> int:
 
     gu = None  # training: the gate/up pre-activations the forward keeps for the backward
 
+    experts = ws8 = None
+    if args.int8:
+        if w.dtype != "bf16" or not fused or args.train:
+            print("--int8 runs the fused bf16 forward", file=sys.stderr)
+            return 2
+        experts = moe.quantize_experts(dgu, ddn)
+        ws8 = torch.empty(moe.grouped_gemm_int8_workspace_bytes(w.T, w.d, w.d_ff, w.E, w.k, w.e_begin, w.e_end),
+                          dtype=torch.uint8, device=dev)
+    if args.clip_norm > 0 and not args.train:
+        print("--clip-norm needs --train", file=sys.stderr)
+        return 2
+
     def gemm():
-        if fused:
+        if args.int8:
+            moe.grouped_gemm_int8(dx, disp.perm, disp.offsets, experts, w.k, w.E, w.e_begin, w.e_end, y=y,
+                                  workspace=ws8, stream=cur())
+        elif fused:
             moe.grouped_gemm_gather(dx, disp.perm, disp.offsets, dgu, ddn, w.k, w.E, w.e_begin, w.e_end,
                                     h=h, y=y, stream=cur(), gu=gu)
         else:
@@ -301,6 +322,11 @@ def main() -> int:
             ("route_topk_backward", lambda: moe.route_topk_backward(idx, wts, d_w, w.E, d_logits=d_logits,
                                                                     stream=cur())),
         ]
+        if args.clip_norm > 0:
+            norm = torch.empty(1, dtype=torch.float32, device=dev)
+            ws_norm = torch.empty(moe.grad_norm_workspace_bytes(2), dtype=torch.uint8, device=dev)
+            calls.append(("clip_grad_norm", lambda: moe.clip_grad_norm([d_wgu, d_wdn], args.clip_norm, norm=norm,
+                                                                       workspace=ws_norm, stream=cur())))
     timed = "grouped_gemm_backward" if train else "grouped_gemm"  # the roofline's kernel
 
     def step(i=None):
@@ -380,7 +406,9 @@ def main() -> int:
         gemm_bytes = 6.0 * active * w.d * w.d_ff * b + n_loc * (6.0 * w.d + 9.0 * w.d_ff) * b
     else:
         gemm_bytes = 3.0 * active * w.d * w.d_ff * b + 2.0 * n_loc * (w.d + w.d_ff) * b
-    peak_flops = PEAK_BF16_TFLOPS if w.dtype == "bf16" else PEAK_FP32_TFLOPS
+    if args.int8:  # one byte per weight and an fp32 scale per channel; x's rows read, y written
+        gemm_bytes = active * (3.0 * w.d * w.d_ff + 4.0 * (w.d + 2 * w.d_ff)) + 2.0 * n_loc * w.d * b
+    peak_flops = PEAK_INT8_TOPS if args.int8 else PEAK_BF16_TFLOPS if w.dtype == "bf16" else PEAK_FP32_TFLOPS
     t_gemm = gemm_ms * 1e-3
     # the bound is whichever of MFMA time and HBM time is longer at peak
     if w.dtype == "bf16" and gemm_bytes / (PEAK_HBM_GBS * 1e9) > flops / (peak_flops * 1e12):
@@ -389,7 +417,8 @@ def main() -> int:
         bound = "mfma" if w.dtype == "bf16" else "alu"
         achieved, peak, unit = flops / t_gemm / 1e12, peak_flops, "TFLOP/s"
     roofline = {
-        "kernel": ("moe_grouped_gemm_backward_saved (row gather, blocked copy of dY, dH+SwiGLU "
+        "kernel": "moe_grouped_gemm_int8 (rows quantised, gate/up+SwiGLU, h quantised, down)" if args.int8 else
+                  ("moe_grouped_gemm_backward_saved (row gather, blocked copy of dY, dH+SwiGLU "
                    "backward, dX, dW_down, dW_gate_up launches; gate/up pre-activations kept by "
                    "the forward)" if train else
                    ("moe_grouped_gemm_gather" if fused else "moe_grouped_gemm")
@@ -400,7 +429,7 @@ def main() -> int:
         "peak": peak,
         "unit": unit,
         "frac": round(achieved / peak, 4),
-        "traffic": None if train else stored_traffic(w.name),
+        "traffic": None if train or args.int8 else stored_traffic(w.name),
         "flops_per_launch": flops,
         "algorithmic_bytes_per_launch": gemm_bytes,
         "median_ms": round(gemm_ms, 4),
@@ -418,13 +447,14 @@ def main() -> int:
         "higher_is_better": True,
         "scaling": "weak",
         "vs_baseline": None,
-        "dtype": w.dtype,
+        "dtype": "int8" if args.int8 else w.dtype,
         "data": "synthetic (seeded normal draws; see moe_inputs)",
         "config": {"workload": w.name, "T": w.T, "d": w.d, "d_ff": w.d_ff, "E": w.E, "k": w.k,
                    "local_experts": [w.e_begin, w.e_end], "N_loc": n_loc, "active_local_experts": active,
                    "parallelism": "one rank's share on 1 GPU", "path": "fused" if fused else "staged",
                    "launch": "hip graph" if args.graph else "eager",
-                   "step": "forward + backward" if args.train else "forward"},
+                   "step": ("forward + backward" + (" + clip" if args.clip_norm > 0 else "")) if args.train
+                           else "forward, int8 experts" if args.int8 else "forward"},
         "local_pairs_per_s": round(n_loc / (ms_step * 1e-3), 1),
         "timing": {"per_step": f"median of {args.steps} per-step event times, each step after a "
                                f"{args.flush_mib} MiB flush ({args.flush_mode}) outside its events",
