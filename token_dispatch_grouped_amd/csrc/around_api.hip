@@ -36,10 +36,18 @@ moe_status check_norm(const moe_shape* s, moe_dtype dt, moe_dtype wdt) {
 
 // ------------------------------------------------------------------------ int8
 
+int64_t n_max_of(const moe_shape* s) {
+  const int64_t e_loc = s->e_end - s->e_begin;
+  return s->T * (s->k < e_loc ? s->k : e_loc);
+}
+
 // The parts of the int8 workspace, each 256-byte aligned.
 struct Int8Workspace {
   size_t xq, xs, h, hq, hs, plan, bytes;
-  Int8Workspace(int64_t n_max, int e_loc, int d, int d_ff) {
+  int tile_rows;
+  explicit Int8Workspace(const moe_shape* s) {
+    const int64_t n_max = n_max_of(s);
+    const int e_loc = s->e_end - s->e_begin, d = s->d, d_ff = s->d_ff;
     const size_t n = static_cast<size_t>(n_max);
     size_t at = 0;
     auto part = [&](size_t b) {
@@ -52,6 +60,7 @@ struct Int8Workspace {
     h = part(n * static_cast<size_t>(d_ff) * 2);
     hq = part(n * moe::int8_kblocks(d_ff) * 64);
     hs = part(n * sizeof(float));
+    tile_rows = moe::int8_tile_rows(s->T, s->k, s->E, e_loc, d, d_ff);
     plan = part(n > 0 ? moe::int8_plan_bytes(n_max, e_loc) : 0);
     bytes = at;
   }
@@ -73,11 +82,6 @@ moe_status check_int8(const moe_shape* s) {
   if (s->T < 0 || s->k < 1 || s->k > s->E) return MOE_EINVAL;
   if (s->T * static_cast<int64_t>(s->k) > INT32_MAX) return MOE_EINVAL;
   return MOE_OK;
-}
-
-int64_t n_max_of(const moe_shape* s) {
-  const int64_t e_loc = s->e_end - s->e_begin;
-  return s->T * (s->k < e_loc ? s->k : e_loc);
 }
 
 // ------------------------------------------------------------------- gradients
@@ -200,7 +204,7 @@ moe_status moe_quantize_experts(const moe_shape* s, moe_dtype dt, const void* w_
 
 size_t moe_grouped_gemm_int8_workspace_bytes(const moe_shape* s) {
   if (check_int8(s) != MOE_OK) return 0;
-  return Int8Workspace(n_max_of(s), s->e_end - s->e_begin, s->d, s->d_ff).bytes;
+  return Int8Workspace(s).bytes;
 }
 
 moe_status moe_grouped_gemm_int8(const moe_shape* s, moe_dtype dt, const void* x, const int32_t* perm,
@@ -220,7 +224,7 @@ moe_status moe_grouped_gemm_int8(const moe_shape* s, moe_dtype dt, const void* x
     return MOE_EINVAL;
   const int64_t n_max = n_max_of(s);
   const int e_loc = s->e_end - s->e_begin, d = s->d, d_ff = s->d_ff;
-  const Int8Workspace ws(n_max, e_loc, d, d_ff);
+  const Int8Workspace ws(s);
   char* p = static_cast<char*>(workspace);
   float* xs = reinterpret_cast<float*>(p + ws.xs);
   float* hs = reinterpret_cast<float*>(p + ws.hs);
@@ -228,16 +232,16 @@ moe_status moe_grouped_gemm_int8(const moe_shape* s, moe_dtype dt, const void* x
     return from_hip(moe::launch_int8_few(x, perm, offsets, q_gate_up, scale_gate_up, q_down, scale_down, p + ws.h, y, d,
                                          d_ff, s->e_begin, e_loc, s->k, s->T, n_max, stream));
   hipError_t e = moe::launch_quantize_rows(x, perm, offsets, p + ws.xq, xs, s->e_begin, s->e_end, s->k, s->T, d, n_max,
-                                           p + ws.plan, stream);
+                                           p + ws.plan, ws.tile_rows, stream);
   if (e == hipSuccess)
-    e = moe::launch_grouped_gemm_int8(p + ws.xq, xs, q_gate_up, scale_gate_up, p + ws.h, p + ws.plan, e_loc, d, d_ff, n_max,
-                                      true, stream);
+    e = moe::launch_grouped_gemm_int8(p + ws.xq, xs, q_gate_up, scale_gate_up, p + ws.h, p + ws.plan, ws.tile_rows, e_loc, d,
+                                      d_ff, n_max, true, stream);
   if (e == hipSuccess)
     e = moe::launch_quantize_rows(p + ws.h, nullptr, offsets, p + ws.hq, hs, s->e_begin, s->e_end, s->k, s->T, d_ff,
-                                  n_max, nullptr, stream);
+                                  n_max, nullptr, 0, stream);
   if (e == hipSuccess)
-    e = moe::launch_grouped_gemm_int8(p + ws.hq, hs, q_down, scale_down, y, p + ws.plan, e_loc, d_ff, d, n_max, false,
-                                      stream);
+    e = moe::launch_grouped_gemm_int8(p + ws.hq, hs, q_down, scale_down, y, p + ws.plan, ws.tile_rows, e_loc, d_ff, d,
+                                      n_max, false, stream);
   return from_hip(e);
 }
 

@@ -15,7 +15,7 @@
 // The order of K inside a fragment is free as long as A and B agree; both take the
 // bytes 16 * (lane / 32) .. + 15 of a 32-byte slice.
 //
-// Two shapes of workgroup:
+// Two shapes of workgroup (int8_tile_rows says when; a third, for few rows, is in int8_few.hip):
 //   tall   BM = 256 (288 where a remainder of up to 32 rows rides along), one workgroup
 //          per CU with all of its LDS: five stages (four with 288 rows). For experts with
 //          many rows: each byte brought to a CU is used by the most products.
@@ -432,11 +432,13 @@ __global__ __launch_bounds__(kThreads, TALL ? 1 : 2) void grouped_gemm_int8_kern
 }  // namespace
 
 hipError_t launch_grouped_gemm_int8(const void* a, const float* a_scale, const void* w, const float* w_scale, void* c,
-                                    const void* plan, int e_loc, int K, int N, int64_t n_max, bool swiglu,
-                                    hipStream_t stream) {
-  const bool tall = int8_tall(n_max, e_loc);
+                                    const void* plan, int tile_rows, int e_loc, int K, int N, int64_t n_max,
+                                    bool swiglu, hipStream_t stream) {
+  if (tile_rows == int8::kThinRows)
+    return launch_int8_thin(a, a_scale, w, w_scale, c, plan, e_loc, K, N, n_max, swiglu, stream);
+  const bool tall = tile_rows == int8::kTallRows;
   const int cols = swiglu ? 128 : 256;
-  const int64_t tiles = int8::max_row_tiles(n_max, e_loc, tall) * ((N + cols - 1) / cols);
+  const int64_t tiles = int8::max_row_tiles(n_max, e_loc, tile_rows) * ((N + cols - 1) / cols);
   const int slots = device_cu_count() * (tall ? 1 : 2);
   const unsigned grid = static_cast<unsigned>(tiles < slots ? (tiles + 7) / 8 * 8 : slots);
   const int kblocks = int8_kblocks(K);

@@ -14,7 +14,7 @@
 // contiguous KB, lane L's 16 bytes at (L & 15) * 64 + (L >> 4) * 16. Integer sums are
 // exact, so the quarters of K are joined in any order with the same bits.
 #include "int8_code.h"
-#include "gemm_common.h"
+#include "int8_plan.h"
 
 namespace moe {
 namespace {
@@ -32,7 +32,73 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 __host__ __device__ constexpr int code_stride(int kblocks) { return kblocks * 64 + 16; }  // rows fall into different banks
 
 // FRAGS 16-channel blocks of a workgroup (SwiGLU: half gate, half up), AHEAD K-blocks that
-// a wave has in flight; three waves per SIMD.
+// a wave has in flight.
+template <bool SWIGLU, int FRAGS, int AHEAD>
+struct Weights {
+  static constexpr int NO = SWIGLU ? FRAGS / 2 : FRAGS;  // blocks of output columns
+  const uint8_t* base;  // the expert's
+  int64_t block_bytes;  // of one K-block
+  int lo, hi;           // this wave's K-blocks, a quarter of all
+  uint32_t off[FRAGS];
+  i32x4 b[AHEAD][FRAGS];
+
+  __device__ Weights(const uint8_t* w, int e, int n0, int kblocks, int N) {
+    const int lane = lane_id(), wv = uniform(static_cast<int>(threadIdx.x) / kWave);
+    const int64_t channels = SWIGLU ? 2 * static_cast<int64_t>(N) : N;
+    block_bytes = channels * 64;
+    base = w + e * block_bytes * kblocks;
+    lo = kblocks * wv / kWaves;
+    hi = kblocks * (wv + 1) / kWaves;
+#pragma unroll
+    for (int f = 0; f < FRAGS; ++f) {
+      const int col = min(n0 + 16 * (f % NO) + (lane & 15), N - 1);  // channels past N are read again and not stored
+      off[f] = static_cast<uint32_t>(col + (f >= NO ? N : 0)) * 64u + static_cast<uint32_t>(lane >> 4) * 16u;
+    }
+  }
+  __device__ void load(int kb0) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (kb0 + u < hi) {
+        const uint8_t* p = base + (kb0 + u) * block_bytes;
+#pragma unroll
+        for (int f = 0; f < FRAGS; ++f) b[u][f] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p + off[f]));
+      }
+  }
+};
+
+// The four quarters of K joined, scaled and stored: `rows` rows from row r0 of `out`.
+// part: [wave][RT * FRAGS][lane], lane l's element j of a block is row (l >> 4) * 4 + j,
+// channel l & 15; a thread takes one element of every block.
+template <bool SWIGLU, int FRAGS, int RT>
+__device__ __forceinline__ void finish(const i32x4* part, const float* row_scale, const float* __restrict__ w_scale,
+                                       __bf16* __restrict__ out, int64_t r0, int rows, int n0, int N) {
+  constexpr int NO = SWIGLU ? FRAGS / 2 : FRAGS;
+  const int lane = lane_id(), j = static_cast<int>(threadIdx.x) / kWave;
+  auto sum = [&](int t, int f) {
+    int s = 0;
+#pragma unroll
+    for (int q = 0; q < kWaves; ++q)
+      s += reinterpret_cast<const int*>(part)[(((q * RT + t) * FRAGS + f) * kWave + lane) * 4 + j];
+    return static_cast<float>(s);
+  };
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int row = t * 16 + (lane >> 4) * 4 + j;
+    if (row >= rows) continue;
+    const float sa = row_scale[row];
+#pragma unroll
+    for (int f = 0; f < NO; ++f) {
+      const int col = n0 + 16 * f + (lane & 15);
+      if (col < N) {
+        float v = sum(t, f) * w_scale[col] * sa;
+        if constexpr (SWIGLU) v = gemm::silu_fast(v) * (sum(t, f + NO) * w_scale[N + col] * sa);
+        out[(r0 + row) * N + col] = static_cast<__bf16>(v);
+      }
+    }
+  }
+}
+
+// A few tokens: the workgroup quantises its rows. Three waves per SIMD.
 template <bool SWIGLU, int FRAGS, int AHEAD>
 __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
     const uint4* __restrict__ src, const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets,
@@ -42,7 +108,7 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
   __shared__ i32x4 part[kWaves * FRAGS * kWave];
   __shared__ float scales[kRows];
   __shared__ uint32_t tops[2][kWaves];
-  constexpr int NO = SWIGLU ? FRAGS / 2 : FRAGS;
+  using Wt = Weights<SWIGLU, FRAGS, AHEAD>;
   const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid / kWave);
   const int e = blockIdx.y;
   const int seg0 = offsets[e_begin];
@@ -51,31 +117,10 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
   const int r0 = start + static_cast<int>(blockIdx.z) * kRows;
   if (r0 >= end) return;
   const int R = min(kRows, end - r0);
-  const int n0 = static_cast<int>(blockIdx.x) * 16 * NO;
-  const int64_t channels = SWIGLU ? 2 * static_cast<int64_t>(N) : N;
-  const uint8_t* we = w + e * channels * kblocks * 64;
-
-  // this wave's quarter of K, its first weights in flight
-  const int lo = kblocks * wv / kWaves, hi = kblocks * (wv + 1) / kWaves;
-  uint32_t off[FRAGS];
-#pragma unroll
-  for (int f = 0; f < FRAGS; ++f) {
-    const int col = min(n0 + 16 * (f % NO) + (lane & 15), N - 1);  // channels past N are read again and not stored
-    off[f] = static_cast<uint32_t>(col + (f >= NO ? N : 0)) * 64u + static_cast<uint32_t>(lane >> 4) * 16u;
-  }
-  i32x4 b[AHEAD][FRAGS];
-  auto load = [&](int kb0) {
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u)
-      if (kb0 + u < hi) {
-        const uint8_t* p = we + (kb0 + u) * channels * 64;
-#pragma unroll
-        for (int f = 0; f < FRAGS; ++f)
-          b[u][f] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p + off[f]));
-      }
-  };
-  load(lo);
-  __builtin_amdgcn_sched_barrier(0);
+  const int n0 = static_cast<int>(blockIdx.x) * 16 * Wt::NO;
+  Wt wt(w, e, n0, kblocks, N);
+  wt.load(wt.lo);
+  __builtin_amdgcn_sched_barrier(0);  // in flight before anything else
 
   // the rows' codes, a row at a time by all threads
   const int stride = code_stride(kblocks);
@@ -119,41 +164,82 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
   i32x4 acc[FRAGS];
 #pragma unroll
   for (int f = 0; f < FRAGS; ++f) acc[f] = i32x4{0, 0, 0, 0};
-  for (int kb0 = lo; kb0 < hi; kb0 += AHEAD) {
+  for (int kb0 = wt.lo; kb0 < wt.hi; kb0 += AHEAD) {
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
-      if (kb0 + u < hi) {
+      if (kb0 + u < wt.hi) {
         const i32x4 a = *reinterpret_cast<const i32x4*>(mine + (kb0 + u) * 64);
 #pragma unroll
-        for (int f = 0; f < FRAGS; ++f) acc[f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b[u][f], acc[f], 0, 0, 0);
+        for (int f = 0; f < FRAGS; ++f)
+          acc[f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, wt.b[u][f], acc[f], 0, 0, 0);
       }
-    if (kb0 + AHEAD < hi) load(kb0 + AHEAD);
+    if (kb0 + AHEAD < wt.hi) wt.load(kb0 + AHEAD);
   }
 #pragma unroll
   for (int f = 0; f < FRAGS; ++f) part[(wv * FRAGS + f) * kWave + lane] = acc[f];
   __syncthreads();
+  finish<SWIGLU, FRAGS, 1>(part, scales, w_scale + e * (wt.block_bytes / 64), out, r0, R, n0, N);
+}
 
-  // a thread per element of a 16 x 16 block: lane l's element j of a block is row (l >> 4) * 4 + j, channel l & 15
-  const int j = wv, row = (lane >> 4) * 4 + j;
-  auto sum = [&](int f) {
-    int s = 0;
+// Up to 32 rows of an expert whose codes are there already: as above, the rows' codes
+// loaded like the weights (a K-block of 16 rows is one contiguous KB as well).
+template <bool SWIGLU, int FRAGS, int AHEAD>
+__global__ __launch_bounds__(kThreads, 3) void int8_thin_kernel(
+    const uint8_t* __restrict__ codes, const float* __restrict__ a_scale, const uint8_t* __restrict__ w,
+    const float* __restrict__ w_scale, __bf16* __restrict__ out, const int* __restrict__ n_row_tiles,
+    const RowGroup* __restrict__ groups, int kblocks, int N, int64_t n_max) {
+  constexpr int RT = kThinRows / 16;
+  __shared__ i32x4 part[kWaves * RT * FRAGS * kWave];
+  __shared__ float scales[kThinRows];
+  using Wt = Weights<SWIGLU, FRAGS, AHEAD>;
+  if (static_cast<int>(blockIdx.y) >= *n_row_tiles) return;
+  const RowGroup g = groups[blockIdx.y];
+  const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid / kWave);
+  const int r0 = g.row0 + g.index * kThinRows;
+  const int R = min(kThinRows, g.row_end - r0);
+  const int n0 = static_cast<int>(blockIdx.x) * 16 * Wt::NO;
+  Wt wt(w, g.expert, n0, kblocks, N);
+  uint32_t off[RT];
 #pragma unroll
-    for (int q = 0; q < kWaves; ++q) s += reinterpret_cast<const int*>(part)[((q * FRAGS + f) * kWave + lane) * 4 + j];
-    return static_cast<float>(s);
-  };
-  if (row < R) {
-    const float* se = w_scale + e * channels;
-    const float sa = scales[row];
+  for (int t = 0; t < RT; ++t)
+    off[t] = static_cast<uint32_t>(min(16 * t + (lane & 15), R - 1)) * 64u + static_cast<uint32_t>(lane >> 4) * 16u;
+  const uint8_t* rows0 = codes + static_cast<int64_t>(r0) * 64;
+  i32x4 a[AHEAD][RT];
+  auto load = [&](int kb0) {
 #pragma unroll
-    for (int f = 0; f < NO; ++f) {
-      const int col = n0 + 16 * f + (lane & 15);
-      if (col < N) {
-        float v = sum(f) * se[col] * sa;
-        if constexpr (SWIGLU) v = gemm::silu_fast(v) * (sum(f + NO) * se[N + col] * sa);
-        out[static_cast<int64_t>(r0 + row) * N + col] = static_cast<__bf16>(v);
+    for (int u = 0; u < AHEAD; ++u)
+      if (kb0 + u < wt.hi) {
+        const uint8_t* p = rows0 + (kb0 + u) * n_max * 64;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) a[u][t] = *reinterpret_cast<const i32x4*>(p + off[t]);
       }
-    }
+    wt.load(kb0);
+  };
+  load(wt.lo);
+  if (tid < R) scales[tid] = a_scale[r0 + tid];
+  i32x4 acc[RT][FRAGS];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int f = 0; f < FRAGS; ++f) acc[t][f] = i32x4{0, 0, 0, 0};
+  for (int kb0 = wt.lo; kb0 < wt.hi; kb0 += AHEAD) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (kb0 + u < wt.hi) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int f = 0; f < FRAGS; ++f)
+            acc[t][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][t], wt.b[u][f], acc[t][f], 0, 0, 0);
+      }
+    if (kb0 + AHEAD < wt.hi) load(kb0 + AHEAD);
   }
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int f = 0; f < FRAGS; ++f) part[((wv * RT + t) * FRAGS + f) * kWave + lane] = acc[t][f];
+  __syncthreads();
+  finish<SWIGLU, FRAGS, RT>(part, scales, w_scale + g.expert * (wt.block_bytes / 64), out, r0, R, n0, N);
 }
 
 template <bool SWIGLU, int FRAGS, int AHEAD>
@@ -206,6 +292,25 @@ hipError_t launch_int8_few(const void* x, const int32_t* perm, const int32_t* of
       launch_product<true>(x, perm, offsets, q_gu, s_gu, h, e_begin, e_loc, k, T, d, d_ff, n_max, stream);
   if (e != hipSuccess) return e;
   return launch_product<false>(h, nullptr, offsets, q_dn, s_dn, y, e_begin, e_loc, k, T, d_ff, d, n_max, stream);
+}
+
+hipError_t launch_int8_thin(const void* a, const float* a_scale, const void* w, const float* w_scale, void* c,
+                            const void* plan, int e_loc, int K, int N, int64_t n_max, bool swiglu, hipStream_t stream) {
+  const int* count = static_cast<const int*>(plan);
+  const int8::RowGroup* groups =
+      reinterpret_cast<const int8::RowGroup*>(static_cast<const char*>(plan) + int8::kPlanHeader);
+  const unsigned tiles = static_cast<unsigned>(int8::max_row_tiles(n_max, e_loc, int8::kThinRows));
+  const int kblocks = int8_kblocks(K);
+#define MOE_THIN(S, F, A)                                                                                         \
+  hipLaunchKernelGGL((int8_thin_kernel<S, F, A>),                                                                 \
+                     dim3(static_cast<unsigned>((N + 16 * (S ? F / 2 : F) - 1) / (16 * (S ? F / 2 : F))), tiles), \
+                     dim3(kThreads), 0, stream, static_cast<const uint8_t*>(a), a_scale,                          \
+                     static_cast<const uint8_t*>(w), w_scale, static_cast<__bf16*>(c), count, groups, kblocks, N, \
+                     n_max)
+  if (swiglu) MOE_THIN(true, 4, 3);
+  else MOE_THIN(false, 4, 3);
+#undef MOE_THIN
+  return hipGetLastError();
 }
 
 }  // namespace moe

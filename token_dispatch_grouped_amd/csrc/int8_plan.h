@@ -9,6 +9,7 @@ namespace int8 {
 
 constexpr int kTallRows = 256, kTallMerge = 32;  // a remainder of up to 32 rows rides on the last tile
 constexpr int kShortRows = 128;
+constexpr int kThinRows = 32;
 constexpr int kGroup = 4;  // row tiles of an expert that are walked together
 
 // One entry per row tile; entries of an expert are consecutive, in groups of up to
@@ -27,12 +28,8 @@ static_assert(sizeof(RowGroup) == 16, "one 16-byte load");
 
 constexpr size_t kPlanHeader = 256;  // two ints: how many entries, and how many are of experts with more than 128 rows
 
-inline int64_t max_row_tiles(int64_t n_max, int e_loc, bool tall) {
-  return n_max / (tall ? kTallRows : kShortRows) + (n_max < e_loc ? n_max : e_loc);
-}
-
-inline size_t plan_bytes(int64_t n_max, int e_loc, bool tall) {
-  return kPlanHeader + static_cast<size_t>(max_row_tiles(n_max, e_loc, tall)) * sizeof(RowGroup);
+inline int64_t max_row_tiles(int64_t n_max, int e_loc, int tile_rows) {
+  return n_max / tile_rows + (n_max < e_loc ? n_max : e_loc);
 }
 
 template <int BM, int MERGE>

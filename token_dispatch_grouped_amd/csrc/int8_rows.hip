@@ -13,6 +13,8 @@
 // of R rows holds [R][64] bytes, columns 64 kb .. 64 kb + 63 of every row, zero
 // past the last column. A K = 64 stage of a tile is then one contiguous run.
 // Everything here is bound by HBM: a row is read once and its codes written once.
+#include <math.h>
+
 #include "int8_code.h"
 #include "int8_plan.h"
 
@@ -33,7 +35,7 @@ template <int G, int VPT>
 __global__ __launch_bounds__(block_threads<G>()) void quantize_rows_kernel(
     const uint4* __restrict__ src, const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets,
     uint8_t* __restrict__ q, float* __restrict__ scale, int e_begin, int e_end, int k, int64_t T, int cols_vec,
-    int kblocks, int64_t n_max, void* __restrict__ plan, int tall) {
+    int kblocks, int64_t n_max, void* __restrict__ plan, int tile_rows) {
   constexpr int kRows = block_threads<G>() / G;
   __shared__ uint32_t lds[2][G > kWave ? G / kWave : 1];
   int turn = 0;
@@ -42,8 +44,9 @@ __global__ __launch_bounds__(block_threads<G>()) void quantize_rows_kernel(
     int* count = static_cast<int*>(plan);
     int8::RowGroup* groups = reinterpret_cast<int8::RowGroup*>(static_cast<char*>(plan) + int8::kPlanHeader);
     const int e_loc = e_end - e_begin, n = static_cast<int>(n_max);
-    if (tall) int8::plan_tiles<int8::kTallRows, int8::kTallMerge>(offsets, e_begin, e_loc, n, count, groups);
-    else int8::plan_tiles<int8::kShortRows, 0>(offsets, e_begin, e_loc, n, count, groups);
+    if (tile_rows == kTallRows) plan_tiles<kTallRows, kTallMerge>(offsets, e_begin, e_loc, n, count, groups);
+    else if (tile_rows == kShortRows) plan_tiles<kShortRows, 0>(offsets, e_begin, e_loc, n, count, groups);
+    else plan_tiles<kThinRows, 0>(offsets, e_begin, e_loc, n, count, groups);
     return;
   }
   const int64_t block = static_cast<int64_t>(blockIdx.x) - planners;
@@ -139,13 +142,13 @@ __global__ __launch_bounds__(256) void quantize_weights_kernel(const void* __res
 
 template <int G, int VPT>
 hipError_t launch_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale, int e_begin,
-                       int e_end, int k, int64_t T, int cols, int64_t n_max, void* plan, hipStream_t stream) {
+                       int e_end, int k, int64_t T, int cols, int64_t n_max, void* plan, int tile_rows, hipStream_t stream) {
   constexpr int kRows = block_threads<G>() / G;
   const int64_t blocks = (n_max + kRows - 1) / kRows;
   hipLaunchKernelGGL((quantize_rows_kernel<G, VPT>), dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536) + (plan != nullptr ? 1u : 0u)),
                      dim3(block_threads<G>()), 0, stream, static_cast<const uint4*>(src), perm, offsets,
                      static_cast<uint8_t*>(q), scale, e_begin, e_end, k, T, cols / 8, (cols + 63) / 64, n_max, plan,
-                     int8_tall(n_max, e_end - e_begin) ? 1 : 0);
+                     tile_rows);
   return hipGetLastError();
 }
 
@@ -155,19 +158,60 @@ int int8_kblocks(int K) { return (K + 63) / 64; }
 
 int64_t int8_max_k() { return 65536; }
 
-// Average rows per local expert from which the tall workgroups pay (2880 x 2880, per
-// call of both products: 16 experts of 128 rows short 97 us, tall 108; of 256 rows
-// short 137, tall 137; 8 experts of 1024 rows at 4096 x 14336 short 1424, tall 1280).
-bool int8_tall(int64_t n_max, int e_loc) { return n_max >= int64_t{192} * e_loc; }
+// Which workgroups a call's products use, from the rows per expert that uniform routing gives
+// (the real counts are on the device only; any choice is right for any counts):
+//
+// thin  (tiles of 32 rows) where the short tiles of a product are too few for the chip, as few
+//       experts with few columns give. Graph replays: 8 experts, 64 tokens x 2, 1024 x 3584:
+//       33.8 us against 41.6; 4 experts, 64 tokens, 4096 x 512: 22.6 against 34.2; but 32 experts,
+//       64 tokens x 4, 1024 x 1024 (128 short tiles): 32.8 against 31.0, and 8 experts, 512 tokens x
+//       2, 1024 x 3584 (128 rows each): 75 against 64.
+// tall  where its rounds cost less than the short ones'. A round of tall tiles on 256 CUs
+//       measured as its K stages + 18 (fill, and the epilogue that nothing overlaps), a round of short
+//       tiles, two per CU, as 1.31 times its stages + 1 (1.5 times the bytes through LDS, but one tile
+//       computes while the other waits); a round that is at most half full costs 0.55. 8 experts of 1024
+//       rows: 4096 x 14336 tall 2718 us (16384 tokens), short 2905; 4096 x 4096 tall 486, short 458;
+//       8 experts of 512 rows 4096 x 4096 tall 233, short 265; 16 of 256 rows 2880 x 2880 tall 164,
+//       short 177; 16 of 1024 rows 1024 x 2048 tall 215, short 173.
+// short otherwise.
+int int8_tile_rows(int64_t T, int k, int E, int e_loc, int d, int d_ff) {
+  const double rows = static_cast<double>(T) * k / E;  // per expert
+  const double experts = rows * e_loc < 1.0 ? 1.0 : rows < 1.0 ? rows * e_loc : e_loc;
+  const double cols[2] = {(d_ff + 127) / 128 * 1.0, (d + 255) / 256 * 1.0};
+  const double stages[2] = {int8_kblocks(d) * 1.0, int8_kblocks(d_ff) * 1.0};
+  const double cus = device_cu_count();
+  const double short_tiles = experts * ceil(rows / kShortRows);
+  const double fewest = fmin(short_tiles * cols[0], short_tiles * cols[1]);
+  const double most = fmax(short_tiles * cols[0], short_tiles * cols[1]);
+  if ((fewest < cus / 4 && rows <= 64) || most < cus / 4) return kThinRows;
+  const double full = floor(rows / kTallRows), rest = rows - full * kTallRows;
+  // a short last tile costs about half of a tall one; one of up to 32 rows rides along
+  const double tall_tiles = experts * fmax(1.0, full + (rest > 128 ? 1.0 : rest > kTallMerge ? 0.5 : 0.0));
+  auto rounds = [](double r) {
+    const double whole = floor(r), part = r - whole;
+    return whole + (part < 0.02 ? 0.0 : part <= 0.5 ? 0.55 : 1.0);
+  };
+  // counts that scatter around their mean leave a few tiles more than it says
+  const double tall_more = experts > 1 && rows > 512 ? 0.3 : 0.0, short_more = 0.1;
+  double tall = 0, shorter = 0;
+  for (int i = 0; i < 2; ++i) {
+    tall += (rounds(tall_tiles * cols[i] / cus) + tall_more) * (stages[i] + 18);
+    shorter += (rounds(short_tiles * cols[i] / (2 * cus)) + short_more) * (1.31 * stages[i] + 1);
+  }
+  return tall <= shorter ? kTallRows : kShortRows;
+}
 
-size_t int8_plan_bytes(int64_t n_max, int e_loc) { return int8::plan_bytes(n_max, e_loc, int8_tall(n_max, e_loc)); }
+// Room for the list of any choice.
+size_t int8_plan_bytes(int64_t n_max, int e_loc) {
+  return kPlanHeader + static_cast<size_t>(max_row_tiles(n_max, e_loc, kThinRows)) * sizeof(RowGroup);
+}
 
 hipError_t launch_quantize_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale,
                                 int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max, void* plan,
-                                hipStream_t stream) {
+                                int tile_rows, hipStream_t stream) {
   const int vec = int8_kblocks(cols) * 8;  // the padded row, in vectors of 8 elements
 #define MOE_QROWS(G, VPT) \
-  return launch_rows<G, VPT>(src, perm, offsets, q, scale, e_begin, e_end, k, T, cols, n_max, plan, stream)
+  return launch_rows<G, VPT>(src, perm, offsets, q, scale, e_begin, e_end, k, T, cols, n_max, plan, tile_rows, stream)
   if (vec <= 64) MOE_QROWS(64, 1);
   if (vec <= 256) MOE_QROWS(64, 4);
   if (vec <= 512) MOE_QROWS(64, 8);

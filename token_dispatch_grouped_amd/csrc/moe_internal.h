@@ -144,19 +144,21 @@ hipError_t launch_layer_norm_backward(const void* dy, const void* s, const void*
 int int8_kblocks(int K);
 int64_t int8_max_k();  // int32 sums of 127 * 127 * K, and rows held in registers
 // the local rows (through perm, or in order with perm == nullptr) as codes and scales; with plan (of
-// int8_plan_bytes), the list of row tiles that launch_grouped_gemm_int8 walks is written there too
-bool int8_tall(int64_t n_max, int e_loc);
+// int8_plan_bytes), the list of row tiles of int8_tile_rows that launch_grouped_gemm_int8 walks is written there too
+int int8_tile_rows(int64_t T, int k, int E, int e_loc, int d, int d_ff);
 size_t int8_plan_bytes(int64_t n_max, int e_loc);
 hipError_t launch_quantize_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale,
                                 int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max, void* plan,
-                                hipStream_t stream);
+                                int tile_rows, hipStream_t stream);
 // [e_loc, K, N] weights as codes [e_loc][int8_kblocks(K)][N][64] and scales [e_loc, N]
 hipError_t launch_quantize_weights(const void* w, void* q, float* scale, int e_loc, int K, int N, bool bf16,
                                    hipStream_t stream);
 // C[rows, N] (bf16) = A @ W_e per local expert, with swiglu silu(gate) * up of W_e's 2 N channels
 hipError_t launch_grouped_gemm_int8(const void* a, const float* a_scale, const void* w, const float* w_scale, void* c,
-                                    const void* plan, int e_loc, int K, int N, int64_t n_max, bool swiglu,
-                                    hipStream_t stream);
+                                    const void* plan, int tile_rows, int e_loc, int K, int N, int64_t n_max,
+                                    bool swiglu, hipStream_t stream);
+hipError_t launch_int8_thin(const void* a, const float* a_scale, const void* w, const float* w_scale, void* c,
+                            const void* plan, int e_loc, int K, int N, int64_t n_max, bool swiglu, hipStream_t stream);
 
 // The same FFN for a few tokens, in two launches that quantise their own rows (h: n_max rows of d_ff, bf16)
 bool int8_few(int64_t T, int k, int E, int d, int d_ff);
