@@ -150,27 +150,37 @@ def test_every_row_count():
     """Expert row counts at the edges of the row tiles, empty experts among them."""
     counts = [0, 1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 289, 0, 513]
     E, T = len(counts), sum(counts)
-    rng = np.random.default_rng(73)
-    owner = np.repeat(np.arange(E), counts)
-    rng.shuffle(owner)
-    logits = rng.standard_normal((T, E)).astype(np.float32)
-    logits[np.arange(T), owner] += 50.0
+    logits = _routed(counts, 73)
     disp, _ = _case(W("i8_rows", T, 256, 160, E, 1, 0, E, "bf16", 73), logits)
     np.testing.assert_array_equal(_np(disp.counts), counts)
 
 
-@pytest.mark.parametrize("d,f", [(256, 160), (264, 1352), (1480, 72)])
-def test_every_row_count_of_tall_tiles(d, f):
-    """Many rows per expert: tiles of 256 rows, remainders that ride along (up to 288 rows) or
-    get a tile of their own, whole and halved, and empty and light experts among them."""
-    counts = [256, 0, 257, 288, 289, 300, 512, 544, 545, 1, 384, 600, 40]
-    E, T = len(counts), sum(counts)
-    rng = np.random.default_rng(74)
+def _routed(counts, seed):
+    """Logits that send counts[e] tokens to expert e, in random order."""
+    rng = np.random.default_rng(seed)
+    T, E = sum(counts), len(counts)
     owner = np.repeat(np.arange(E), counts)
     rng.shuffle(owner)
     logits = rng.standard_normal((T, E)).astype(np.float32)
     logits[np.arange(T), owner] += 50.0
-    disp, _ = _case(W("i8_tall", T, d, f, E, 1, 0, E, "bf16", 74), logits)
+    return logits
+
+
+@pytest.mark.parametrize("d,f", [(256, 160), (264, 1352), (1480, 72)])
+def test_every_row_count_of_many_rows(d, f):
+    """Many rows per expert at the edges of the row tiles, empty and light experts among them."""
+    counts = [256, 0, 257, 288, 289, 300, 512, 544, 545, 1, 384, 600, 40]
+    disp, _ = _case(W("i8_many", sum(counts), d, f, 13, 1, 0, 13, "bf16", 74), _routed(counts, 74))
+    np.testing.assert_array_equal(_np(disp.counts), counts)
+
+
+# 257 to 288 rows per expert on average go to the tallest tiles also at small sizes
+@pytest.mark.parametrize("d,f", [(200, 520), (200, 3320), (712, 2184)])
+@pytest.mark.parametrize("counts", [(545, 1, 257, 300, 257), (544, 255, 129, 0, 432), (288, 272, 264, 280, 256)])
+def test_every_row_count_of_tall_tiles(counts, d, f):
+    """Tiles of 256 rows, remainders that ride along (up to 288 rows) or get a tile of their
+    own, whole and halved."""
+    disp, _ = _case(W("i8_tall", sum(counts), d, f, 5, 1, 0, 5, "bf16", 82), _routed(counts, 82))
     np.testing.assert_array_equal(_np(disp.counts), counts)
 
 

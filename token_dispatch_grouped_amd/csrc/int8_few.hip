@@ -192,12 +192,14 @@ __global__ __launch_bounds__(kThreads, 3) void int8_thin_kernel(
   __shared__ i32x4 part[kWaves * RT * FRAGS * kWave];
   __shared__ float scales[kThinRows];
   using Wt = Weights<SWIGLU, FRAGS, AHEAD>;
-  if (static_cast<int>(blockIdx.y) >= *n_row_tiles) return;
-  const RowGroup g = groups[blockIdx.y];
   const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid / kWave);
+  // column blocks fastest
+  const int cols = (N + 16 * Wt::NO - 1) / (16 * Wt::NO), q = static_cast<int>(blockIdx.x) / cols;
+  const int n0 = (static_cast<int>(blockIdx.x) - q * cols) * 16 * Wt::NO;
+  if (q >= *n_row_tiles) return;
+  const RowGroup g = groups[q];
   const int r0 = g.row0 + g.index * kThinRows;
   const int R = min(kThinRows, g.row_end - r0);
-  const int n0 = static_cast<int>(blockIdx.x) * 16 * Wt::NO;
   Wt wt(w, g.expert, n0, kblocks, N);
   uint32_t off[RT];
 #pragma unroll
@@ -303,7 +305,7 @@ hipError_t launch_int8_thin(const void* a, const float* a_scale, const void* w, 
   const int kblocks = int8_kblocks(K);
 #define MOE_THIN(S, F, A)                                                                                         \
   hipLaunchKernelGGL((int8_thin_kernel<S, F, A>),                                                                 \
-                     dim3(static_cast<unsigned>((N + 16 * (S ? F / 2 : F) - 1) / (16 * (S ? F / 2 : F))), tiles), \
+                     dim3(tiles * static_cast<unsigned>((N + 16 * (S ? F / 2 : F) - 1) / (16 * (S ? F / 2 : F)))), \
                      dim3(kThreads), 0, stream, static_cast<const uint8_t*>(a), a_scale,                          \
                      static_cast<const uint8_t*>(w), w_scale, static_cast<__bf16*>(c), count, groups, kblocks, N, \
                      n_max)

@@ -144,8 +144,9 @@ template <int G, int VPT>
 hipError_t launch_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale, int e_begin,
                        int e_end, int k, int64_t T, int cols, int64_t n_max, void* plan, int tile_rows, hipStream_t stream) {
   constexpr int kRows = block_threads<G>() / G;
+  // n_max may be many times the local rows: workgroups take turns, eight per CU
   const int64_t blocks = (n_max + kRows - 1) / kRows;
-  hipLaunchKernelGGL((quantize_rows_kernel<G, VPT>), dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536) + (plan != nullptr ? 1u : 0u)),
+  hipLaunchKernelGGL((quantize_rows_kernel<G, VPT>), dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048) + (plan != nullptr ? 1u : 0u)),
                      dim3(block_threads<G>()), 0, stream, static_cast<const uint4*>(src), perm, offsets,
                      static_cast<uint8_t*>(q), scale, e_begin, e_end, k, T, cols / 8, (cols + 63) / 64, n_max, plan,
                      tile_rows);
@@ -165,7 +166,8 @@ int64_t int8_max_k() { return 65536; }
 //       experts with few columns give. Graph replays: 8 experts, 64 tokens x 2, 1024 x 3584:
 //       33.8 us against 41.6; 4 experts, 64 tokens, 4096 x 512: 22.6 against 34.2; but 32 experts,
 //       64 tokens x 4, 1024 x 1024 (128 short tiles): 32.8 against 31.0, and 8 experts, 512 tokens x
-//       2, 1024 x 3584 (128 rows each): 75 against 64.
+//       2, 1024 x 3584 (128 rows each): 75 against 64. Its grid holds every tile there could be,
+//       so a rank that might get far more rows than it will (a small share) takes the others.
 // tall  where its rounds cost less than the short ones'. A round of tall tiles on 256 CUs
 //       measured as its K stages + 18 (fill, and the epilogue that nothing overlaps), a round of short
 //       tiles, two per CU, as 1.31 times its stages + 1 (1.5 times the bytes through LDS, but one tile
@@ -183,7 +185,9 @@ int int8_tile_rows(int64_t T, int k, int E, int e_loc, int d, int d_ff) {
   const double short_tiles = experts * ceil(rows / kShortRows);
   const double fewest = fmin(short_tiles * cols[0], short_tiles * cols[1]);
   const double most = fmax(short_tiles * cols[0], short_tiles * cols[1]);
-  if ((fewest < cus / 4 && rows <= 64) || most < cus / 4) return kThinRows;
+  const int64_t n_max = T * (k < e_loc ? k : e_loc);
+  if (((fewest < cus / 4 && rows <= 64) || most < cus / 4) && max_row_tiles(n_max, e_loc, kThinRows) <= kThinTiles)
+    return kThinRows;
   const double full = floor(rows / kTallRows), rest = rows - full * kTallRows;
   // a short last tile costs about half of a tall one; one of up to 32 rows rides along
   const double tall_tiles = experts * fmax(1.0, full + (rest > 128 ? 1.0 : rest > kTallMerge ? 0.5 : 0.0));
