@@ -102,7 +102,8 @@ def _backward(case, dt, wdt, s, mean, rstd, bias, ds, **kw):
 TYPES = [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")]
 # every row shape: groups of 16, 32, 64 threads with full and ragged last vectors,
 # workgroups of 256 and 1024, and the widest rows
-DIMS = [8, 72, 128, 136, 256, 264, 512, 520, 1024, 1032, 2048, 2056, 2880, 4096, 4104, 7168, 8200, 16384, 16392, 32768]
+DIMS = [8, 72, 128, 136, 256, 264, 512, 520, 1024, 1032, 1544, 2048, 2056, 2880, 4096, 4104, 6152, 7168, 8200, 12296, 16384,
+        16392, 32768]
 
 
 @pytest.mark.parametrize("dt,wdt", TYPES, ids=["-".join(t) for t in TYPES])
