@@ -137,6 +137,7 @@ CASES = [
     W("i8_few_many_rows", 64, 136, 72, 64, 1, 0, 64, "bf16", 78, 3.0),  # skewed: several row tiles of one expert
     W("i8_few_wide", 8, 512, 2056, 64, 4, 0, 64, "bf16", 79),   # enough channels for the wide workgroups
     W("i8_few_long_k", 1, 64, 8712, 2, 1, 0, 2, "bf16", 80),    # more of a row than its threads hold
+    W("i8_long_rows", 9273, 2824, 784, 2, 1, 1, 2, "bf16", 83),  # one expert of thousands, several rounds
     W("i8_stages", 260, 448, 192, 2, 1, 0, 2, "bf16", 72),      # 7 and 3 K stages
 ]
 
@@ -166,7 +167,7 @@ def _routed(counts, seed):
     return logits
 
 
-@pytest.mark.parametrize("d,f", [(256, 160), (264, 1352), (1480, 72)])
+@pytest.mark.parametrize("d,f", [(256, 160), (264, 1352), (1480, 72), (136, 520), (520, 136), (64, 1032)])
 def test_every_row_count_of_many_rows(d, f):
     """Many rows per expert at the edges of the row tiles, empty and light experts among them."""
     counts = [256, 0, 257, 288, 289, 300, 512, 544, 545, 1, 384, 600, 40]
@@ -174,8 +175,8 @@ def test_every_row_count_of_many_rows(d, f):
     np.testing.assert_array_equal(_np(disp.counts), counts)
 
 
-# 257 to 288 rows per expert on average go to the tallest tiles also at small sizes
-@pytest.mark.parametrize("d,f", [(200, 520), (200, 3320), (712, 2184)])
+# the last two pairs of sizes, with 272 rows per expert on average, go to the tallest tiles
+@pytest.mark.parametrize("d,f", [(200, 520), (200, 3320), (712, 2184), (1160, 2360), (1288, 2472)])
 @pytest.mark.parametrize("counts", [(545, 1, 257, 300, 257), (544, 255, 129, 0, 432), (288, 272, 264, 280, 256)])
 def test_every_row_count_of_tall_tiles(counts, d, f):
     """Tiles of 256 rows, remainders that ride along (up to 288 rows) or get a tile of their

@@ -160,48 +160,50 @@ int int8_kblocks(int K) { return (K + 63) / 64; }
 int64_t int8_max_k() { return 65536; }
 
 // Which workgroups a call's products use, from the rows per expert that uniform routing gives
-// (the real counts are on the device only; any choice is right for any counts):
+// (the real counts are on the device only; any choice is right for any counts): the one whose two
+// launches would take the least time, in microseconds, by what single launches measured.
 //
-// thin  (tiles of 32 rows) where the short tiles of a product are too few for the chip, as few
-//       experts with few columns give. Graph replays: 8 experts, 64 tokens x 2, 1024 x 3584:
-//       33.8 us against 41.6; 4 experts, 64 tokens, 4096 x 512: 22.6 against 34.2; but 32 experts,
-//       64 tokens x 4, 1024 x 1024 (128 short tiles): 32.8 against 31.0, and 8 experts, 512 tokens x
-//       2, 1024 x 3584 (128 rows each): 75 against 64. Its grid holds every tile there could be,
-//       so a rank that might get far more rows than it will (a small share) takes the others.
-// tall  where its rounds cost less than the short ones'. A round of tall tiles on 256 CUs
-//       measured as its K stages + 18 (fill, and the epilogue that nothing overlaps), a round of short
-//       tiles, two per CU, as 1.31 times its stages + 1 (1.5 times the bytes through LDS, but one tile
-//       computes while the other waits); a round that is at most half full costs 0.55. 8 experts of 1024
-//       rows: 4096 x 14336 tall 2718 us (16384 tokens), short 2905; 4096 x 4096 tall 486, short 458;
-//       8 experts of 512 rows 4096 x 4096 tall 233, short 265; 16 of 256 rows 2880 x 2880 tall 164,
-//       short 177; 16 of 1024 rows 1024 x 2048 tall 215, short 173.
-// short otherwise.
+// thin   5 + the longer of 0.1 per K-block (a wave's loads wait for each other over a quarter of K)
+//        and the bytes of all workgroups, 6 KB per K-block each, at 8.5 TB/s (mostly L2), and 1.5 for
+//        each time they fill the chip (three a CU)
+// short  7 + 0.4 per K stage while each tile has a CU to itself; past that 6 + rounds of two tiles
+//        per CU, 1.05 per stage + 0.8 (its products, and 1.5 times tall's bytes through LDS)
+// tall   4 + rounds of one tile per CU, 0.8 per stage + 14 (the fill, and the epilogue that nothing
+//        overlaps)
+// A round that is at most half full costs 0.55 (tall: its tiles are halved). Whole calls (graph
+// replays): 8 experts, 64 tokens x 2, 1024 x 3584: thin 34 us, short 42; 32 experts, 64 tokens x 4, 1024
+// x 1024: thin 33, short 31; 8 experts of 1024 rows, 4096 x 4096: short 458, tall 486; 4096 x 14336
+// (16384 tokens): short 2905, tall 2718; 16 experts of 256 rows, 2880 x 2880: short 177, tall 164.
 int int8_tile_rows(int64_t T, int k, int E, int e_loc, int d, int d_ff) {
   const double rows = static_cast<double>(T) * k / E;  // per expert
-  const double experts = rows * e_loc < 1.0 ? 1.0 : rows < 1.0 ? rows * e_loc : e_loc;
-  const double cols[2] = {(d_ff + 127) / 128 * 1.0, (d + 255) / 256 * 1.0};
-  const double stages[2] = {int8_kblocks(d) * 1.0, int8_kblocks(d_ff) * 1.0};
+  const double experts = fmin(static_cast<double>(e_loc), fmax(1.0, rows * e_loc));
+  const double per = fmax(rows * e_loc / experts, 1.0);  // rows of an expert that has any
   const double cus = device_cu_count();
-  const double short_tiles = experts * ceil(rows / kShortRows);
-  const double fewest = fmin(short_tiles * cols[0], short_tiles * cols[1]);
-  const double most = fmax(short_tiles * cols[0], short_tiles * cols[1]);
-  const int64_t n_max = T * (k < e_loc ? k : e_loc);
-  if (((fewest < cus / 4 && rows <= 64) || most < cus / 4) && max_row_tiles(n_max, e_loc, kThinRows) <= kThinTiles)
-    return kThinRows;
-  const double full = floor(rows / kTallRows), rest = rows - full * kTallRows;
-  // a short last tile costs about half of a tall one; one of up to 32 rows rides along
-  const double tall_tiles = experts * fmax(1.0, full + (rest > 128 ? 1.0 : rest > kTallMerge ? 0.5 : 0.0));
   auto rounds = [](double r) {
     const double whole = floor(r), part = r - whole;
-    return whole + (part < 0.02 ? 0.0 : part <= 0.5 ? 0.55 : 1.0);
+    return whole + (whole > 0 && part < 0.02 ? 0.0 : part <= 0.5 ? 0.55 : 1.0);
   };
-  // counts that scatter around their mean leave a few tiles more than it says
-  const double tall_more = experts > 1 && rows > 512 ? 0.3 : 0.0, short_more = 0.1;
-  double tall = 0, shorter = 0;
+  const double thin_rows = experts * ceil(per / kThinRows);
+  const double short_rows = experts * ceil(per / kShortRows);
+  // in rounds, a light last tile counts half; counts that scatter leave light tiles more than their mean
+  const double s_rest = fmod(per, kShortRows), t_rest = fmod(per, kTallRows);
+  const double short_cost =
+      experts * (floor(per / kShortRows) + (s_rest > 64 ? 1.0 : s_rest > 0 ? 0.5 : 0.0) + (per >= 64 ? 0.2 : 0.0));
+  const double tall_cost =
+      experts * fmax(1.0, floor(per / kTallRows) + (t_rest > 128 ? 1.0 : t_rest > kTallMerge ? 0.5 : 0.0));
+  const double tall_more = per > 512 ? fmin(0.3, 0.04 * experts) : 0.0;
+  double thin = 0, shorter = 0, tall = 0;
   for (int i = 0; i < 2; ++i) {
-    tall += (rounds(tall_tiles * cols[i] / cus) + tall_more) * (stages[i] + 18);
-    shorter += (rounds(short_tiles * cols[i] / (2 * cus)) + short_more) * (1.31 * stages[i] + 1);
+    const int N = i ? d : d_ff;
+    const double st = int8_kblocks(i ? d_ff : d), cols = (N + (i ? 255 : 127)) / (i ? 256 : 128);
+    const double thin_groups = thin_rows * ((N + (i ? 63 : 31)) / (i ? 64 : 32));
+    thin += 5 + fmax(0.1 * st, thin_groups * st * 6e3 / 8.5e6) + thin_groups / (3 * cus) * 1.5;
+    shorter += short_rows * cols <= cus ? 7 + 0.4 * st : 6 + rounds(short_cost * cols / (2 * cus)) * (1.05 * st + 0.8);
+    tall += 4 + (rounds(tall_cost * cols / cus) + tall_more) * 0.8 * (st + 18);
   }
+  // a thin launch's grid holds every tile there could be: a share that might get far more rows takes another
+  const int64_t n_max = T * (k < e_loc ? k : e_loc);
+  if (thin <= fmin(shorter, tall) && max_row_tiles(n_max, e_loc, kThinRows) <= kThinTiles) return kThinRows;
   return tall <= shorter ? kTallRows : kShortRows;
 }
 
