@@ -63,8 +63,9 @@ def _inputs(w, logits=None):
     return g.to_dev(x, "bf16"), g.to_dev(logits, "f32"), g.to_dev(wgu, "bf16"), g.to_dev(wdn, "bf16")
 
 
-def _run(w, x, logits, experts, y=None):
-    idx, _ = moe.route_topk(logits, w.k)
+def _run(w, x, logits, experts, y=None, idx=None):
+    if idx is None:
+        idx, _ = moe.route_topk(logits, w.k)
     disp = moe.dispatch(x, idx, w.E, w.e_begin, w.e_end, gather=False)
     ws = torch.full((moe.grouped_gemm_int8_workspace_bytes(w.T, w.d, w.d_ff, w.E, w.k, w.e_begin, w.e_end),), 0x5A,
                     dtype=torch.uint8, device="cuda")
@@ -75,11 +76,12 @@ def _run(w, x, logits, experts, y=None):
     return disp, ws, y
 
 
-def _check(w, x, logits, experts):
+def _check(w, x, logits, experts, idx=None):
     print(f"case {w}", flush=True)
-    disp, ws, y = _run(w, x, logits, experts)
+    disp, ws, y = _run(w, x, logits, experts, idx=idx)
     offs, perm = _np(disp.offsets), _np(disp.perm)
-    lo, n_loc = offs[w.e_begin], int(offs[w.e_end] - offs[w.e_begin])
+    lo = offs[w.e_begin]
+    n_loc = min(int(offs[w.e_end] - lo), w.n_max)  # ids that a token repeats may give more: rows past n_max are dropped
     tok = perm[lo:lo + n_loc] // w.k
     xq, xs, h, hq, hs = _parts(ws, w.n_max, w.d, w.d_ff)
     x32 = x.float().cpu().numpy()[tok]
@@ -96,7 +98,7 @@ def _check(w, x, logits, experts):
     y_got = g.to_f64(y)
     worst = [0.0, 0.0]
     for e in range(w.E_loc):
-        r0, r1 = (int(offs[w.e_begin + e + i] - lo) for i in (0, 1))
+        r0, r1 = (min(int(offs[w.e_begin + e + i] - lo), w.n_max) for i in (0, 1))
         if r0 == r1:
             continue
         gu = oa.int8_product(want_q[r0:r1], want_s[r0:r1], wgu[e], sgu[e])
@@ -154,6 +156,17 @@ def test_every_row_count():
     logits = _routed(counts, 73)
     disp, _ = _case(W("i8_rows", T, 256, 160, E, 1, 0, E, "bf16", 73), logits)
     np.testing.assert_array_equal(_np(disp.counts), counts)
+
+
+@pytest.mark.parametrize("T,k,E,lo,hi", [(4, 4, 8, 0, 8), (20, 4, 64, 0, 64), (20, 4, 64, 7, 8), (64, 2, 64, 3, 9),
+                                         (300, 4, 8, 0, 8), (300, 4, 8, 3, 4)])
+def test_ids_that_a_token_repeats(T, k, E, lo, hi):
+    """Ids from elsewhere that name an expert several times: it gets more rows than there are tokens."""
+    w = W("i8_again", T, 200, 328, E, k, lo, hi, "bf16", 84)
+    x, lg, wgu, wdn = _inputs(w)
+    idx = torch.full((T, k), min(7, E - 1) if E > 8 else 3, dtype=torch.int32, device="cuda")
+    idx[::5, 0] = 5  # and a few elsewhere
+    _check(w, x, lg, moe.quantize_experts(wgu, wdn), idx=idx)
 
 
 def _routed(counts, seed):

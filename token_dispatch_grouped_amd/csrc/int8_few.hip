@@ -29,6 +29,8 @@ constexpr int kMaxCodes = 48 * 1024;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+// rows of a workgroup's turn
+__host__ __device__ constexpr int few_rows(int64_t T) { return T < kRows ? static_cast<int>(T) : kRows; }
 __host__ __device__ constexpr int code_stride(int kblocks) { return kblocks * 64 + 16; }  // rows fall into different banks
 
 // FRAGS 16-channel blocks of a workgroup (SwiGLU: half gate, half up), AHEAD K-blocks that
@@ -114,71 +116,76 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
   const int seg0 = offsets[e_begin];
   const int start = static_cast<int>(min(static_cast<int64_t>(offsets[e_begin + e] - seg0), n_max));
   const int end = static_cast<int>(min(static_cast<int64_t>(offsets[e_begin + e + 1] - seg0), n_max));
-  const int r0 = start + static_cast<int>(blockIdx.z) * kRows;
-  if (r0 >= end) return;
-  const int R = min(kRows, end - r0);
-  const int n0 = static_cast<int>(blockIdx.x) * 16 * Wt::NO;
-  Wt wt(w, e, n0, kblocks, N);
-  wt.load(wt.lo);
-  __builtin_amdgcn_sched_barrier(0);  // in flight before anything else
+  // An expert has T rows at most, and this is one turn, unless topk_idx repeats an id in a token: then
+  // more turns of as many rows as there is LDS for.
+  const int tile = few_rows(T);
+#pragma clang loop unroll(disable)
+  for (int r0 = start + static_cast<int>(blockIdx.z) * tile; r0 < end; r0 += static_cast<int>(gridDim.z) * tile) {
+    const int R = min(tile, end - r0);
+    const int n0 = static_cast<int>(blockIdx.x) * 16 * Wt::NO;
+    Wt wt(w, e, n0, kblocks, N);
+    wt.load(wt.lo);
+    __builtin_amdgcn_sched_barrier(0);  // in flight before anything else
 
-  // the rows' codes, a row at a time by all threads
-  const int stride = code_stride(kblocks);
-  for (int r = 0; r < R; ++r) {
-    int64_t from = r0 + r;
-    if (perm != nullptr) from = perm[seg0 + r0 + r] / k;
-    const int n = perm == nullptr || (from >= 0 && from < T) ? cols_vec : 0;
-    const uint4* row = src + from * cols_vec;
-    uint4 v[kHeld];
-    uint32_t top = 0;
+    // the rows' codes, a row at a time by all threads
+    const int stride = code_stride(kblocks);
+    for (int r = 0; r < R; ++r) {
+      int64_t from = r0 + r;
+      if (perm != nullptr) from = perm[seg0 + r0 + r] / k;
+      const int n = perm == nullptr || (from >= 0 && from < T) ? cols_vec : 0;
+      const uint4* row = src + from * cols_vec;
+      uint4 v[kHeld];
+      uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int c = i * kThreads + tid;
-      v[i] = c < n ? row[c] : make_uint4(0, 0, 0, 0);
-    }
-    for (int c = kHeld * kThreads + tid; c < n; c += kThreads) top = rows::Max::apply(top, amax8(row[c]));
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) top = rows::Max::apply(top, amax8(v[i]));
-    top = rows::group_reduce<kThreads, rows::Max>(top, tops[r & 1]);
-    float sc, inv;
-    scale_of(top, &sc, &inv);
-    if (tid == 0) scales[r] = sc;
-    char* codes = smem + r * stride;
-    auto put = [&](int c, const uint4& a) {
-      float f[8];
-      rows::Vec16<true>::unpack(a, f);
-      *reinterpret_cast<uint2*>(codes + c * 8) = codes8(f, inv);
-    };
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int c = i * kThreads + tid;
-      if (c < kblocks * 8) put(c, v[i]);  // zeros past the last column
-    }
-    for (int c = kHeld * kThreads + tid; c < kblocks * 8; c += kThreads)
-      put(c, c < n ? row[c] : make_uint4(0, 0, 0, 0));
-  }
-  __syncthreads();
-
-  // lanes of rows past the last read the last row's codes; their sums are not stored
-  const char* mine = smem + min(lane & 15, R - 1) * stride + (lane >> 4) * 16;
-  i32x4 acc[FRAGS];
-#pragma unroll
-  for (int f = 0; f < FRAGS; ++f) acc[f] = i32x4{0, 0, 0, 0};
-  for (int kb0 = wt.lo; kb0 < wt.hi; kb0 += AHEAD) {
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u)
-      if (kb0 + u < wt.hi) {
-        const i32x4 a = *reinterpret_cast<const i32x4*>(mine + (kb0 + u) * 64);
-#pragma unroll
-        for (int f = 0; f < FRAGS; ++f)
-          acc[f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, wt.b[u][f], acc[f], 0, 0, 0);
+      for (int i = 0; i < kHeld; ++i) {
+        const int c = i * kThreads + tid;
+        v[i] = c < n ? row[c] : make_uint4(0, 0, 0, 0);
       }
-    if (kb0 + AHEAD < wt.hi) wt.load(kb0 + AHEAD);
-  }
+      for (int c = kHeld * kThreads + tid; c < n; c += kThreads) top = rows::Max::apply(top, amax8(row[c]));
 #pragma unroll
-  for (int f = 0; f < FRAGS; ++f) part[(wv * FRAGS + f) * kWave + lane] = acc[f];
-  __syncthreads();
-  finish<SWIGLU, FRAGS, 1>(part, scales, w_scale + e * (wt.block_bytes / 64), out, r0, R, n0, N);
+      for (int i = 0; i < kHeld; ++i) top = rows::Max::apply(top, amax8(v[i]));
+      top = rows::group_reduce<kThreads, rows::Max>(top, tops[r & 1]);
+      float sc, inv;
+      scale_of(top, &sc, &inv);
+      if (tid == 0) scales[r] = sc;
+      char* codes = smem + r * stride;
+      auto put = [&](int c, const uint4& a) {
+        float f[8];
+        rows::Vec16<true>::unpack(a, f);
+        *reinterpret_cast<uint2*>(codes + c * 8) = codes8(f, inv);
+      };
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const int c = i * kThreads + tid;
+        if (c < kblocks * 8) put(c, v[i]);  // zeros past the last column
+      }
+      for (int c = kHeld * kThreads + tid; c < kblocks * 8; c += kThreads)
+        put(c, c < n ? row[c] : make_uint4(0, 0, 0, 0));
+    }
+    __syncthreads();
+
+    // lanes of rows past the last read the last row's codes; their sums are not stored
+    const char* mine = smem + min(lane & 15, R - 1) * stride + (lane >> 4) * 16;
+    i32x4 acc[FRAGS];
+#pragma unroll
+    for (int f = 0; f < FRAGS; ++f) acc[f] = i32x4{0, 0, 0, 0};
+    for (int kb0 = wt.lo; kb0 < wt.hi; kb0 += AHEAD) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (kb0 + u < wt.hi) {
+          const i32x4 a = *reinterpret_cast<const i32x4*>(mine + (kb0 + u) * 64);
+#pragma unroll
+          for (int f = 0; f < FRAGS; ++f)
+            acc[f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, wt.b[u][f], acc[f], 0, 0, 0);
+        }
+      if (kb0 + AHEAD < wt.hi) wt.load(kb0 + AHEAD);
+    }
+#pragma unroll
+    for (int f = 0; f < FRAGS; ++f) part[(wv * FRAGS + f) * kWave + lane] = acc[f];
+    __syncthreads();
+    finish<SWIGLU, FRAGS, 1>(part, scales, w_scale + e * (wt.block_bytes / 64), out, r0, R, n0, N);
+    __syncthreads();  // the next turn writes the codes, scales and sums again
+  }
 }
 
 // Up to 32 rows of an expert whose codes are there already: as above, the rows' codes
@@ -250,9 +257,9 @@ hipError_t launch_one(const void* src, const int32_t* perm, const int32_t* offse
                       int64_t n_max, hipStream_t stream) {
   constexpr int cols = 16 * (SWIGLU ? FRAGS / 2 : FRAGS);
   const int kblocks = int8_kblocks(K);
-  const int rows = static_cast<int>(T < kRows ? T : kRows);
+  const int rows = few_rows(T);
   const dim3 grid(static_cast<unsigned>((N + cols - 1) / cols), static_cast<unsigned>(e_loc),
-                  static_cast<unsigned>((T + kRows - 1) / kRows));
+                  static_cast<unsigned>((T + rows - 1) / rows));
   hipLaunchKernelGGL((int8_few_kernel<SWIGLU, FRAGS, AHEAD>), grid, dim3(kThreads),
                      static_cast<unsigned>(rows * code_stride(kblocks)), stream, static_cast<const uint4*>(src), perm,
                      offsets, static_cast<const uint8_t*>(w), w_scale, static_cast<__bf16*>(out), e_begin, k, T, K / 8,
@@ -282,9 +289,8 @@ hipError_t launch_product(const void* src, const int32_t* perm, const int32_t* o
 // for 120, 32 tokens 289 for 294, 64 tokens (two rows each) 415 for 414, 128 tokens 541 for 476; small
 // experts lose earlier (16 tokens x 2 of 8 experts of 64 x 64, four rows each: 17.5 for 13.9).
 bool int8_few(int64_t T, int k, int E, int d, int d_ff) {
-  const int64_t rows = T < kRows ? T : kRows;
   return T <= 64 && T * k <= 2 * static_cast<int64_t>(E) &&
-         rows * code_stride(int8_kblocks(d > d_ff ? d : d_ff)) <= kMaxCodes;
+         few_rows(T) * code_stride(int8_kblocks(d > d_ff ? d : d_ff)) <= kMaxCodes;
 }
 
 hipError_t launch_int8_few(const void* x, const int32_t* perm, const int32_t* offsets, const void* q_gu,
