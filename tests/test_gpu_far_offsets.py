@@ -49,6 +49,21 @@ def test_layer_norm_and_its_gradient():
     assert bool(((db.double() - want).abs() <= bound).all())
 
 
+def test_layer_norm_of_more_rows_than_a_launch_has_threads_for():
+    d, T = 8, (1 << 28) + 21  # 16 threads a row: 2^32 and more
+    x = _normal((1 << 20, d), 6).repeat(T // (1 << 20) + 1, 1)[:T]
+    w = _normal((1, d), 7)[0]
+    y, _, mean, rstd = moe.layer_norm(x, w, None, EPS)
+    torch.cuda.synchronize()
+    part = T % (1 << 20)
+    yr, _, mr, sr = moe.layer_norm(x[:1 << 20], w, None, EPS)
+    torch.cuda.synchronize()
+    for at in (0, T // (1 << 21) << 20, T - part):
+        n = min(1 << 20, T - at)
+        assert torch.equal(y[at:at + n], yr[:n]) and torch.equal(mean[at:at + n], mr[:n]), at
+        assert torch.equal(rstd[at:at + n], sr[:n]), at
+
+
 def test_gradient_norm_and_clip():
     n = (1 << 32) + 5  # elements, past 32 bits
     g = torch.full((n,), 0.5, dtype=BF, device="cuda")

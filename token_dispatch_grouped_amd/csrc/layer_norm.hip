@@ -297,6 +297,7 @@ unsigned row_blocks(int64_t T, int64_t most) {
 }
 
 constexpr int kBackwardBlocks = 512;  // partial rows at most
+constexpr int64_t kForwardBlocks = int64_t{1} << 21;  // a launch holds fewer than 2^32 threads; rows past it take turns
 
 // F(G, VPT) for a row of row_vec vectors. A row that no more than half fills its threads wastes
 // their loads, hence the steps between powers of two (16384 x 1032 bf16, three vectors of a wave against
@@ -343,7 +344,7 @@ hipError_t launch_layer_norm(const void* x, const void* r, const void* w, const 
   const int row_vec = bf16 ? d / 8 : d / 4;
   const bool big = T * d * (bf16 ? 2 : 4) * (r != nullptr ? 4 : 2) > kStreamBytes;
 #define MOE_NORM_S(B, W, G, VPT, S)                                                                              \
-  hipLaunchKernelGGL((layer_norm_kernel<B, W, G, VPT, S>), dim3(row_blocks<G>(T, int64_t{1} << 30)),             \
+  hipLaunchKernelGGL((layer_norm_kernel<B, W, G, VPT, S>), dim3(row_blocks<G>(T, kForwardBlocks)),               \
                      dim3(block_threads<G>()), 0, stream, static_cast<const uint4*>(x),                          \
                      static_cast<const uint4*>(r), w, b, eps, static_cast<uint4*>(y), static_cast<uint4*>(s),    \
                      mean, rstd, T, row_vec)
