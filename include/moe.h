@@ -442,11 +442,13 @@ moe_status moe_grad_norm(const moe_tensor* grads, int32_t n, float* norm, void* 
  *   scale in place. An entry may be its own gradient. In place, tensors are not
  *   touched when the factor is 1.
  * MOE_EINVAL if max_norm is negative or not finite, if two written tensors
- * overlap, or if a written tensor overlaps a gradient other than its own or its own in part. */
+ * overlap, or if a written tensor overlaps the norm, a gradient other than its own
+ * or its own in part. */
 moe_status moe_clip_grads(const moe_tensor* grads, const moe_tensor* out, int32_t n, const float* norm,
                           float max_norm, hipStream_t stream);
 
-/* moe_grad_norm, then moe_clip_grads with that norm. Same arguments and errors. */
+/* moe_grad_norm, then moe_clip_grads with that norm. Same arguments and errors;
+ * norm and workspace are written, and may overlap no tensor of either list. */
 moe_status moe_clip_grad_norm(const moe_tensor* grads, const moe_tensor* out, int32_t n, float max_norm,
                               float* norm, void* workspace, hipStream_t stream);
 

@@ -159,6 +159,21 @@ def test_clip_refuses_overlaps():
     assert clip([a], [(0x1004, 16, F)]) == EINVAL  # a result over its own gradient, shifted
 
 
+def test_clip_refuses_a_norm_or_workspace_among_the_tensors():
+    lib = moe.lib()
+    g, o = _list((0x1000, 16, F)), _list((0x8000, 16, F))
+    far, ws = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x200000)
+    for at in (0x1000, 0x103C):
+        inside = ctypes.c_void_p(at)
+        assert lib.moe_clip_grads(g, None, 1, inside, 1.0, NULL) == EINVAL  # scaled while others read it
+        assert lib.moe_clip_grad_norm(g, o, 1, 1.0, inside, ws, NULL) == EINVAL  # written while others read the gradient
+    assert lib.moe_clip_grads(g, o, 1, ctypes.c_void_p(0x8004), 1.0, NULL) == EINVAL
+    assert lib.moe_clip_grad_norm(g, o, 1, 1.0, ctypes.c_void_p(0x8004), ws, NULL) == EINVAL
+    for at in (0x1000, 0x8000, 0x1000 - 8):
+        assert lib.moe_clip_grad_norm(g, o, 1, 1.0, far, ctypes.c_void_p(at), NULL) == EINVAL
+    assert lib.moe_clip_grad_norm(g, o, 1, 1.0, ws, ws, NULL) == EINVAL
+
+
 def test_layer_norm_binding_checks():
     x, w = t((4, 64), bf16), t((64,), bf16)
     with pytest.raises(TypeError):

@@ -100,13 +100,14 @@ moe_status check_list(const moe_tensor* t, int32_t n) {
 
 struct Range {
   uintptr_t lo, hi;
-  int32_t i;       // entry
   bool written;
 };
 
 // Whether the list can be scaled into `out` (null: in place): each tensor's bytes
 // are sorted by address, and a written one may meet no other but its own gradient.
-moe_status check_clip(const moe_tensor* t, const moe_tensor* out, int32_t n, float max_norm) {
+// The norm (and the workspace, if any) are among them, written by the call or not.
+moe_status check_clip(const moe_tensor* t, const moe_tensor* out, int32_t n, float max_norm, const float* norm,
+                      bool norm_written, const void* workspace, size_t ws_bytes) {
   const moe_status st = check_list(t, n);
   if (st != MOE_OK) return st;
   if (!(max_norm >= 0.f) || isinf(max_norm)) return MOE_EINVAL;
@@ -116,17 +117,19 @@ moe_status check_clip(const moe_tensor* t, const moe_tensor* out, int32_t n, flo
     for (int32_t i = 0; i < n; ++i)
       if (out[i].numel != t[i].numel || out[i].dt != t[i].dt) return MOE_EINVAL;
   }
-  if (n == 0) return MOE_OK;
-  std::unique_ptr<Range[]> r(new (std::nothrow) Range[2 * static_cast<size_t>(n)]);
+  std::unique_ptr<Range[]> r(new (std::nothrow) Range[2 * static_cast<size_t>(n) + 2]);
   if (!r) return MOE_EHIP;
   size_t m = 0;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(norm), ws = reinterpret_cast<uintptr_t>(workspace);
+  r[m++] = Range{at, at + sizeof(float), norm_written};
+  if (workspace != nullptr) r[m++] = Range{ws, ws + ws_bytes, true};
   for (int32_t i = 0; i < n; ++i) {
     const size_t bytes = static_cast<size_t>(t[i].numel) * elem_bytes(t[i].dt);
     if (bytes == 0) continue;
     const uintptr_t src = reinterpret_cast<uintptr_t>(t[i].data);
     const uintptr_t dst = out != nullptr ? reinterpret_cast<uintptr_t>(out[i].data) : src;
-    if (dst != src) r[m++] = Range{src, src + bytes, i, false};
-    r[m++] = Range{dst, dst + bytes, i, true};
+    if (dst != src) r[m++] = Range{src, src + bytes, false};
+    r[m++] = Range{dst, dst + bytes, true};
   }
   std::sort(r.get(), r.get() + m, [](const Range& a, const Range& b) { return a.lo < b.lo; });
   // the furthest end so far, of any tensor and of the written ones
@@ -256,18 +259,19 @@ moe_status moe_grad_norm(const moe_tensor* grads, int32_t n, float* norm, void* 
 
 moe_status moe_clip_grads(const moe_tensor* grads, const moe_tensor* out, int32_t n, const float* norm, float max_norm,
                           hipStream_t stream) {
-  const moe_status st = check_clip(grads, out, n, max_norm);
-  if (st != MOE_OK) return st;
   if (norm == nullptr || !aligned(norm, 4)) return MOE_EINVAL;
+  const moe_status st = check_clip(grads, out, n, max_norm, norm, false, nullptr, 0);
+  if (st != MOE_OK) return st;
   if (n == 0) return MOE_OK;
   return from_hip(moe::launch_clip_grads(grads, out != nullptr ? out : grads, n, norm, max_norm, stream));
 }
 
 moe_status moe_clip_grad_norm(const moe_tensor* grads, const moe_tensor* out, int32_t n, float max_norm, float* norm,
                               void* workspace, hipStream_t stream) {
-  const moe_status st = check_clip(grads, out, n, max_norm);
-  if (st != MOE_OK) return st;
   if (norm == nullptr || workspace == nullptr || !aligned(norm, 4) || !aligned(workspace, 8)) return MOE_EINVAL;
+  const moe_status st =
+      check_clip(grads, out, n, max_norm, norm, true, workspace, n < 0 ? 0 : moe::grad_norm_workspace_bytes(n));
+  if (st != MOE_OK) return st;
   return from_hip(moe::launch_clip_grad_norm(grads, out != nullptr ? out : grads, n, max_norm, norm, workspace, stream));
 }
 
