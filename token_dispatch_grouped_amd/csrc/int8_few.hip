@@ -119,8 +119,13 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
   // An expert has T rows at most, and this is one turn, unless topk_idx repeats an id in a token: then
   // more turns of as many rows as there is LDS for.
   const int tile = few_rows(T);
+  int r0 = start + static_cast<int>(blockIdx.z) * tile;
+  if (r0 >= end) return;
 #pragma clang loop unroll(disable)
-  for (int r0 = start + static_cast<int>(blockIdx.z) * tile; r0 < end; r0 += static_cast<int>(gridDim.z) * tile) {
+  for (;;) {
+    // vmcnt(0), at once in the first turn: without it the compiler has every weight load wait, in the first
+    // turn too, for a load of the turn before that might still write its registers (one token: 2.4 us)
+    __builtin_amdgcn_s_waitcnt(0x0F70);
     const int R = min(tile, end - r0);
     const int n0 = static_cast<int>(blockIdx.x) * 16 * Wt::NO;
     Wt wt(w, e, n0, kblocks, N);
@@ -184,6 +189,8 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
     for (int f = 0; f < FRAGS; ++f) part[(wv * FRAGS + f) * kWave + lane] = acc[f];
     __syncthreads();
     finish<SWIGLU, FRAGS, 1>(part, scales, w_scale + e * (wt.block_bytes / 64), out, r0, R, n0, N);
+    r0 += static_cast<int>(gridDim.z) * tile;
+    if (r0 >= end) break;
     __syncthreads();  // the next turn writes the codes, scales and sums again
   }
 }
