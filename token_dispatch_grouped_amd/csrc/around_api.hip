@@ -231,9 +231,9 @@ moe_status moe_grouped_gemm_int8(const moe_shape* s, moe_dtype dt, const void* x
   char* p = static_cast<char*>(workspace);
   float* xs = reinterpret_cast<float*>(p + ws.xs);
   float* hs = reinterpret_cast<float*>(p + ws.hs);
-  if (moe::int8_few(s->T, s->k, s->E, d, d_ff))
+  if (ws.tile_rows == moe::kInt8FewRows)
     return from_hip(moe::launch_int8_few(x, perm, offsets, q_gate_up, scale_gate_up, q_down, scale_down, p + ws.h, y, d,
-                                         d_ff, s->e_begin, e_loc, s->k, s->T, n_max, stream));
+                                         d_ff, s->E, s->e_begin, e_loc, s->k, s->T, n_max, stream));
   hipError_t e = moe::launch_quantize_rows(x, perm, offsets, p + ws.xq, xs, s->e_begin, s->e_end, s->k, s->T, d, n_max,
                                            p + ws.plan, ws.tile_rows, stream);
   if (e == hipSuccess)

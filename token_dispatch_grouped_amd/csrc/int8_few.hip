@@ -1,5 +1,5 @@
-// The experts' FFN in 8-bit integers for a few tokens (single-token decoding): two
-// launches, each quantising its own rows.
+// The experts' FFN in 8-bit integers for a few rows per expert (decoding): two launches,
+// each quantising its own rows.
 //
 //   gate/up: rows of x (through perm) -> codes in LDS; H = silu(G) * U (bf16)
 //   down:    rows of H -> codes in LDS; Y (bf16)
@@ -9,7 +9,10 @@
 // expert and 16 * FRAGS weight channels over all of K; its four waves take a quarter of
 // K each and ask for their weights, straight into registers, before anything else.
 // While those are on their way the workgroup quantises its rows (each workgroup of an
-// expert does so again: a few KB from L2 next to its 100 KB of weights).
+// expert does so again: a few KB from L2 next to its 100 KB of weights). 32 tokens x 4 of
+// 128 experts of 2880 x 2880: 310 us, 2.0 GB of weights at 6.5 TB/s; one token of 4 of 32
+// experts of 1000 x 1480: 12.5 us, of which half is the latency of its two launches' chains
+// of loads (offsets, row ids, rows).
 // v_mfma_i32_16x16x64_i8: 16 channels x 64 K values of the K-blocked weights are one
 // contiguous KB, lane L's 16 bytes at (L & 15) * 64 + (L >> 4) * 16. Integer sums are
 // exact, so the quarters of K are joined in any order with the same bits.
@@ -23,14 +26,13 @@ using namespace int8;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kRows = 16;
 constexpr int kHeld = 4;    // vectors of a row a thread holds between its two passes
-constexpr int kMaxCodes = 48 * 1024;
+constexpr int kMaxCodes = 48 * 1024 - 128;  // with the sums 64 KB, and two workgroups a CU at least
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // rows of a workgroup's turn
-__host__ __device__ constexpr int few_rows(int64_t T) { return T < kRows ? static_cast<int>(T) : kRows; }
+__host__ __device__ constexpr int few_rows(int64_t T) { return T < kFewRows ? static_cast<int>(T) : kFewRows; }
 __host__ __device__ constexpr int code_stride(int kblocks) { return kblocks * 64 + 16; }  // rows fall into different banks
 
 // FRAGS 16-channel blocks of a workgroup (SwiGLU: half gate, half up), AHEAD K-blocks that
@@ -100,15 +102,15 @@ __device__ __forceinline__ void finish(const i32x4* part, const float* row_scale
   }
 }
 
-// A few tokens: the workgroup quantises its rows. Three waves per SIMD.
-template <bool SWIGLU, int FRAGS, int AHEAD>
+// The workgroup quantises its rows, G threads a row. Three waves per SIMD.
+template <bool SWIGLU, int FRAGS, int AHEAD, int G>
 __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
     const uint4* __restrict__ src, const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets,
     const uint8_t* __restrict__ w, const float* __restrict__ w_scale, __bf16* __restrict__ out, int e_begin, int k,
     int64_t T, int cols_vec, int kblocks, int N, int64_t n_max) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ i32x4 part[kWaves * FRAGS * kWave];
-  __shared__ float scales[kRows];
+  __shared__ float scales[kFewRows];
   __shared__ uint32_t tops[2][kWaves];
   using Wt = Weights<SWIGLU, FRAGS, AHEAD>;
   const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid / kWave);
@@ -116,8 +118,7 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
   const int seg0 = offsets[e_begin];
   const int start = static_cast<int>(min(static_cast<int64_t>(offsets[e_begin + e] - seg0), n_max));
   const int end = static_cast<int>(min(static_cast<int64_t>(offsets[e_begin + e + 1] - seg0), n_max));
-  // An expert has T rows at most, and this is one turn, unless topk_idx repeats an id in a token: then
-  // more turns of as many rows as there is LDS for.
+  // one turn for most experts; their number has no bound but n_max, as topk_idx may repeat an id in a token
   const int tile = few_rows(T);
   int r0 = start + static_cast<int>(blockIdx.z) * tile;
   if (r0 >= end) return;
@@ -132,9 +133,10 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
     wt.load(wt.lo);
     __builtin_amdgcn_sched_barrier(0);  // in flight before anything else
 
-    // the rows' codes, a row at a time by all threads
+    // the rows' codes
     const int stride = code_stride(kblocks);
-    for (int r = 0; r < R; ++r) {
+    const int li = tid % G;
+    for (int r = G == kThreads ? 0 : wv; r < R; r += kThreads / G) {
       int64_t from = r0 + r;
       if (perm != nullptr) from = perm[seg0 + r0 + r] / k;
       const int n = perm == nullptr || (from >= 0 && from < T) ? cols_vec : 0;
@@ -143,16 +145,16 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        const int c = i * kThreads + tid;
+        const int c = i * G + li;
         v[i] = c < n ? row[c] : make_uint4(0, 0, 0, 0);
       }
-      for (int c = kHeld * kThreads + tid; c < n; c += kThreads) top = rows::Max::apply(top, amax8(row[c]));
+      for (int c = kHeld * G + li; c < n; c += G) top = rows::Max::apply(top, amax8(row[c]));
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) top = rows::Max::apply(top, amax8(v[i]));
-      top = rows::group_reduce<kThreads, rows::Max>(top, tops[r & 1]);
+      top = rows::group_reduce<G, rows::Max>(top, tops[r & 1]);
       float sc, inv;
       scale_of(top, &sc, &inv);
-      if (tid == 0) scales[r] = sc;
+      if (li == 0) scales[r] = sc;
       char* codes = smem + r * stride;
       auto put = [&](int c, const uint4& a) {
         float f[8];
@@ -161,11 +163,10 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
       };
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        const int c = i * kThreads + tid;
+        const int c = i * G + li;
         if (c < kblocks * 8) put(c, v[i]);  // zeros past the last column
       }
-      for (int c = kHeld * kThreads + tid; c < kblocks * 8; c += kThreads)
-        put(c, c < n ? row[c] : make_uint4(0, 0, 0, 0));
+      for (int c = kHeld * G + li; c < kblocks * 8; c += G) put(c, c < n ? row[c] : make_uint4(0, 0, 0, 0));
     }
     __syncthreads();
 
@@ -258,55 +259,71 @@ __global__ __launch_bounds__(kThreads, 3) void int8_thin_kernel(
   finish<SWIGLU, FRAGS, RT>(part, scales, w_scale + g.expert * (wt.block_bytes / 64), out, r0, R, n0, N);
 }
 
-template <bool SWIGLU, int FRAGS, int AHEAD>
+template <bool SWIGLU, int FRAGS, int AHEAD, int G>
 hipError_t launch_one(const void* src, const int32_t* perm, const int32_t* offsets, const void* w,
-                      const float* w_scale, void* out, int e_begin, int e_loc, int k, int64_t T, int K, int N,
+                      const float* w_scale, void* out, int E, int e_begin, int e_loc, int k, int64_t T, int K, int N,
                       int64_t n_max, hipStream_t stream) {
   constexpr int cols = 16 * (SWIGLU ? FRAGS / 2 : FRAGS);
   const int kblocks = int8_kblocks(K);
   const int rows = few_rows(T);
+  // workgroups for twice the rows that uniform routing gives an expert; they take turns for more
+  const int64_t twice = min((2 * T * k + E - 1) / E, T);
   const dim3 grid(static_cast<unsigned>((N + cols - 1) / cols), static_cast<unsigned>(e_loc),
-                  static_cast<unsigned>((T + rows - 1) / rows));
-  hipLaunchKernelGGL((int8_few_kernel<SWIGLU, FRAGS, AHEAD>), grid, dim3(kThreads),
+                  static_cast<unsigned>((twice + rows - 1) / rows));
+  hipLaunchKernelGGL((int8_few_kernel<SWIGLU, FRAGS, AHEAD, G>), grid, dim3(kThreads),
                      static_cast<unsigned>(rows * code_stride(kblocks)), stream, static_cast<const uint4*>(src), perm,
                      offsets, static_cast<const uint8_t*>(w), w_scale, static_cast<__bf16*>(out), e_begin, k, T, K / 8,
                      kblocks, N, n_max);
   return hipGetLastError();
 }
 
-// Narrow workgroups where wide ones would be fewer than four per CU (one token, 4 of 32 experts of
-// 1000 x 1480: 11.2 us against 13.4; one token, 2 experts of 4096 x 14336: 59.6 against 63.5); the
-// wide ones' longer runs stream better once they fill the chip (32 tokens, 128 experts of 2880 x
-// 2880: 296 us against 342).
 template <bool SWIGLU>
 hipError_t launch_product(const void* src, const int32_t* perm, const int32_t* offsets, const void* w,
-                          const float* w_scale, void* out, int e_begin, int e_loc, int k, int64_t T, int K, int N,
-                          int64_t n_max, hipStream_t stream) {
-  const int wide = 16 * (SWIGLU ? 2 : 4);
-  const int64_t active = n_max < e_loc ? n_max : e_loc;
-  if (active * ((N + wide - 1) / wide) < 4 * device_cu_count())
-    return launch_one<SWIGLU, 2, 6>(src, perm, offsets, w, w_scale, out, e_begin, e_loc, k, T, K, N, n_max, stream);
-  return launch_one<SWIGLU, 4, 4>(src, perm, offsets, w, w_scale, out, e_begin, e_loc, k, T, K, N, n_max, stream);
+                          const float* w_scale, void* out, int E, int e_begin, int e_loc, int k, int64_t T, int K,
+                          int N, int64_t n_max, hipStream_t stream) {
+  const bool narrow = int8_few_columns(T, k, e_loc, N, SWIGLU) == 16 * (SWIGLU ? 1 : 2);
+#define MOE_FEW(F, A, G)                                                                                          \
+  return launch_one<SWIGLU, F, A, G>(src, perm, offsets, w, w_scale, out, E, e_begin, e_loc, k, T, K, N, n_max, \
+                                     stream)
+  if (int8_few_waves(T, k, E, K)) {
+    if (narrow) MOE_FEW(2, 6, kWave);
+    MOE_FEW(4, 4, kWave);
+  }
+  if (narrow) MOE_FEW(2, 6, kThreads);
+  MOE_FEW(4, 4, kThreads);
+#undef MOE_FEW
 }
 
 }  // namespace
 
-// Up to two rows per expert on average and 64 tokens, whose codes fit a workgroup's LDS. Against the
-// staged path (graph replays): one token 11 us for 25, 8 tokens x 4 of 128 experts of 2880 x 2880 107
-// for 120, 32 tokens 289 for 294, 64 tokens (two rows each) 415 for 414, 128 tokens 541 for 476; small
-// experts lose earlier (16 tokens x 2 of 8 experts of 64 x 64, four rows each: 17.5 for 13.9).
-bool int8_few(int64_t T, int k, int E, int d, int d_ff) {
-  return T <= 64 && T * k <= 2 * static_cast<int64_t>(E) &&
-         few_rows(T) * code_stride(int8_kblocks(d > d_ff ? d : d_ff)) <= kMaxCodes;
+// Output columns of a workgroup: narrow where wide ones would be fewer than four per CU (one token, 4 of
+// 32 experts of 1000 x 1480: 11.2 us against 13.4; one token, 2 experts of 4096 x 14336: 59.6 against
+// 63.5); the wide ones' longer runs stream better once they fill the chip (32 tokens, 128 experts
+// of 2880 x 2880: 296 us against 342).
+int int8_few_columns(int64_t T, int k, int e_loc, int N, bool swiglu) {
+  const int wide = swiglu ? 32 : 64;
+  const int64_t n_max = T * (k < e_loc ? k : e_loc), active = n_max < e_loc ? n_max : e_loc;
+  return active * ((N + wide - 1) / wide) < 4 * device_cu_count() ? wide / 2 : wide;
 }
+
+// A wave quantises a row (four at a time) unless it is long, by how many there are: a wave holds 2048
+// elements between its two passes and reads the others twice. 6 tokens x 3 of 8 experts, 520 x 640: 9.2
+// us against 14.5 with all threads on one row after the other; one token of 64 experts, 608 x 10312:
+// 32.4 against 26.2.
+bool int8_few_waves(int64_t T, int k, int E, int K) {
+  return K * static_cast<int64_t>(E) <= kHeld * kWave * 8 * max(T * k, static_cast<int64_t>(E));
+}
+
+// whether the codes of a workgroup's rows fit its LDS
+bool int8_few_fits(int64_t T, int K) { return few_rows(T) * code_stride(int8_kblocks(K)) <= kMaxCodes; }
 
 hipError_t launch_int8_few(const void* x, const int32_t* perm, const int32_t* offsets, const void* q_gu,
                            const float* s_gu, const void* q_dn, const float* s_dn, void* h, void* y, int d, int d_ff,
-                           int e_begin, int e_loc, int k, int64_t T, int64_t n_max, hipStream_t stream) {
+                           int E, int e_begin, int e_loc, int k, int64_t T, int64_t n_max, hipStream_t stream) {
   const hipError_t e =
-      launch_product<true>(x, perm, offsets, q_gu, s_gu, h, e_begin, e_loc, k, T, d, d_ff, n_max, stream);
+      launch_product<true>(x, perm, offsets, q_gu, s_gu, h, E, e_begin, e_loc, k, T, d, d_ff, n_max, stream);
   if (e != hipSuccess) return e;
-  return launch_product<false>(h, nullptr, offsets, q_dn, s_dn, y, e_begin, e_loc, k, T, d_ff, d, n_max, stream);
+  return launch_product<false>(h, nullptr, offsets, q_dn, s_dn, y, E, e_begin, e_loc, k, T, d_ff, d, n_max, stream);
 }
 
 hipError_t launch_int8_thin(const void* a, const float* a_scale, const void* w, const float* w_scale, void* c,

@@ -9,6 +9,7 @@ namespace int8 {
 
 constexpr int kTallRows = 256, kTallMerge = 32;  // a remainder of up to 32 rows rides on the last tile
 constexpr int kShortRows = 128;
+constexpr int kFewRows = kInt8FewRows;  // these tiles are not listed
 constexpr int kThinRows = 32, kThinTiles = 2048;  // row tiles of a thin launch at most
 constexpr int kGroup = 4;  // row tiles of an expert that are walked together
 

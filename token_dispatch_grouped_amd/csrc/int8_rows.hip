@@ -160,31 +160,36 @@ int int8_kblocks(int K) { return (K + 63) / 64; }
 int64_t int8_max_k() { return 65536; }
 
 // Which workgroups a call's products use, from the rows per expert that uniform routing gives
-// (the real counts are on the device only; any choice is right for any counts): the one whose two
-// launches would take the least time, in microseconds, by what single launches measured.
+// (the real counts are on the device only; any choice is right for any counts): the one whose
+// launches would take the least time, in microseconds, by what single launches measured. A launch
+// takes no less than its weights at 6.6 TB/s.
 //
-// thin   5 + the longer of 0.1 per K-block (a wave's loads wait for each other over a quarter of K)
-//        and the bytes of all workgroups, 6 KB per K-block each, at 8.5 TB/s (mostly L2), and 1.5 for
-//        each time they fill the chip (three a CU)
+// few    3 + the longer of 0.06 (wide: 0.1) per K-block, as a wave's loads wait for each other over a
+//        quarter of K, and the bytes of all workgroups, 2 or 4 KB per K-block each, at 8.5 TB/s (mostly
+//        L2), 1.5 for each time they fill the chip (three a CU), and 1.3 times as often what a
+//        workgroup takes to quantise its rows: 0.6 + 0.25 per 1024 of K for each row (waves: four rows)
+// thin   6 (with the quantising launch), 0.12 per K-block, 6 KB per K-block, else as few
 // short  7 + 0.4 per K stage while each tile has a CU to itself; past that 6 + rounds of two tiles
 //        per CU, 1.05 per stage + 0.8 (its products, and 1.5 times tall's bytes through LDS)
 // tall   4 + rounds of one tile per CU, 0.8 per stage + 14 (the fill, and the epilogue that nothing
 //        overlaps)
 // A round that is at most half full costs 0.55 (tall: its tiles are halved). Whole calls (graph
-// replays): 8 experts, 64 tokens x 2, 1024 x 3584: thin 34 us, short 42; 32 experts, 64 tokens x 4, 1024
-// x 1024: thin 33, short 31; 8 experts of 1024 rows, 4096 x 4096: short 458, tall 486; 4096 x 14336
-// (16384 tokens): short 2905, tall 2718; 16 experts of 256 rows, 2880 x 2880: short 177, tall 164.
+// replays): one token, 8 experts of 1512 x 824: few 10 us, thin 16; 14 tokens x 2 of 4, 1 here, 944 x
+// 1928: few 13, thin 18; 347 x 4 of 64, 1176 x 344: few 56, thin 35, short 30; 8 experts, 64 tokens x 2,
+// 1024 x 3584: thin 34, short 42; 8 experts of 1024 rows, 4096 x 4096: short 458, tall 486; 4096 x
+// 14336 (16384 tokens): short 2905, tall 2718; 16 experts of 256 rows, 2880 x 2880: short 177, tall 164.
 int int8_tile_rows(int64_t T, int k, int E, int e_loc, int d, int d_ff) {
   const double rows = static_cast<double>(T) * k / E;  // per expert
-  const double experts = fmin(static_cast<double>(e_loc), fmax(1.0, rows * e_loc));
-  const double per = fmax(rows * e_loc / experts, 1.0);  // rows of an expert that has any
+  const double experts = fmax(1.0, e_loc * -expm1(-rows));  // that have any
+  const double per = fmax(rows * e_loc / experts, 1.0);
   const double cus = device_cu_count();
   auto rounds = [](double r) {
     const double whole = floor(r), part = r - whole;
     return whole + (whole > 0 && part < 0.02 ? 0.0 : part <= 0.5 ? 0.55 : 1.0);
   };
-  const double thin_rows = experts * ceil(per / kThinRows);
-  const double short_rows = experts * ceil(per / kShortRows);
+  const double few_tiles = experts * ceil(per / kFewRows);
+  const double thin_tiles = experts * ceil(per / kThinRows);
+  const double short_tiles = experts * ceil(per / kShortRows);
   // in rounds, a light last tile counts half; counts that scatter leave light tiles more than their mean
   const double s_rest = fmod(per, kShortRows), t_rest = fmod(per, kTallRows);
   const double short_cost =
@@ -192,15 +197,25 @@ int int8_tile_rows(int64_t T, int k, int E, int e_loc, int d, int d_ff) {
   const double tall_cost =
       experts * fmax(1.0, floor(per / kTallRows) + (t_rest > 128 ? 1.0 : t_rest > kTallMerge ? 0.5 : 0.0));
   const double tall_more = per > 512 ? fmin(0.3, 0.04 * experts) : 0.0;
-  double thin = 0, shorter = 0, tall = 0;
+  double few = 0, thin = 0, shorter = 0, tall = 0;
   for (int i = 0; i < 2; ++i) {
-    const int N = i ? d : d_ff;
-    const double st = int8_kblocks(i ? d_ff : d), cols = (N + (i ? 255 : 127)) / (i ? 256 : 128);
-    const double thin_groups = thin_rows * ((N + (i ? 63 : 31)) / (i ? 64 : 32));
-    thin += 5 + fmax(0.1 * st, thin_groups * st * 6e3 / 8.5e6) + thin_groups / (3 * cus) * 1.5;
-    shorter += short_rows * cols <= cus ? 7 + 0.4 * st : 6 + rounds(short_cost * cols / (2 * cus)) * (1.05 * st + 0.8);
-    tall += 4 + (rounds(tall_cost * cols / cus) + tall_more) * 0.8 * (st + 18);
+    const int K = i ? d_ff : d, N = i ? d : d_ff;
+    const double st = int8_kblocks(K), cols = (N + (i ? 255 : 127)) / (i ? 256 : 128);
+    const double least = experts * K * N * (i ? 1.0 : 2.0) / 6.6e6;
+    const int few_cols = int8_few_columns(T, k, e_loc, N, i == 0);
+    const double few_groups = few_tiles * ((N + few_cols - 1) / few_cols), fills = few_groups / (3 * cus);
+    const double quantized = fmin(per, kFewRows);  // rows of a workgroup
+    const double turns = int8_few_waves(T, k, E, K) ? ceil(quantized / 4) : quantized;
+    const double block = few_cols * (i ? 64 : 128);  // bytes of a workgroup's K-block
+    few += 3 + fmax(fmax((block > 2048 ? 0.1 : 0.06) * st, few_groups * st * block / 8.5e6) + 1.5 * fills +
+                        fmax(1.0, 1.3 * fills) * turns * (0.6 + K / 4096.0), least);
+    const double thin_groups = thin_tiles * ((N + (i ? 63 : 31)) / (i ? 64 : 32));
+    thin += 6 + fmax(fmax(0.12 * st, thin_groups * st * 6e3 / 8.5e6) + 1.5 * thin_groups / (3 * cus), least);
+    const double s = short_cost * cols / (2 * cus);
+    shorter += short_tiles * cols <= cus ? 7 + fmax(0.4 * st, least) : 6 + fmax(rounds(s) * (1.05 * st + 0.8), least);
+    tall += 4 + fmax((rounds(tall_cost * cols / cus) + tall_more) * 0.8 * (st + 18), least);
   }
+  if (few <= fmin(thin, fmin(shorter, tall)) && rows <= 64 && int8_few_fits(T, d > d_ff ? d : d_ff)) return kFewRows;
   // a thin launch's grid holds every tile there could be: a share that might get far more rows takes another
   const int64_t n_max = T * (k < e_loc ? k : e_loc);
   if (thin <= fmin(shorter, tall) && max_row_tiles(n_max, e_loc, kThinRows) <= kThinTiles) return kThinRows;

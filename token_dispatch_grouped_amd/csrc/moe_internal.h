@@ -145,6 +145,8 @@ int int8_kblocks(int K);
 int64_t int8_max_k();  // int32 sums of 127 * 127 * K, and rows held in registers
 // the local rows (through perm, or in order with perm == nullptr) as codes and scales; with plan (of
 // int8_plan_bytes), the list of row tiles of int8_tile_rows that launch_grouped_gemm_int8 walks is written there too
+// (kInt8FewRows: launch_int8_few takes the call instead)
+constexpr int kInt8FewRows = 16;
 int int8_tile_rows(int64_t T, int k, int E, int e_loc, int d, int d_ff);
 size_t int8_plan_bytes(int64_t n_max, int e_loc);
 hipError_t launch_quantize_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale,
@@ -161,10 +163,12 @@ hipError_t launch_int8_thin(const void* a, const float* a_scale, const void* w, 
                             const void* plan, int e_loc, int K, int N, int64_t n_max, bool swiglu, hipStream_t stream);
 
 // The same FFN for a few tokens, in two launches that quantise their own rows (h: n_max rows of d_ff, bf16)
-bool int8_few(int64_t T, int k, int E, int d, int d_ff);
+int int8_few_columns(int64_t T, int k, int e_loc, int N, bool swiglu);
+bool int8_few_waves(int64_t T, int k, int E, int K);
+bool int8_few_fits(int64_t T, int K);
 hipError_t launch_int8_few(const void* x, const int32_t* perm, const int32_t* offsets, const void* q_gu,
                            const float* s_gu, const void* q_dn, const float* s_dn, void* h, void* y, int d, int d_ff,
-                           int e_begin, int e_loc, int k, int64_t T, int64_t n_max, hipStream_t stream);
+                           int E, int e_begin, int e_loc, int k, int64_t T, int64_t n_max, hipStream_t stream);
 
 size_t grad_norm_workspace_bytes(int n);
 hipError_t launch_grad_norm(const moe_tensor* t, int n, float* norm, void* ws, hipStream_t stream);
