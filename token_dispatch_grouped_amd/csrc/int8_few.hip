@@ -10,9 +10,9 @@
 // K each and ask for their weights, straight into registers, before anything else.
 // While those are on their way the workgroup quantises its rows (each workgroup of an
 // expert does so again: a few KB from L2 next to its 100 KB of weights). 32 tokens x 4 of
-// 128 experts of 2880 x 2880: 310 us, 2.0 GB of weights at 6.5 TB/s; one token of 4 of 32
-// experts of 1000 x 1480: 12.5 us, of which half is the latency of its two launches' chains
-// of loads (offsets, row ids, rows).
+// 128 experts of 2880 x 2880: 306 us, 2.0 GB of weights at 6.6 TB/s; one token of 4 of 32
+// experts of 1000 x 1480: 6.0 + 4.8 us for 18 MB, bound by its chains of loads (offsets, row
+// ids, rows, then the product).
 // v_mfma_i32_16x16x64_i8: 16 channels x 64 K values of the K-blocked weights are one
 // contiguous KB, lane L's 16 bytes at (L & 15) * 64 + (L >> 4) * 16. Integer sums are
 // exact, so the quarters of K are joined in any order with the same bits.
