@@ -119,7 +119,7 @@ def test_every_row_shape(d, dt, wdt):
     _backward(case, dt, wdt, s, mean, rstd, bias=False, ds=False)
 
 
-@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 511, 512, 513, 1500, 4099])
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 127, 255, 300, 511, 512, 513, 1500, 2047, 2048, 4099])
 @pytest.mark.parametrize("d", [64, 136, 640, 2880])
 def test_row_counts(T, d):
     case = _make(T, d, "bf16", "f32", seed=T + d)

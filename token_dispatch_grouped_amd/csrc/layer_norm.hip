@@ -111,7 +111,7 @@ __global__ __launch_bounds__(block_threads<G>()) void layer_norm_kernel(
 // The gradient. Workgroups walk rows with a fixed stride and keep their columns'
 // sums of dy * h and dy in registers; each leaves one fp32 row of both in
 // `partial` [gridDim.x][2][d], added in a fixed order by the kernel below (no
-// atomics: the same bits every time). There are only two workgroups per CU (more
+// atomics: the same bits every time). There are one or two workgroups per CU (more
 // would leave more partial rows), so each asks for its next row before it reduces
 // the present one.
 template <bool BF16, int VPT>
@@ -297,6 +297,20 @@ unsigned row_blocks(int64_t T, int64_t most) {
 }
 
 constexpr int kBackwardBlocks = 512;  // partial rows at most
+
+// Workgroups (and partial rows) of the gradient. Two per CU where every one then has four turns or more:
+// a partial row is 2 d fp32 values written and read again, and a workgroup of one or two turns has
+// nothing to prefetch. Of bf16, two, one and half a workgroup per CU: 256 x 2880 9.7, 9.7, 8.5 us; 777 x 2880 15.1,
+// 12.1, 12.9; 2048 x 2880 17.5, 17.9, 24.6; 16384 x 2880 69, 100, 183. One per CU is as many as fit (and
+// prefetch) where a row has more than 768 vectors: 2048 x 7168 33, 28, 37; 12000 x 8192 137, 133, 210.
+template <int G>
+unsigned backward_blocks(int64_t T, int row_vec) {
+  const int64_t turns = row_blocks<G>(T, int64_t{1} << 30);  // of one workgroup alone
+  if (turns >= 4 * kBackwardBlocks && row_vec <= 768) return kBackwardBlocks;
+  const int64_t most = turns / 2 < 128 ? 128 : turns / 2 < 256 ? turns / 2 : 256;
+  return static_cast<unsigned>(turns < most ? turns : most);
+}
+
 constexpr int64_t kForwardBlocks = int64_t{1} << 21;  // a launch holds fewer than 2^32 threads; rows past it take turns
 
 // F(G, VPT) for a row of row_vec vectors. A row that no more than half fills its threads wastes
@@ -387,7 +401,7 @@ hipError_t launch_layer_norm_backward(const void* dy, const void* s, const void*
                      static_cast<const uint4*>(ds), static_cast<uint4*>(dx), partial, T, row_vec, inv_d)
 #define MOE_NORM_BWD(B, W, G, VPT)                   \
   do {                                               \
-    blocks = row_blocks<G>(T, kBackwardBlocks);      \
+    blocks = backward_blocks<G>(T, row_vec);         \
     if (big) MOE_NORM_BWD_S(B, W, G, VPT, true);     \
     else MOE_NORM_BWD_S(B, W, G, VPT, false);        \
   } while (0)
