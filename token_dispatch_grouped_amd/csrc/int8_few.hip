@@ -45,6 +45,7 @@ struct Weights {
   int lo, hi;           // this wave's K-blocks, a quarter of all
   uint32_t off[FRAGS];
   i32x4 b[AHEAD][FRAGS];
+  float scale[FRAGS];   // of this lane's channels, for the end
 
   __device__ Weights(const uint8_t* w, int e, int n0, int kblocks, int N) {
     const int lane = lane_id(), wv = uniform(static_cast<int>(threadIdx.x) / kWave);
@@ -58,6 +59,10 @@ struct Weights {
       const int col = min(n0 + 16 * (f % NO) + (lane & 15), N - 1);  // channels past N are read again and not stored
       off[f] = static_cast<uint32_t>(col + (f >= NO ? N : 0)) * 64u + static_cast<uint32_t>(lane >> 4) * 16u;
     }
+  }
+  __device__ void load_scales(const float* __restrict__ w_scale, int e) {
+#pragma unroll
+    for (int f = 0; f < FRAGS; ++f) scale[f] = w_scale[e * (block_bytes / 64) + off[f] / 64];
   }
   __device__ void load(int kb0) {
 #pragma unroll
@@ -74,7 +79,7 @@ struct Weights {
 // part: [wave][RT * FRAGS][lane], lane l's element j of a block is row (l >> 4) * 4 + j,
 // channel l & 15; a thread takes one element of every block.
 template <bool SWIGLU, int FRAGS, int RT>
-__device__ __forceinline__ void finish(const i32x4* part, const float* row_scale, const float* __restrict__ w_scale,
+__device__ __forceinline__ void finish(const i32x4* part, const float* row_scale, const float* w_scale,
                                        __bf16* __restrict__ out, int64_t r0, int rows, int n0, int N) {
   constexpr int NO = SWIGLU ? FRAGS / 2 : FRAGS;
   const int lane = lane_id(), j = static_cast<int>(threadIdx.x) / kWave;
@@ -94,8 +99,8 @@ __device__ __forceinline__ void finish(const i32x4* part, const float* row_scale
     for (int f = 0; f < NO; ++f) {
       const int col = n0 + 16 * f + (lane & 15);
       if (col < N) {
-        float v = sum(t, f) * w_scale[col] * sa;
-        if constexpr (SWIGLU) v = gemm::silu_fast(v) * (sum(t, f + NO) * w_scale[N + col] * sa);
+        float v = sum(t, f) * w_scale[f] * sa;
+        if constexpr (SWIGLU) v = gemm::silu_fast(v) * (sum(t, f + NO) * w_scale[f + NO] * sa);
         out[(r0 + row) * N + col] = static_cast<__bf16>(v);
       }
     }
@@ -131,6 +136,7 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
     const int n0 = static_cast<int>(blockIdx.x) * 16 * Wt::NO;
     Wt wt(w, e, n0, kblocks, N);
     wt.load(wt.lo);
+    wt.load_scales(w_scale, e);
     __builtin_amdgcn_sched_barrier(0);  // in flight before anything else
 
     // the rows' codes
@@ -189,7 +195,7 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
 #pragma unroll
     for (int f = 0; f < FRAGS; ++f) part[(wv * FRAGS + f) * kWave + lane] = acc[f];
     __syncthreads();
-    finish<SWIGLU, FRAGS, 1>(part, scales, w_scale + e * (wt.block_bytes / 64), out, r0, R, n0, N);
+    finish<SWIGLU, FRAGS, 1>(part, scales, wt.scale, out, r0, R, n0, N);
     r0 += static_cast<int>(gridDim.z) * tile;
     if (r0 >= end) break;
     __syncthreads();  // the next turn writes the codes, scales and sums again
@@ -233,6 +239,7 @@ __global__ __launch_bounds__(kThreads, 3) void int8_thin_kernel(
     wt.load(kb0);
   };
   load(wt.lo);
+  wt.load_scales(w_scale, g.expert);
   if (tid < R) scales[tid] = a_scale[r0 + tid];
   i32x4 acc[RT][FRAGS];
 #pragma unroll
@@ -256,7 +263,7 @@ __global__ __launch_bounds__(kThreads, 3) void int8_thin_kernel(
 #pragma unroll
     for (int f = 0; f < FRAGS; ++f) part[((wv * RT + t) * FRAGS + f) * kWave + lane] = acc[t][f];
   __syncthreads();
-  finish<SWIGLU, FRAGS, RT>(part, scales, w_scale + g.expert * (wt.block_bytes / 64), out, r0, R, n0, N);
+  finish<SWIGLU, FRAGS, RT>(part, scales, wt.scale, out, r0, R, n0, N);
 }
 
 template <bool SWIGLU, int FRAGS, int AHEAD, int G>
