@@ -139,7 +139,7 @@ CASES = [
     W("i8_few_wide", 8, 512, 2056, 64, 4, 0, 64, "bf16", 79),   # enough channels for the wide workgroups
     W("i8_few_long_k", 1, 64, 8712, 2, 1, 0, 2, "bf16", 80),    # more of a row than its threads hold
     W("i8_few_twelve", 96, 200, 136, 8, 1, 0, 8, "bf16", 85),   # twelve rows per expert, four at a time
-    W("i8_few_share", 300, 136, 264, 64, 1, 8, 24, "bf16", 86, 2.0),  # skewed: some experts take several turns
+    W("i8_few_share", 128, 136, 264, 64, 1, 8, 24, "bf16", 86, 2.0),  # skewed: some experts take several turns
     W("i8_few_full", 16, 64, 3008, 4, 1, 0, 4, "bf16", 87),     # sixteen rows, all of the LDS
     W("i8_few_longest", 1, 64, 48904, 2, 1, 0, 2, "bf16", 88),  # one row, all of the LDS
     W("i8_few_wide_rows", 2, 2056, 8200, 8, 8, 0, 8, "bf16", 89),  # two long rows, one after the other

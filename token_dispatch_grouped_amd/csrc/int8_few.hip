@@ -26,6 +26,7 @@ using namespace int8;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
+constexpr int kFewTokens = 128;  // of a call at most
 constexpr int kHeld = 4;    // vectors of a row a thread holds between its two passes
 constexpr int kMaxCodes = 48 * 1024 - 128;  // with the sums 64 KB, and two workgroups a CU at least
 
@@ -273,10 +274,12 @@ hipError_t launch_one(const void* src, const int32_t* perm, const int32_t* offse
   constexpr int cols = 16 * (SWIGLU ? FRAGS / 2 : FRAGS);
   const int kblocks = int8_kblocks(K);
   const int rows = few_rows(T);
-  // workgroups for twice the rows that uniform routing gives an expert; they take turns for more
-  const int64_t twice = min((2 * T * k + E - 1) / E, T);
+  // Workgroups for twice the rows that uniform routing gives an expert, and no fewer than a quarter of what
+  // one could get: an expert with more takes up to four turns, and few workgroups are empty (128 tokens,
+  // 64 experts of 1024 x 1024: all on one expert 56 us in four turns, 96 in eight; spread 35 either way).
+  const int64_t likely = min(max((2 * T * k + E - 1) / E, (T + 3) / 4), T);
   const dim3 grid(static_cast<unsigned>((N + cols - 1) / cols), static_cast<unsigned>(e_loc),
-                  static_cast<unsigned>((twice + rows - 1) / rows));
+                  static_cast<unsigned>((likely + rows - 1) / rows));
   hipLaunchKernelGGL((int8_few_kernel<SWIGLU, FRAGS, AHEAD, G>), grid, dim3(kThreads),
                      static_cast<unsigned>(rows * code_stride(kblocks)), stream, static_cast<const uint4*>(src), perm,
                      offsets, static_cast<const uint8_t*>(w), w_scale, static_cast<__bf16*>(out), e_begin, k, T, K / 8,
@@ -321,8 +324,12 @@ bool int8_few_waves(int64_t T, int k, int E, int K) {
   return K * static_cast<int64_t>(E) <= kHeld * kWave * 8 * max(T * k, static_cast<int64_t>(E));
 }
 
-// whether the codes of a workgroup's rows fit its LDS
-bool int8_few_fits(int64_t T, int K) { return few_rows(T) * code_stride(int8_kblocks(K)) <= kMaxCodes; }
+// Whether the codes of a workgroup's rows fit its LDS; and not too many tokens, whatever their number per
+// expert, as all of them may go to one (512 tokens, 64 experts of 1024 x 1024: all on one expert 70 us,
+// thin 20; spread 49 both).
+bool int8_few_fits(int64_t T, int K) {
+  return T <= kFewTokens && few_rows(T) * code_stride(int8_kblocks(K)) <= kMaxCodes;
+}
 
 hipError_t launch_int8_few(const void* x, const int32_t* perm, const int32_t* offsets, const void* q_gu,
                            const float* s_gu, const void* q_dn, const float* s_dn, void* h, void* y, int d, int d_ff,
