@@ -257,6 +257,39 @@ def test_no_local_rows_and_no_tokens():
     assert y.shape == (w0.n_max, 64)
 
 
+@pytest.mark.parametrize("d,f", [(1160, 2360), (200, 520)])
+def test_a_row_has_the_same_bits_in_any_batch(d, f):
+    """The same tokens for one expert: one at a time, in a few, and among many (other workgroups each time)."""
+    x = g.to_dev(mi.hidden_states(W("i8_bits", 1360, d, f, 1, 1, 0, 1, "bf16", 90)), "bf16")
+    wgu, wdn = (g.to_dev(a, "bf16") for a in mi.expert_weights(W("i8_bits", 8, d, f, 1, 1, 0, 1, "bf16", 90)))
+    experts = moe.quantize_experts(wgu, wdn)
+
+    def run(n):
+        perm = torch.arange(n, dtype=torch.int32, device="cuda")
+        return moe.grouped_gemm_int8(x[:n], perm, torch.tensor([0, n], dtype=torch.int32, device="cuda"), experts, 1, 1,
+                                     0, 1)
+
+    most = run(1360)
+    for n in (1, 2, 5, 16, 40, 100, 272, 700):
+        assert torch.equal(run(n), most[:n]), n
+
+
+def test_a_row_has_the_same_bits_in_the_tallest_tiles():
+    E, rows, d, f = 5, 272, 1160, 2360
+    T = E * rows
+    x = g.to_dev(mi.hidden_states(W("i8_bits", T, d, f, E, 1, 0, E, "bf16", 91)), "bf16")
+    wgu, wdn = (g.to_dev(a, "bf16") for a in mi.expert_weights(W("i8_bits", 8, d, f, E, 1, 0, E, "bf16", 91)))
+    perm = torch.arange(T, dtype=torch.int32, device="cuda")
+    offsets = torch.arange(0, T + 1, rows, dtype=torch.int32, device="cuda")
+    every = moe.grouped_gemm_int8(x, perm, offsets, moe.quantize_experts(wgu, wdn), 1, E, 0, E)
+    ends = torch.tensor([0, 16], dtype=torch.int32, device="cuda")
+    for e in range(E):
+        one = moe.quantize_experts(wgu[e:e + 1].contiguous(), wdn[e:e + 1].contiguous())
+        for r in (e * rows, e * rows + 100, (e + 1) * rows - 16):
+            few = moe.grouped_gemm_int8(x[r:r + 16].contiguous(), perm[:16], ends, one, 1, 1, 0, 1)
+            assert torch.equal(few, every[r:r + 16]), (e, r)
+
+
 def test_streams_repeats_and_shared_inputs():
     w = CASES[2]
     x, lg, wgu, wdn = _inputs(w)
