@@ -15,7 +15,7 @@
 // The order of K inside a fragment is free as long as A and B agree; both take the
 // bytes 16 * (lane / 32) .. + 15 of a 32-byte slice.
 //
-// Two shapes of workgroup (int8_tile_rows says when; a third, for few rows, is in int8_few.hip):
+// Two shapes of workgroup (int8_tile_rows says when; two more, for few rows, are in int8_few.hip):
 //   tall   BM = 256 (288 where a remainder of up to 32 rows rides along), one workgroup
 //          per CU with all of its LDS: five stages (four with 288 rows). For experts with
 //          many rows: each byte brought to a CU is used by the most products.
