@@ -340,7 +340,8 @@ moe_status moe_route_topk_backward(const moe_shape* s, const int32_t* topk_idx,
  *   x        [T, d] dt, read only.
  *   residual [T, d] dt, read only, or NULL.
  *   weight   [d] wdt, bias [d] wdt or NULL; wdt is dt or MOE_F32.
- *   y        [T, d] dt, written. May be x or residual.
+ *   y        [T, d] dt, written. May be x or residual. With y = x and no residual
+ *            the rows s that moe_layer_norm_backward reads are gone after the call.
  *   sum      [T, d] dt, written when residual is given (then required, ignored
  *            otherwise). May be x or residual, not y.
  *   mean, rstd [T] fp32, written (4-byte aligned).

@@ -803,7 +803,9 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s
                stream=None):
     """(y, s, mean, rstd): s = x + residual (x itself without one), normalised to
     y = (s - mean) * rstd * weight + bias, with fp32 statistics [T]. weight and
-    bias [d] are of x's dtype or fp32. y may be x or residual, and so may s."""
+    bias [d] are of x's dtype or fp32. y may be x or residual, and so may s. With
+    y = x and no residual, the rows that were normalised are overwritten: s is
+    None, and there is nothing for layer_norm_backward to start from."""
     torch = _torch()
     T, d = size = _rows(x, "x")
     _norm_params(x, weight, bias, d)
@@ -815,6 +817,8 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s
     _like(mean, "mean", torch.float32, (T,))
     _like(rstd, "rstd", torch.float32, (T,))
     h, ctx = _ready(stream, (x, weight, bias, residual, y, s), (mean, rstd))
+    if residual is None and not (y is not None and T > 0 and y.data_ptr() == x.data_ptr()):
+        s = x
     sh = moe_shape(T, d, 8, 1, 1, 0, 1)
     with ctx:
         if y is None:
@@ -826,9 +830,10 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s
         if rstd is None:
             rstd = torch.empty(T, dtype=torch.float32, device=x.device)
         _check(_load().moe_layer_norm(ctypes.byref(sh), _CODES[x.dtype], x.data_ptr(), _addr(residual),
-                                      _CODES[weight.dtype], weight.data_ptr(), _addr(bias), eps, y.data_ptr(), _addr(s),
-                                      mean.data_ptr(), rstd.data_ptr(), h), "moe_layer_norm")
-    return y, x if residual is None else s, mean, rstd
+                                      _CODES[weight.dtype], weight.data_ptr(), _addr(bias), eps, y.data_ptr(),
+                                      None if residual is None else s.data_ptr(), mean.data_ptr(), rstd.data_ptr(), h),
+               "moe_layer_norm")
+    return y, s, mean, rstd
 
 
 def layer_norm_backward_workspace_bytes(T: int, d: int) -> int:
