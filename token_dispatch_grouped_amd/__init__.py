@@ -2,7 +2,8 @@
 
 Thin ctypes marshalling over libmoe.so (include/moe.h). Every step of the path
 runs in the library's HIP kernels; PyTorch only provides device memory and the
-current stream. There is no fallback: if the library is missing, importing the
+current stream. With its `stream` argument, a call runs on that stream and what
+it allocates (results, workspaces) belongs to it. There is no fallback: if the library is missing, importing the
 binding works only for introspection (`lib_path`, `declared_symbols`) and every
 compute call raises.
 
@@ -170,12 +171,6 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
-def _stream(stream=None):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
-
-
 def _dtype_code(t) -> int:
     torch = _torch()
     if t.dtype == torch.bfloat16:
@@ -218,11 +213,37 @@ def _want(t, name: str, dtype=None, shape=None, min_rows=None):
 
 
 class _SameStream:
+    """The caller's own stream."""
+
     def __enter__(self):
         return self
 
     def __exit__(self, *exc):
         return False
+
+    def give(self, *ts):
+        pass
+
+
+class _OnStream:
+    """Another stream made current: what is allocated inside belongs to it."""
+
+    def __init__(self, stream, caller):
+        self._ctx, self._caller = _torch().cuda.stream(stream), caller
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+    def give(self, *ts):
+        """What the call returns: once the caller's stream has waited, it may use these
+        and free them, before the uses have run."""
+        for t in ts:
+            if t is not None and self._caller is not None:
+                t.record_stream(self._caller)
 
 
 _SAME = _SameStream()
@@ -231,44 +252,49 @@ _SAME = _SameStream()
 def _place(stream, ts):
     """Where a call on the GPU tensors `ts` runs: (stream handle, context), on
     `stream` or their GPU's current stream. The context makes both the GPU and the
-    stream current, so that memory allocated inside belongs to that stream. Tensors
-    that come from another stream are recorded on it, so that freeing them early
-    does not hand their memory out while the call still runs."""
+    stream current, so that memory allocated inside belongs to that stream. The
+    tensors that the call is given are recorded on a stream other than the current
+    one, so that freeing them early does not hand their memory out while it runs."""
     torch = _torch()
     devices = set(map(torch.Tensor.get_device, ts))
     index = devices.pop()
     if devices or index < 0:
         _dev(*ts)
         raise ValueError(f"every tensor must be on one GPU, got GPUs {sorted({index, *devices})}")
-    if stream is None and index == torch.cuda.current_device():
+    if index == torch.cuda.current_device():
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
-        return (raw(index) if raw else torch.cuda.current_stream(index).cuda_stream), _SAME
+        here = raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
+        if stream is None or (stream.cuda_stream == here and stream.device_index == index):
+            return here, _SAME
     dev = ts[0].device
     current = torch.cuda.current_stream(dev)
-    if stream is None:
-        stream = current
-    elif stream.device != dev:
+    if stream is None or stream == current:
+        return current.cuda_stream, _OnStream(current, None)
+    if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    if stream != current:
-        for t in ts:
-            t.record_stream(stream)
-    return stream.cuda_stream, torch.cuda.stream(stream)
+    for t in ts:
+        t.record_stream(stream)
+    return stream.cuda_stream, _OnStream(stream, current)
+
+
+def _dense(stream, ts):
+    """_place after checking that every tensor (None: not given) is dense and on the GPU."""
+    ts = [t for t in ts if t is not None]
+    if not all(map(_torch().Tensor.is_contiguous, ts)):
+        _dev(*ts)
+    return _place(stream, ts)
 
 
 def _ready(stream, vectors, others=()):
-    """_place after checking that every tensor (None: not given) is dense and on the
-    GPU, and that `vectors`, which move in 16-byte pieces, start at such a boundary."""
+    """_dense after checking that `vectors`, which move in 16-byte pieces, start at such
+    a boundary."""
     ts = [t for t in vectors if t is not None]
     low = 0
     for t in ts:
         low |= t.data_ptr()
-    n = len(ts)
-    ts += [t for t in others if t is not None]
-    if not all(map(_torch().Tensor.is_contiguous, ts)):
-        _dev(*ts)
-    placed = _place(stream, ts)
+    placed = _dense(stream, [*ts, *others])
     if low & 15:
-        bad = next(t for t in ts[:n] if t.data_ptr() & 15)
+        bad = next(t for t in ts if t.data_ptr() & 15)
         raise ValueError(f"a tensor of shape {list(bad.shape)} does not start at a 16-byte boundary")
     return placed
 
@@ -331,14 +357,16 @@ def route_topk(logits, k: int, topk_idx=None, topk_w=None, stream=None):
         _want(topk_idx, "topk_idx", torch.int32, (T, k))
     if topk_w is not None:
         _want(topk_w, "topk_w", torch.float32, (T, k))
-    _dev(logits, topk_idx, topk_w)
-    if topk_idx is None:
-        topk_idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    st, ctx = _dense(stream, (logits, topk_idx, topk_w))
     s = shape(T, 8, 8, E, k, 0, E)
-    _check(_load().moe_route_topk(ctypes.byref(s), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _stream(stream)),
-           "moe_route_topk")
+    with ctx:
+        if topk_idx is None:
+            topk_idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        if topk_w is None:
+            topk_w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        ctx.give(topk_idx, topk_w)
+        _check(_load().moe_route_topk(ctypes.byref(s), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), st),
+               "moe_route_topk")
     return topk_idx, topk_w
 
 
@@ -391,13 +419,13 @@ def _check_dispatch(out: Dispatch, x, T: int, k: int, E: int, n_max: int, gather
         raise ValueError(f"workspace must hold at least {need} bytes, got {out.workspace.numel()}")
 
 
-def _debug_word(out: Dispatch, E: int, stream) -> None:
-    """Debug mode: wait for the dispatch, then refuse ids outside [0, E)."""
+def _debug_word(out: Dispatch, E: int) -> None:
+    """Debug mode: wait for the dispatch on the current stream, then refuse ids outside [0, E)."""
     torch = _torch()
     off = int(_load().moe_dispatch_debug_word_offset())
     if off == _SIZE_MAX:
         return
-    (stream if stream is not None else torch.cuda.current_stream()).synchronize()
+    torch.cuda.current_stream().synchronize()
     bad = int(out.workspace[off:off + 4].view(torch.int32).item())
     if bad:
         raise ValueError(f"moe_dispatch: topk_idx holds {bad} expert id(s) outside [0, {E})")
@@ -420,21 +448,24 @@ def dispatch(x, topk_idx, E: int, e_begin: int, e_end: int, out: Dispatch | None
     n_max = _n_max(T, k, e_begin, e_end)
     if out is not None:
         _check_dispatch(out, x, T, k, E, n_max, gather)
-    _dev(x, topk_idx)
-    if out is None:
-        out = dispatch_alloc(x, k, E, e_begin, e_end, gather=gather)
-    _dev(out.counts, out.offsets, out.perm, out.pair_pos, out.x_perm if gather else None, out.workspace)
+    st, ctx = _dense(stream, (x, topk_idx) if out is None else
+                     (x, topk_idx, out.counts, out.offsets, out.perm, out.pair_pos, out.x_perm if gather else None,
+                      out.workspace))
     s = shape(T, d, 8, E, k, e_begin, e_end)
-    if gather:
-        _check(_load().moe_dispatch(ctypes.byref(s), _dtype_code(x), _ptr(x), _ptr(topk_idx), _ptr(out.counts),
-                                    _ptr(out.offsets), _ptr(out.perm), _ptr(out.pair_pos), _ptr(out.x_perm),
-                                    _ptr(out.workspace), _stream(stream)), "moe_dispatch")
-    else:
-        _check(_load().moe_dispatch_indices(ctypes.byref(s), _ptr(topk_idx), _ptr(out.counts), _ptr(out.offsets),
-                                            _ptr(out.perm), _ptr(out.pair_pos), _ptr(out.workspace),
-                                            _stream(stream)), "moe_dispatch_indices")
-    if _debug:
-        _debug_word(out, E, stream)
+    with ctx:
+        if out is None:
+            out = dispatch_alloc(x, k, E, e_begin, e_end, gather=gather)
+        ctx.give(out.counts, out.offsets, out.perm, out.pair_pos, out.x_perm, out.workspace)
+        if gather:
+            _check(_load().moe_dispatch(ctypes.byref(s), _dtype_code(x), _ptr(x), _ptr(topk_idx), _ptr(out.counts),
+                                        _ptr(out.offsets), _ptr(out.perm), _ptr(out.pair_pos), _ptr(out.x_perm),
+                                        _ptr(out.workspace), st), "moe_dispatch")
+        else:
+            _check(_load().moe_dispatch_indices(ctypes.byref(s), _ptr(topk_idx), _ptr(out.counts), _ptr(out.offsets),
+                                                _ptr(out.perm), _ptr(out.pair_pos), _ptr(out.workspace), st),
+                   "moe_dispatch_indices")
+        if _debug:
+            _debug_word(out, E)
     return out
 
 
@@ -453,23 +484,26 @@ def dispatch_indices_noalloc(topk_idx, E: int, e_begin: int, e_end: int, counts,
     _want(offsets, "offsets", torch.int32, (E + 1,))
     _want(perm, "perm", torch.int32, (T * k,))
     _want(pair_pos, "pair_pos", torch.int32, (T * k,))
-    _dev(topk_idx, counts, offsets, perm, pair_pos)
+    st, ctx = _dense(stream, (topk_idx, counts, offsets, perm, pair_pos))
     s = shape(T, 8, 8, E, k, e_begin, e_end)
-    _check(_load().moe_dispatch_indices_noalloc(ctypes.byref(s), _ptr(topk_idx), _ptr(counts), _ptr(offsets),
-                                                _ptr(perm), _ptr(pair_pos), _stream(stream)),
-           "moe_dispatch_indices_noalloc")
+    with ctx:
+        _check(_load().moe_dispatch_indices_noalloc(ctypes.byref(s), _ptr(topk_idx), _ptr(counts), _ptr(offsets),
+                                                    _ptr(perm), _ptr(pair_pos), st), "moe_dispatch_indices_noalloc")
+
+
+def _check_gemm_outputs(h, y, n_max: int, d: int, d_ff: int, dtype) -> None:
+    if h is not None:
+        _want(h, "h", dtype, (n_max, d_ff), min_rows=n_max)
+    if y is not None:
+        _want(y, "y", dtype, (n_max, d), min_rows=n_max)
 
 
 def _gemm_outputs(h, y, n_max: int, d: int, d_ff: int, dtype, device):
     torch = _torch()
     if h is None:
         h = torch.empty((n_max, d_ff), dtype=dtype, device=device)
-    else:
-        _want(h, "h", dtype, (n_max, d_ff), min_rows=n_max)
     if y is None:
         y = torch.empty((n_max, d), dtype=dtype, device=device)
-    else:
-        _want(y, "y", dtype, (n_max, d), min_rows=n_max)
     return h, y
 
 
@@ -486,15 +520,17 @@ def grouped_gemm(x_perm, offsets, w_gate_up, w_down, T: int, k: int, E: int, e_b
     _want(x_perm, "x_perm", x_perm.dtype, (n_max, d), min_rows=n_max)
     _want(offsets, "offsets", torch.int32, (E + 1,))
     d_ff = _expert_weights(w_gate_up, w_down, x_perm.dtype, d, e_begin, e_end)
-    h, y = _gemm_outputs(h, y, n_max, d, d_ff, x_perm.dtype, x_perm.device)
-    _dev(x_perm, offsets, w_gate_up, w_down, h, y)
+    _check_gemm_outputs(h, y, n_max, d, d_ff, x_perm.dtype)
+    st, ctx = _dense(stream, (x_perm, offsets, w_gate_up, w_down, h, y))
     s = shape(T, d, d_ff, E, k, e_begin, e_end)
     dt = _dtype_code(x_perm)
     ws_bytes = _load().moe_grouped_gemm_workspace_bytes(ctypes.byref(s), dt)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x_perm.device) if ws_bytes else None
-    _check(_load().moe_grouped_gemm(ctypes.byref(s), dt, _ptr(x_perm), _ptr(offsets), _ptr(w_gate_up),
-                                    _ptr(w_down), _ptr(h), _ptr(y), _ptr(ws), _stream(stream)),
-           "moe_grouped_gemm")
+    with ctx:
+        h, y = _gemm_outputs(h, y, n_max, d, d_ff, x_perm.dtype, x_perm.device)
+        ctx.give(h, y)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x_perm.device) if ws_bytes else None
+        _check(_load().moe_grouped_gemm(ctypes.byref(s), dt, _ptr(x_perm), _ptr(offsets), _ptr(w_gate_up),
+                                        _ptr(w_down), _ptr(h), _ptr(y), _ptr(ws), st), "moe_grouped_gemm")
     return h, y
 
 
@@ -514,22 +550,25 @@ def grouped_gemm_gather(x, perm, offsets, w_gate_up, w_down, k: int, E: int, e_b
     _want(perm, "perm", torch.int32, (T * k,))
     _want(offsets, "offsets", torch.int32, (E + 1,))
     d_ff = _expert_weights(w_gate_up, w_down, x.dtype, d, e_begin, e_end)
-    h, y = _gemm_outputs(h, y, n_max, d, d_ff, x.dtype, x.device)
+    _check_gemm_outputs(h, y, n_max, d, d_ff, x.dtype)
     if gu is not None:
         _want(gu, "gu", x.dtype, (n_max, 2 * d_ff), min_rows=n_max)
-    _dev(x, perm, offsets, w_gate_up, w_down, h, y, gu)
+    st, ctx = _dense(stream, (x, perm, offsets, w_gate_up, w_down, h, y, gu))
     s = shape(T, d, d_ff, E, k, e_begin, e_end)
     dt = _dtype_code(x)
     ws_bytes = _load().moe_grouped_gemm_workspace_bytes(ctypes.byref(s), dt)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device) if ws_bytes else None
-    if gu is None:
-        _check(_load().moe_grouped_gemm_gather(ctypes.byref(s), dt, _ptr(x), _ptr(perm), _ptr(offsets),
-                                               _ptr(w_gate_up), _ptr(w_down), _ptr(h), _ptr(y), _ptr(ws),
-                                               _stream(stream)), "moe_grouped_gemm_gather")
-    else:
-        _check(_load().moe_grouped_gemm_gather_save(ctypes.byref(s), dt, _ptr(x), _ptr(perm), _ptr(offsets),
-                                                    _ptr(w_gate_up), _ptr(w_down), _ptr(h), _ptr(y), _ptr(gu),
-                                                    _ptr(ws), _stream(stream)), "moe_grouped_gemm_gather_save")
+    with ctx:
+        h, y = _gemm_outputs(h, y, n_max, d, d_ff, x.dtype, x.device)
+        ctx.give(h, y)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device) if ws_bytes else None
+        if gu is None:
+            _check(_load().moe_grouped_gemm_gather(ctypes.byref(s), dt, _ptr(x), _ptr(perm), _ptr(offsets),
+                                                   _ptr(w_gate_up), _ptr(w_down), _ptr(h), _ptr(y), _ptr(ws), st),
+                   "moe_grouped_gemm_gather")
+        else:
+            _check(_load().moe_grouped_gemm_gather_save(ctypes.byref(s), dt, _ptr(x), _ptr(perm), _ptr(offsets),
+                                                        _ptr(w_gate_up), _ptr(w_down), _ptr(h), _ptr(y), _ptr(gu),
+                                                        _ptr(ws), st), "moe_grouped_gemm_gather_save")
     return h, y
 
 
@@ -547,12 +586,14 @@ def combine(y, pair_pos, topk_w, T: int, k: int, E: int, e_begin: int, e_end: in
     _want(topk_w, "topk_w", torch.float32, (T, k))
     if out is not None:
         _want(out, "out", y.dtype, (T, d))
-    _dev(y, pair_pos, topk_w, out)
-    if out is None:
-        out = torch.empty((T, d), dtype=y.dtype, device=y.device)
+    st, ctx = _dense(stream, (y, pair_pos, topk_w, out))
     s = shape(T, d, 8, E, k, e_begin, e_end)
-    _check(_load().moe_combine(ctypes.byref(s), _dtype_code(y), _ptr(y), _ptr(pair_pos), _ptr(topk_w),
-                               _ptr(out), _stream(stream)), "moe_combine")
+    with ctx:
+        if out is None:
+            out = torch.empty((T, d), dtype=y.dtype, device=y.device)
+        ctx.give(out)
+        _check(_load().moe_combine(ctypes.byref(s), _dtype_code(y), _ptr(y), _ptr(pair_pos), _ptr(topk_w),
+                                   _ptr(out), st), "moe_combine")
     return out
 
 
@@ -580,7 +621,10 @@ def layer(x, logits, w_gate_up, w_down, k: int, e_begin: int, e_end: int, stream
     if fused:
         if save:
             e_loc, d_ff = w_down.shape[0], w_down.shape[1]
-            gu = torch.empty((T * min(k, e_loc), 2 * d_ff), dtype=x.dtype, device=x.device)
+            _, ctx = _dense(stream, (x,))
+            with ctx:
+                gu = torch.empty((T * min(k, e_loc), 2 * d_ff), dtype=x.dtype, device=x.device)
+                ctx.give(gu)
         h, y = grouped_gemm_gather(x, disp.perm, disp.offsets, w_gate_up, w_down, k, E, e_begin, e_end,
                                    stream=stream, gu=gu)
     else:
@@ -628,15 +672,16 @@ def combine_backward(d_out, y, pair_pos, topk_w, T: int, k: int, E: int, e_begin
         _want(d_y, "d_y", d_out.dtype, (n_max, d), min_rows=n_max)
     if d_topk_w is not None:
         _want(d_topk_w, "d_topk_w", torch.float32, (T, k))
-    _dev(d_out, y, pair_pos, topk_w, d_y, d_topk_w)
-    if d_y is None:
-        d_y = torch.empty_like(y)
-    if d_topk_w is None:
-        d_topk_w = torch.empty((T, k), dtype=torch.float32, device=d_out.device)
+    st, ctx = _dense(stream, (d_out, y, pair_pos, topk_w, d_y, d_topk_w))
     s = shape(T, d, 8, E, k, e_begin, e_end)
-    _check(_load().moe_combine_backward(ctypes.byref(s), _dtype_code(d_out), _ptr(d_out), _ptr(y), _ptr(pair_pos),
-                                        _ptr(topk_w), _ptr(d_y), _ptr(d_topk_w), _stream(stream)),
-           "moe_combine_backward")
+    with ctx:
+        if d_y is None:
+            d_y = torch.empty_like(y)
+        if d_topk_w is None:
+            d_topk_w = torch.empty((T, k), dtype=torch.float32, device=d_out.device)
+        ctx.give(d_y, d_topk_w)
+        _check(_load().moe_combine_backward(ctypes.byref(s), _dtype_code(d_out), _ptr(d_out), _ptr(y), _ptr(pair_pos),
+                                            _ptr(topk_w), _ptr(d_y), _ptr(d_topk_w), st), "moe_combine_backward")
     return d_y, d_topk_w
 
 
@@ -678,26 +723,30 @@ def grouped_gemm_backward(x, perm, offsets, w_gate_up, w_down, h, d_y, k: int, E
         _want(workspace, "workspace", torch.uint8)
         if workspace.numel() < ws_bytes:
             raise ValueError(f"workspace must hold at least {ws_bytes} bytes, got {workspace.numel()}")
-    _dev(x, perm, offsets, w_gate_up, w_down, h, d_y, d_x_perm, d_w_gate_up, d_w_down, gu, workspace)
-    if d_x_perm is None:
-        d_x_perm = torch.empty((n_max, d), dtype=dt_, device=x.device)
-    if d_w_gate_up is None:
-        d_w_gate_up = torch.empty_like(w_gate_up)
-    if d_w_down is None:
-        d_w_down = torch.empty_like(w_down)
-    ws = workspace
-    if ws is None:
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device) if ws_bytes else None
-    if gu is None:
-        _check(_load().moe_grouped_gemm_backward(ctypes.byref(s), dt, _ptr(x), _ptr(perm), _ptr(offsets),
-                                                 _ptr(w_gate_up), _ptr(w_down), _ptr(h), _ptr(d_y), _ptr(d_x_perm),
-                                                 _ptr(d_w_gate_up), _ptr(d_w_down), _ptr(ws), _stream(stream)),
-               "moe_grouped_gemm_backward")
-    else:
-        _check(_load().moe_grouped_gemm_backward_saved(ctypes.byref(s), dt, _ptr(x), _ptr(perm), _ptr(offsets),
-                                                       _ptr(w_gate_up), _ptr(w_down), _ptr(h), _ptr(gu), _ptr(d_y),
-                                                       _ptr(d_x_perm), _ptr(d_w_gate_up), _ptr(d_w_down), _ptr(ws),
-                                                       _stream(stream)), "moe_grouped_gemm_backward_saved")
+    st, ctx = _dense(stream, (x, perm, offsets, w_gate_up, w_down, h, d_y, d_x_perm, d_w_gate_up, d_w_down, gu,
+                              workspace))
+    with ctx:
+        if d_x_perm is None:
+            d_x_perm = torch.empty((n_max, d), dtype=dt_, device=x.device)
+        if d_w_gate_up is None:
+            d_w_gate_up = torch.empty_like(w_gate_up)
+        if d_w_down is None:
+            d_w_down = torch.empty_like(w_down)
+        ctx.give(d_x_perm, d_w_gate_up, d_w_down)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device) if ws_bytes else None
+        if gu is None:
+            _check(_load().moe_grouped_gemm_backward(ctypes.byref(s), dt, _ptr(x), _ptr(perm), _ptr(offsets),
+                                                     _ptr(w_gate_up), _ptr(w_down), _ptr(h), _ptr(d_y),
+                                                     _ptr(d_x_perm), _ptr(d_w_gate_up), _ptr(d_w_down), _ptr(ws), st),
+                   "moe_grouped_gemm_backward")
+        else:
+            _check(_load().moe_grouped_gemm_backward_saved(ctypes.byref(s), dt, _ptr(x), _ptr(perm), _ptr(offsets),
+                                                           _ptr(w_gate_up), _ptr(w_down), _ptr(h), _ptr(gu),
+                                                           _ptr(d_y), _ptr(d_x_perm), _ptr(d_w_gate_up),
+                                                           _ptr(d_w_down), _ptr(ws), st),
+                   "moe_grouped_gemm_backward_saved")
     return d_x_perm, d_w_gate_up, d_w_down
 
 
@@ -714,12 +763,14 @@ def dispatch_backward(d_x_perm, pair_pos, T: int, k: int, E: int, e_begin: int, 
     _want(pair_pos, "pair_pos", torch.int32, (T * k,))
     if d_x is not None:
         _want(d_x, "d_x", d_x_perm.dtype, (T, d))
-    _dev(d_x_perm, pair_pos, d_x)
-    if d_x is None:
-        d_x = torch.empty((T, d), dtype=d_x_perm.dtype, device=d_x_perm.device)
+    st, ctx = _dense(stream, (d_x_perm, pair_pos, d_x))
     s = shape(T, d, 8, E, k, e_begin, e_end)
-    _check(_load().moe_dispatch_backward(ctypes.byref(s), _dtype_code(d_x_perm), _ptr(d_x_perm), _ptr(pair_pos),
-                                         _ptr(d_x), _stream(stream)), "moe_dispatch_backward")
+    with ctx:
+        if d_x is None:
+            d_x = torch.empty((T, d), dtype=d_x_perm.dtype, device=d_x_perm.device)
+        ctx.give(d_x)
+        _check(_load().moe_dispatch_backward(ctypes.byref(s), _dtype_code(d_x_perm), _ptr(d_x_perm), _ptr(pair_pos),
+                                             _ptr(d_x), st), "moe_dispatch_backward")
     return d_x
 
 
@@ -736,12 +787,14 @@ def route_topk_backward(topk_idx, topk_w, d_topk_w, E: int, d_logits=None, strea
     _want(d_topk_w, "d_topk_w", torch.float32, (T, k))
     if d_logits is not None:
         _want(d_logits, "d_logits", torch.float32, (T, E))
-    _dev(topk_idx, topk_w, d_topk_w, d_logits)
-    if d_logits is None:
-        d_logits = torch.empty((T, E), dtype=torch.float32, device=topk_idx.device)
+    st, ctx = _dense(stream, (topk_idx, topk_w, d_topk_w, d_logits))
     s = shape(T, 8, 8, E, k, 0, E)
-    _check(_load().moe_route_topk_backward(ctypes.byref(s), _ptr(topk_idx), _ptr(topk_w), _ptr(d_topk_w),
-                                           _ptr(d_logits), _stream(stream)), "moe_route_topk_backward")
+    with ctx:
+        if d_logits is None:
+            d_logits = torch.empty((T, E), dtype=torch.float32, device=topk_idx.device)
+        ctx.give(d_logits)
+        _check(_load().moe_route_topk_backward(ctypes.byref(s), _ptr(topk_idx), _ptr(topk_w), _ptr(d_topk_w),
+                                               _ptr(d_logits), st), "moe_route_topk_backward")
     return d_logits
 
 
@@ -829,6 +882,7 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s
             mean = torch.empty(T, dtype=torch.float32, device=x.device)
         if rstd is None:
             rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        ctx.give(y, s, mean, rstd)
         _check(_load().moe_layer_norm(ctypes.byref(sh), _CODES[x.dtype], x.data_ptr(), _addr(residual),
                                       _CODES[weight.dtype], weight.data_ptr(), _addr(bias), eps, y.data_ptr(),
                                       None if residual is None else s.data_ptr(), mean.data_ptr(), rstd.data_ptr(), h),
@@ -874,6 +928,7 @@ def layer_norm_backward(d_y, s, weight, mean, rstd, d_s=None, bias: bool = True,
             d_weight = torch.empty_like(weight)
         if d_bias is None and bias:
             d_bias = torch.empty_like(weight)
+        ctx.give(d_x, d_weight, d_bias)
         if workspace is None and ws_bytes:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=d_y.device)
         _check(_load().moe_layer_norm_backward(ctypes.byref(sh), _CODES[d_y.dtype], d_y.data_ptr(), s.data_ptr(),
@@ -938,6 +993,7 @@ def quantize_experts(w_gate_up, w_down, out: Int8Experts | None = None, stream=N
                               torch.empty((e_loc, 2 * d_ff), dtype=torch.float32, device=dev),
                               torch.empty((e_loc, _kblocks(d_ff), d, 64), dtype=torch.int8, device=dev),
                               torch.empty((e_loc, d), dtype=torch.float32, device=dev))
+        ctx.give(out.w_gate_up, out.gate_up_scale, out.w_down, out.down_scale)
         _check(_load().moe_quantize_experts(ctypes.byref(s), _dtype_code(w_down), _ptr(w_gate_up), _ptr(w_down),
                                             _ptr(out.w_gate_up), _ptr(out.gate_up_scale), _ptr(out.w_down),
                                             _ptr(out.down_scale), h), "moe_quantize_experts")
@@ -974,6 +1030,7 @@ def grouped_gemm_int8(x, perm, offsets, experts: Int8Experts, k: int, E: int, e_
     with ctx:
         if y is None:
             y = torch.empty((n_max, d), dtype=x.dtype, device=x.device)
+        ctx.give(y)
         if workspace is None and ws_bytes:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
         _check(_load().moe_grouped_gemm_int8(ctypes.byref(s), MOE_BF16, x.data_ptr(), perm.data_ptr(),
@@ -1029,14 +1086,6 @@ def _host_list(ts, numels, kinds):
     return array.array("q", flat)
 
 
-def _list_ready(stream, ts, *others):
-    """_place for a list of gradients (aligned to their elements only) and its buffers."""
-    all_ = ts + [t for t in others if t is not None]
-    if not all(map(_torch().Tensor.is_contiguous, all_)):
-        _dev(*all_)
-    return _place(stream, all_)
-
-
 def grad_norm_workspace_bytes(n: int) -> int:
     return int(_load().moe_grad_norm_workspace_bytes(n))
 
@@ -1071,11 +1120,12 @@ def grad_norm(grads, norm=None, workspace=None, stream=None):
     torch = _torch()
     ts, numels, kinds = _tensor_list(grads, "grads")
     need = _norm_buffers(len(ts), norm, workspace)
-    h, ctx = _list_ready(stream, ts, norm, workspace)
+    h, ctx = _dense(stream, [*ts, norm, workspace])
     src = _host_list(ts, numels, kinds)
     with ctx:
         if norm is None:
             norm = torch.empty(1, dtype=torch.float32, device=ts[0].device)
+        ctx.give(norm)
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=ts[0].device)
         _check(_load().moe_grad_norm(src.buffer_info()[0], len(ts), norm.data_ptr(), workspace.data_ptr(), h),
@@ -1090,7 +1140,7 @@ def clip_grads(grads, norm, max_norm: float, out=None, stream=None) -> None:
     ts, numels, kinds = _tensor_list(grads, "grads")
     outs = _clip_out(ts, out)
     _want(norm, "norm", torch.float32, (1,))
-    h, ctx = _list_ready(stream, ts + outs, norm)
+    h, ctx = _dense(stream, [*ts, *outs, norm])
     src = _host_list(ts, numels, kinds)
     dst = _host_list(outs, numels, kinds) if outs else None
     with ctx:
@@ -1104,12 +1154,13 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm=None, workspace=None, 
     ts, numels, kinds = _tensor_list(grads, "grads")
     outs = _clip_out(ts, out)
     need = _norm_buffers(len(ts), norm, workspace)
-    h, ctx = _list_ready(stream, ts + outs, norm, workspace)
+    h, ctx = _dense(stream, [*ts, *outs, norm, workspace])
     src = _host_list(ts, numels, kinds)
     dst = _host_list(outs, numels, kinds) if outs else None
     with ctx:
         if norm is None:
             norm = torch.empty(1, dtype=torch.float32, device=ts[0].device)
+        ctx.give(norm)
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=ts[0].device)
         _check(_load().moe_clip_grad_norm(src.buffer_info()[0], dst.buffer_info()[0] if outs else None, len(ts),
