@@ -162,8 +162,8 @@ def _torch():
     global _TORCH
     if _TORCH is None:
         import torch
-        _TORCH = torch
         _CODES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16})
+        _TORCH = torch  # last: another thread's call that finds it finds the table filled
     return _TORCH
 
 
