@@ -333,6 +333,12 @@ def _range(E: int, k: int, e_begin: int, e_end: int) -> None:
 
 
 def shape(T, d, d_ff, E, k, e_begin, e_end) -> moe_shape:
+    """The sizes as the library takes them: T in 64 bits, the others in 32 (ctypes by
+    itself would take a size modulo 2^32)."""
+    if max(d, d_ff, E, k, e_begin, e_end) > 0x7FFFFFFF or min(d, d_ff, E, k, e_begin, e_end) < -0x80000000:
+        raise ValueError(f"sizes must fit 32 bits, got {dict(d=d, d_ff=d_ff, E=E, k=k, e_begin=e_begin, e_end=e_end)}")
+    if not -(1 << 63) <= T < 1 << 63:
+        raise ValueError(f"T must fit 64 bits, got {T}")
     return moe_shape(int(T), int(d), int(d_ff), int(E), int(k), int(e_begin), int(e_end))
 
 
@@ -869,10 +875,10 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, y=None, s
     _like(s, "s", x.dtype, size)
     _like(mean, "mean", torch.float32, (T,))
     _like(rstd, "rstd", torch.float32, (T,))
+    sh = shape(T, d, 8, 1, 1, 0, 1)
     h, ctx = _ready(stream, (x, weight, bias, residual, y, s), (mean, rstd))
     if residual is None and not (y is not None and T > 0 and y.data_ptr() == x.data_ptr()):
         s = x
-    sh = moe_shape(T, d, 8, 1, 1, 0, 1)
     with ctx:
         if y is None:
             y = torch.empty_like(x)
@@ -914,7 +920,7 @@ def layer_norm_backward(d_y, s, weight, mean, rstd, d_s=None, bias: bool = True,
     _like(d_bias, "d_bias", weight.dtype, (d,))
     if d_bias is not None and not bias:
         raise ValueError("d_bias is written only with bias")
-    sh = moe_shape(T, d, 8, 1, 1, 0, 1)
+    sh = shape(T, d, 8, 1, 1, 0, 1)
     ws_bytes = _load().moe_layer_norm_backward_workspace_bytes(ctypes.byref(sh))
     if workspace is not None:
         _want(workspace, "workspace", torch.uint8)
@@ -984,8 +990,8 @@ def quantize_experts(w_gate_up, w_down, out: Int8Experts | None = None, stream=N
     if out is not None:
         _want_int8_experts(out, d, e_loc)
     mine = () if out is None else (out.w_gate_up, out.gate_up_scale, out.w_down, out.down_scale)
-    h, ctx = _ready(stream, (w_gate_up, w_down, *mine[::2]), mine[1::2])
     s = shape(0, d, d_ff, max(e_loc, 1), 1, 0, e_loc)
+    h, ctx = _ready(stream, (w_gate_up, w_down, *mine[::2]), mine[1::2])
     dev = w_down.device
     with ctx:
         if out is None:
@@ -1019,7 +1025,7 @@ def grouped_gemm_int8(x, perm, offsets, experts: Int8Experts, k: int, E: int, e_
     d_ff = _want_int8_experts(experts, d, e_end - e_begin)
     if y is not None:
         _want(y, "y", x.dtype, (n_max, d), min_rows=n_max)
-    s = moe_shape(T, d, d_ff, E, k, e_begin, e_end)
+    s = shape(T, d, d_ff, E, k, e_begin, e_end)
     ws_bytes = _load().moe_grouped_gemm_int8_workspace_bytes(ctypes.byref(s))
     if workspace is not None:
         _want(workspace, "workspace", torch.uint8)
