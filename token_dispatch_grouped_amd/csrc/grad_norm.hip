@@ -253,6 +253,11 @@ hipError_t sum_squares(const moe_tensor* t, int n, bool big, double* partial, in
   return hipSuccess;
 }
 
+hipError_t join_partials(const double* partial, int count, float* norm, hipStream_t stream) {
+  hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(kThreads), 0, stream, partial, count, norm);
+  return hipGetLastError();
+}
+
 hipError_t scale_all(const moe_tensor* t, const moe_tensor* out, int n, bool big, const double* partial, int count, float* norm,
                      float max_norm, hipStream_t stream) {
   int i0 = 0;
@@ -283,8 +288,7 @@ hipError_t launch_grad_norm(const moe_tensor* t, int n, float* norm, void* ws, h
   int count = 0;
   hipError_t e = sum_squares(t, n, stream_list(t, n, 1), static_cast<double*>(ws), &count, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(kThreads), 0, stream, static_cast<const double*>(ws), count, norm);
-  return hipGetLastError();
+  return join_partials(static_cast<const double*>(ws), count, norm, stream);
 }
 
 hipError_t launch_clip_grads(const moe_tensor* t, const moe_tensor* out, int n, const float* norm, float max_norm,
@@ -292,13 +296,22 @@ hipError_t launch_clip_grads(const moe_tensor* t, const moe_tensor* out, int n, 
   return scale_all(t, out, n, stream_list(t, n, out == t ? 1 : 2), nullptr, 0, const_cast<float*>(norm), max_norm, stream);
 }
 
+// The clip's workgroups join the partial sums themselves, which saves a launch, as long as there are no
+// more than one launch's worth. There are as many workgroups as partial sums, so their reads would grow
+// with the square of a list that takes many launches, and those are joined once, by a launch of its own
+// (tensors of 1 MB, joined by every workgroup and once: 65 of them 95 us both, 1000 1652 and 1332, 4096
+// 12.0 ms and 5.3).
 hipError_t launch_clip_grad_norm(const moe_tensor* t, const moe_tensor* out, int n, float max_norm, float* norm,
                                  void* ws, hipStream_t stream) {
   int count = 0;
   const bool big = stream_list(t, n, out == t ? 1 : 2);
-  const hipError_t e = sum_squares(t, n, big, static_cast<double*>(ws), &count, stream);
+  hipError_t e = sum_squares(t, n, big, static_cast<double*>(ws), &count, stream);
   if (e != hipSuccess) return e;
-  return scale_all(t, out, n, big, static_cast<const double*>(ws), count, norm, max_norm, stream);
+  if (count <= kNormBlocks)
+    return scale_all(t, out, n, big, static_cast<const double*>(ws), count, norm, max_norm, stream);
+  e = join_partials(static_cast<const double*>(ws), count, norm, stream);
+  if (e != hipSuccess) return e;
+  return scale_all(t, out, n, big, nullptr, 0, norm, max_norm, stream);
 }
 
 }  // namespace moe
