@@ -23,6 +23,8 @@ namespace {
 
 using namespace rows;
 
+constexpr int kMaxD = 32768;
+
 template <int G>
 constexpr int block_threads() { return G > 256 ? G : 256; }
 
@@ -32,6 +34,7 @@ __global__ __launch_bounds__(block_threads<G>()) void layer_norm_kernel(
     const uint4* x, const uint4* r, const void* __restrict__ w, const void* __restrict__ b, float eps, uint4* y,
     uint4* s, float* __restrict__ mean, float* __restrict__ rstd, int64_t T, int row_vec) {
   using V = Vec16<BF16>;
+  static_assert(G * VPT * V::kN <= kMaxD, "no row is that long");
   constexpr int kRows = block_threads<G>() / G;  // rows per workgroup
   __shared__ float lds[2][G > kWave ? G / kWave : 1];
   const float d = static_cast<float>(row_vec * V::kN);
@@ -126,6 +129,7 @@ __global__ __launch_bounds__(block_threads<G>()) void layer_norm_backward_kernel
     const float* __restrict__ rstd, const uint4* ds, uint4* dx, float* __restrict__ partial, int64_t T, int row_vec,
     float inv_d) {
   using V = Vec16<BF16>;
+  static_assert(G * VPT * V::kN <= kMaxD, "no row is that long");
   constexpr int kRows = block_threads<G>() / G;
   // the next row and the weights stay in registers where there is room for them
   constexpr bool kAhead = G <= 512;
@@ -313,7 +317,7 @@ unsigned backward_blocks(int64_t T, int row_vec) {
 
 constexpr int64_t kForwardBlocks = int64_t{1} << 21;  // a launch holds fewer than 2^32 threads; rows past it take turns
 
-// F(G, VPT) for a row of row_vec vectors. A row that no more than half fills its threads wastes
+// F(G, VPT) for a row of up to 4096 vectors, as many as bf16 rows have; longer fp32 rows take 1024 x 8. A row that no more than half fills its threads wastes
 // their loads, hence the steps between powers of two (16384 x 1032 bf16, three vectors of a wave against
 // one of a workgroup: forward 26 us against 30, gradient 32 against 45; 16384 x 4104, gradient 112
 // against 142). Rows past 16384 bf16 elements run the gradient at 2.3 TB/s (16384 x 32768): their column sums do
@@ -330,8 +334,7 @@ constexpr int64_t kForwardBlocks = int64_t{1} << 21;  // a launch holds fewer th
   else if (row_vec <= 1024) F(256, 4); \
   else if (row_vec <= 1536) F(512, 3); \
   else if (row_vec <= 2048) F(512, 4); \
-  else if (row_vec <= 4096) F(1024, 4); \
-  else F(1024, 8)
+  else F(1024, 4)
 
 #define MOE_NORM_BWD_SHAPES(F)         \
   if (row_vec <= 16) F(16, 1);         \
@@ -345,12 +348,11 @@ constexpr int64_t kForwardBlocks = int64_t{1} << 21;  // a launch holds fewer th
   else if (row_vec <= 1024) F(512, 2); \
   else if (row_vec <= 1536) F(512, 3); \
   else if (row_vec <= 2048) F(1024, 2); \
-  else if (row_vec <= 4096) F(1024, 4); \
-  else F(1024, 8)
+  else F(1024, 4)
 
 }  // namespace
 
-int64_t layer_norm_max_d() { return 32768; }
+int64_t layer_norm_max_d() { return kMaxD; }
 
 hipError_t launch_layer_norm(const void* x, const void* r, const void* w, const void* b, float eps, void* y, void* s,
                              float* mean, float* rstd, int64_t T, int d, bool bf16, bool wbf16, hipStream_t stream) {
@@ -372,6 +374,7 @@ hipError_t launch_layer_norm(const void* x, const void* r, const void* w, const 
 #define MOE_NORM_FF(G, VPT) MOE_NORM(false, false, G, VPT)
   if (bf16 && wbf16) { MOE_NORM_SHAPES(MOE_NORM_BB); }
   else if (bf16) { MOE_NORM_SHAPES(MOE_NORM_BF); }
+  else if (row_vec > 4096) MOE_NORM_FF(1024, 8);
   else { MOE_NORM_SHAPES(MOE_NORM_FF); }
 #undef MOE_NORM_BB
 #undef MOE_NORM_BF
@@ -410,6 +413,7 @@ hipError_t launch_layer_norm_backward(const void* dy, const void* s, const void*
 #define MOE_NORM_BWD_FF(G, VPT) MOE_NORM_BWD(false, false, G, VPT)
     if (bf16 && wbf16) { MOE_NORM_BWD_SHAPES(MOE_NORM_BWD_BB); }
     else if (bf16) { MOE_NORM_BWD_SHAPES(MOE_NORM_BWD_BF); }
+    else if (row_vec > 4096) MOE_NORM_BWD_FF(1024, 8);
     else { MOE_NORM_BWD_SHAPES(MOE_NORM_BWD_FF); }
 #undef MOE_NORM_BWD_BB
 #undef MOE_NORM_BWD_BF
