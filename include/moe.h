@@ -345,7 +345,9 @@ moe_status moe_route_topk_backward(const moe_shape* s, const int32_t* topk_idx,
  *   sum      [T, d] dt, written when residual is given (then required, ignored
  *            otherwise). May be x or residual, not y.
  *   mean, rstd [T] fp32, written (4-byte aligned).
- * A row with an infinity or NaN gets NaN. Uses s->T and s->d only (E, k and the
+ * A row with an infinity or NaN gets NaN. The fp32 mean is off by some units of its
+ * last place, which shows in y where a row's deviations from it are no larger: a
+ * constant row gives the bias exactly in bf16 only. Uses s->T and s->d only (E, k and the
  * local range are not looked at). MOE_EINVAL for eps negative or not finite;
  * MOE_EUNSUPPORTED for d > 32768 or wdt = MOE_BF16 with dt = MOE_F32. */
 moe_status moe_layer_norm(const moe_shape* s, moe_dtype dt, const void* x, const void* residual,

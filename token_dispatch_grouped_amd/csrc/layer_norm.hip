@@ -77,7 +77,10 @@ __global__ __launch_bounds__(block_threads<G>()) void layer_norm_kernel(
 #pragma unroll
       for (int i = 0; i < V::kN; ++i) sum += f[i];
     }
-    const float m = group_reduce<G, Sum>(sum, lds[0]) / d;  // a quotient: a constant row's mean is that constant
+    // A quotient, so that a constant row of bf16 has that constant as its mean: d values of 8 significant bits
+    // add up exactly in 24. A sum of fp32 values rounds, and so does its quotient: a few units of the last
+    // place (7168 times 1000.1: 1000.10004).
+    const float m = group_reduce<G, Sum>(sum, lds[0]) / d;
     float var = 0.f;
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
