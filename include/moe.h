@@ -349,7 +349,7 @@ moe_status moe_route_topk_backward(const moe_shape* s, const int32_t* topk_idx,
  * last place, which shows in y where a row's deviations from it are no larger: a
  * constant row gives the bias exactly in bf16 only. Uses s->T and s->d only (E, k and the
  * local range are not looked at). MOE_EINVAL for eps negative or not finite;
- * MOE_EUNSUPPORTED for d > 32768 or wdt = MOE_BF16 with dt = MOE_F32. */
+ * MOE_EUNSUPPORTED for d > 32768, T > 2^30 or wdt = MOE_BF16 with dt = MOE_F32. */
 moe_status moe_layer_norm(const moe_shape* s, moe_dtype dt, const void* x, const void* residual,
                           moe_dtype wdt, const void* weight, const void* bias, float eps,
                           void* y, void* sum, float* mean, float* rstd, hipStream_t stream);
@@ -428,7 +428,7 @@ moe_status moe_grouped_gemm_int8(const moe_shape* s, moe_dtype dt, const void* x
  * bits. A list without elements has norm 0. */
 typedef struct {
   void* data;    /* device pointer, aligned to the element */
-  int64_t numel; /* elements, >= 0 (data may be NULL when 0) */
+  int64_t numel; /* elements, >= 0 (data may be NULL when 0); MOE_EUNSUPPORTED past 2^48 */
   moe_dtype dt;
 } moe_tensor;
 

@@ -323,8 +323,9 @@ constexpr int64_t kForwardBlocks = int64_t{1} << 21;  // a launch holds fewer th
 // F(G, VPT) for a row of up to 4096 vectors, as many as bf16 rows have; longer fp32 rows take 1024 x 8. A row that no more than half fills its threads wastes
 // their loads, hence the steps between powers of two (16384 x 1032 bf16, three vectors of a wave against
 // one of a workgroup: forward 26 us against 30, gradient 32 against 45; 16384 x 4104, gradient 112
-// against 142). Rows past 16384 bf16 elements run the gradient at 2.3 TB/s (16384 x 32768): their column sums do
-// not fit the registers of the 1024 threads that one workgroup can have.
+// against 142). Rows past 16384 bf16 elements run the gradient at 2.1-2.3 TB/s (16384 x 32768): beside the row,
+// their column sums do not fit the registers of 1024 threads, and 70 to 100 of them are spilled. Column sums in
+// a second pass over dy and s would move 5/3 of the bytes (with ds 3/2); not tried.
 #define MOE_NORM_SHAPES(F)             \
   if (row_vec <= 16) F(16, 1);         \
   else if (row_vec <= 32) F(32, 1);    \
