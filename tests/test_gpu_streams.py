@@ -137,3 +137,45 @@ def test_a_stream_that_is_current_already():
     torch.cuda.synchronize()
     _same(got, want)
     _same(other, want)
+
+
+def test_captured_on_streams_that_fork_and_join():
+    """Two layers of 8-bit experts on two side streams inside one graph, replayed on fresh inputs."""
+    args = _inputs(W)
+    x, lg, wgu, wdn, norm, _ = args
+    experts = moe.quantize_experts(wgu, wdn)
+    bufs = [(x.clone(), lg.clone()) for _ in range(2)]
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    outs = [None, None]
+
+    def step():
+        here = torch.cuda.current_stream()
+        for i, s in enumerate(sides):
+            s.wait_stream(here)
+            outs[i] = moe.layer_int8(*bufs[i], experts, W.k, 0, W.E, stream=s, norm=norm)["normed"]
+        for s in sides:
+            here.wait_stream(s)
+
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        step()
+    torch.cuda.current_stream().wait_stream(warm)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    captured = list(outs)
+    for i in range(4):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(200 + i)
+        want = []
+        for b in bufs:
+            b[0].copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+            b[1].copy_(torch.randn(lg.shape, generator=gen, device="cuda"))
+            want.append(moe.layer_int8(b[0], b[1], experts, W.k, 0, W.E, norm=norm)["normed"])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, w in zip(captured, want):
+            assert torch.equal(got, w), i

@@ -3,9 +3,9 @@
 Thin ctypes marshalling over libmoe.so (include/moe.h). Every step of the path
 runs in the library's HIP kernels; PyTorch only provides device memory and the
 current stream. With its `stream` argument, a call runs on that stream and what
-it allocates (results, workspaces) belongs to it. There is no fallback: if the library is missing, importing the
-binding works only for introspection (`lib_path`, `declared_symbols`) and every
-compute call raises.
+it allocates (results, workspaces) belongs to it. There is no fallback: if the
+library is missing, importing the binding works only for introspection
+(`lib_path`, `declared_symbols`) and every compute call raises.
 
 Every wrapper checks the dtype and shape of each tensor it is given (inputs and
 caller-provided outputs alike) against the sizes of the call before anything
