@@ -2,8 +2,8 @@
  * moe.h — C ABI of one rank's MoE expert layer on an AMD Instinct MI355X
  * (gfx950): router top-k, token dispatch, grouped expert GEMM with SwiGLU, and
  * the weighted combine, with their gradients; and what stands around the
- * experts: residual add and layer norm, the experts in 8-bit integers, and the
- * gradient norm with clipping.
+ * experts: residual add with layer norm or RMS norm, the experts in 8-bit
+ * integers, the gradient norm with clipping, and the AdamW step.
  *
  * Sources of the operations (page title, then section):
  *   [EP] "Paralelismo de especialistas" (transformers v5.23.0 docs, pt), with
@@ -94,6 +94,53 @@ moe_status moe_expert_range(int32_t E, int32_t ep, int32_t rank,
  * Uses s->T, s->E, s->k only. */
 moe_status moe_route_topk(const moe_shape* s, const float* logits,
                           int32_t* topk_idx, float* topk_w, hipStream_t stream);
+
+/* How moe_route_experts scores and chooses: the routers of models whose experts are
+ * balanced by a bias, chosen by groups, or weighted by other than the softmax over
+ * the chosen logits. */
+typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  moe_score score;
+  int32_t groups;      /* equal blocks of consecutive experts; divides E */
+  int32_t top_groups;  /* groups a token may choose from, 1 <= top_groups <= groups */
+  int32_t group_top;   /* a group is ranked by its largest choice value (1) or by the sum of its two largest (2) */
+  int32_t renormalize; /* weights of a token add up to `scale` (0 or 1) */
+  float scale;         /* finite */
+  const float* bias;   /* [E] fp32 DEVICE array, added to the scores for the choice only; or NULL */
+} moe_router;
+
+/* Routing to experts by scores.
+ *   s_e    = softmax of the token's E logits, or the sigmoid of each
+ *   c_e    = s_e + bias_e, computed in fp64 and rounded to fp32 once; the logit itself
+ *            where there is no bias and groups or group_top is 1
+ *   groups   ranked by their largest c, or the fp32 sum of their two largest (of the
+ *            only one where a group has one expert); the first top_groups stay
+ *   topk_idx the k largest c of the groups that stay, in descending order
+ *   topk_w = scale * s                             without renormalize
+ *          = scale * softmax over the k logits     MOE_SOFTMAX with renormalize
+ *          = scale * s / (sum of the k s + 1e-20)  MOE_SIGMOID with renormalize
+ * Equal values go to the lower id; -0.0 equals +0.0; a NaN comes after every number.
+ * Any logits and biases give k distinct ids of groups that stay. -infinity (of a logit or
+ * a bias) puts an expert behind the others. A token with a NaN or +infinity among its
+ * logits, or with k chosen logits of -infinity, may have NaN weights.
+ *   logits [T, E] fp32, read only; topk_idx [T, k] int32, topk_w [T, k] fp32, written.
+ *   Aligned to 4 bytes. r is a HOST struct, read before the call returns.
+ * Uses s->T, s->E, s->k only. MOE_EINVAL unless k <= top_groups * E / groups. */
+moe_status moe_route_experts(const moe_shape* s, const moe_router* r, const float* logits,
+                             int32_t* topk_idx, float* topk_w, hipStream_t stream);
+
+/* Gradient of moe_route_experts' weights with respect to the logits, for its ids; the
+ * choice passes none, so neither does the bias (r->bias, groups, top_groups and
+ * group_top are not looked at). Every expert that is not chosen gets 0, but for
+ * MOE_SOFTMAX without renormalize, where the scores depend on all logits.
+ *   logits, topk_idx: the forward's. The ids of a token are distinct; one outside
+ *            [0, E) is left out of the sums.
+ *   d_topk_w [T, k] fp32, read only.   d_logits [T, E] fp32, written (every entry).
+ * Logits are finite or -infinity. Computed in fp32. */
+moe_status moe_route_experts_backward(const moe_shape* s, const moe_router* r, const float* logits,
+                                      const int32_t* topk_idx, const float* d_topk_w, float* d_logits,
+                                      hipStream_t stream);
 
 /* Bytes of device workspace moe_dispatch needs for this shape (may be 0). */
 size_t moe_dispatch_workspace_bytes(const moe_shape* s);
@@ -377,6 +424,36 @@ moe_status moe_layer_norm_backward(const moe_shape* s, moe_dtype dt, const void*
                                    const float* rstd, const void* d_s, void* d_x, void* d_weight,
                                    void* d_bias, void* workspace, hipStream_t stream);
 
+/* Residual add and RMS norm of T rows of d elements:
+ *     s    = x + residual, rounded to dt (s = x without a residual)
+ *     rstd = 1 / sqrt(sum(s^2) / d + eps)
+ *     y    = s * rstd * weight
+ * The squares are summed in fp64 (none of a finite row over- or underflows), the rest is
+ * fp32; y rounded once.
+ *   x, residual, weight, y, sum, rstd: as for moe_layer_norm (y may be x or residual, sum
+ *            too; with y = x and no residual the rows that moe_rms_norm_backward reads are
+ *            gone). y may be NULL when q is given.
+ *   q        [ceil(d / 64)][T][64] int8 with q_scale [T] fp32 (4-byte aligned), written, or
+ *            both NULL: the rows in 8 bits, as the experts below take them: codes and scale
+ *            of the fp32 y, before its rounding to dt (MOE_EUNSUPPORTED unless dt = MOE_BF16).
+ * A row with a NaN gets NaN; an infinity gives rstd 0 and so NaN for itself, 0 for the
+ * others, and a scale of NaN. Uses s->T and s->d only. Errors as moe_layer_norm. */
+moe_status moe_rms_norm(const moe_shape* s, moe_dtype dt, const void* x, const void* residual,
+                        moe_dtype wdt, const void* weight, float eps, void* y, void* sum, float* rstd,
+                        void* q, float* q_scale, hipStream_t stream);
+
+/* Bytes of device workspace moe_rms_norm_backward needs (0 when T = 0). */
+size_t moe_rms_norm_backward_workspace_bytes(const moe_shape* s);
+
+/* Gradient of moe_rms_norm (of y). With h = s * rstd and g = weight * d_y:
+ *     d_x      = rstd * (g - h * sum(g * h) / d) + d_s
+ *     d_weight = sum over rows of d_y * h
+ * Arguments as for moe_layer_norm_backward, which has a mean and a bias besides; the same
+ * inputs give the same bits. Errors as moe_layer_norm. */
+moe_status moe_rms_norm_backward(const moe_shape* s, moe_dtype dt, const void* d_y, const void* sum,
+                                 moe_dtype wdt, const void* weight, const float* rstd, const void* d_s,
+                                 void* d_x, void* d_weight, void* workspace, hipStream_t stream);
+
 /* Experts in 8-bit integers. A row a (an activation row, or an output channel's
  * weights) is held as codes q and one fp32 scale:
  *     scale = max(max|a| / 127, 2^-126),  q = rint(a * (1 / scale)),  |q| <= 127
@@ -418,6 +495,14 @@ moe_status moe_grouped_gemm_int8(const moe_shape* s, moe_dtype dt, const void* x
                                  const float* scale_down, void* y, void* workspace,
                                  hipStream_t stream);
 
+/* moe_grouped_gemm_int8 on rows that are in 8 bits already: of token t, the codes q_x
+ * [ceil(d / 64)][T][64] int8 and scale_x [T] fp32 (from moe_rms_norm, or laid out alike,
+ * zero past column d) are gathered through perm in place of quantising x. */
+moe_status moe_grouped_gemm_int8_rows(const moe_shape* s, const void* q_x, const float* scale_x,
+                                      const int32_t* perm, const int32_t* offsets, const void* q_gate_up,
+                                      const float* scale_gate_up, const void* q_down, const float* scale_down,
+                                      void* y, void* workspace, hipStream_t stream);
+
 /* The gradient norm over a list of tensors, and clipping to it. A list is a HOST
  * array of n entries, read before the call returns. Tensors are dense, of any
  * length (0 included) and aligned to their elements only; types may be mixed.
@@ -454,6 +539,54 @@ moe_status moe_clip_grads(const moe_tensor* grads, const moe_tensor* out, int32_
  * norm and workspace are written, and may overlap no tensor of either list. */
 moe_status moe_clip_grad_norm(const moe_tensor* grads, const moe_tensor* out, int32_t n, float max_norm,
                               float* norm, void* workspace, hipStream_t stream);
+
+/* One AdamW step over a list of tensors (a HOST array, read before the call returns):
+ *     g = grad * min(1, max_norm / (norm + 1e-6))          (g = grad without a norm)
+ *     m = beta1 * m + (1 - beta1) * g;  v = beta2 * v + (1 - beta2) * g^2
+ *     p = p * (1 - lr * weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, element by element. A bf16 param is the rounding of its fp32 master where it
+ * has one (the step then reads and writes the master, and writes param), else it is read
+ * and rounded itself.
+ * States are fp32, or (MOE_STATE_E4M3) 8-bit: exp_avg holds m and exp_avg_sq holds sqrt(v)
+ * as e4m3 codes (finite up to 448), with one fp32 scale per block of MOE_STATE_BLOCK
+ * consecutive elements:
+ *     scale = max(max|a| * (1 / 448), 2^-126),  code = e4m3(a * (1 / scale)), nearest, ties to even
+ * and a sqrt(v) above 0 has at least the code of 2^-9, so that no element is divided by eps
+ * alone. The step itself uses the new m and v before they are rounded to codes. A block with
+ * an infinity or NaN gets scale NaN and codes 0. All-zero codes and scales are the state
+ * before the first step.
+ * Tensors are dense, of any length (0 included), aligned to their elements only. */
+#define MOE_STATE_BLOCK 128
+typedef enum { MOE_STATE_F32 = 0, MOE_STATE_E4M3 = 1 } moe_state;
+
+typedef struct {
+  void* param;              /* [numel] param_dt, written (read without a master) */
+  const void* grad;         /* [numel] grad_dt, read only */
+  float* master;            /* [numel] fp32, read and written; NULL for an fp32 param, optional for a bf16 one */
+  void* exp_avg;            /* [numel] fp32 or one byte, read and written */
+  void* exp_avg_sq;         /* [numel] fp32 or one byte, read and written */
+  float* exp_avg_scale;     /* [ceil(numel / MOE_STATE_BLOCK)] fp32, read and written; 8-bit states only */
+  float* exp_avg_sq_scale;  /* the same */
+  int64_t numel;            /* >= 0 (pointers may be NULL when 0); MOE_EUNSUPPORTED past 2^40 */
+  moe_dtype param_dt, grad_dt;
+} moe_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps;  /* lr finite; 0 <= beta < 1; 1e-30 <= eps, finite */
+  double weight_decay;           /* finite; of every tensor without weight_decays */
+  const double* weight_decays;   /* HOST array of n, read before the call returns, or NULL */
+  int64_t step;                  /* >= 1: the number of this step */
+  const float* d_lr;             /* [1] DEVICE values that replace lr and step (a captured graph reads them */
+  const int64_t* d_step;         /*     at each replay), or NULL; a step < 1 there counts as 1 */
+  const float* norm;             /* [1] DEVICE fp32, e.g. from moe_grad_norm; or NULL: no clipping */
+  float max_norm;                /* >= 0, finite; with norm only */
+  moe_state state;
+} moe_adamw_args;
+
+/* MOE_EINVAL if a written tensor overlaps another tensor of the list (of any entry), or
+ * norm, d_lr or d_step. */
+moe_status moe_adamw(const moe_adamw_tensor* tensors, int32_t n, const moe_adamw_args* args,
+                     hipStream_t stream);
 
 #ifdef __cplusplus
 }

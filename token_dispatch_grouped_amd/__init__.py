@@ -34,6 +34,8 @@ _SIZE_MAX = ctypes.c_size_t(-1).value
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP = 0, 1, 2, 3
 MOE_F32, MOE_BF16 = 0, 1
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1
+MOE_STATE_F32, MOE_STATE_E4M3, MOE_STATE_BLOCK = 0, 1, 128
 
 
 class MoeError(RuntimeError):
@@ -59,6 +61,50 @@ class moe_tensor(ctypes.Structure):
         ("data", ctypes.c_void_p),
         ("numel", ctypes.c_int64),
         ("dt", ctypes.c_int),
+    ]
+
+
+class moe_router(ctypes.Structure):
+    _fields_ = [
+        ("score", ctypes.c_int),
+        ("groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("bias", ctypes.c_void_p),
+    ]
+
+
+class moe_adamw_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("exp_avg", ctypes.c_void_p),
+        ("exp_avg_sq", ctypes.c_void_p),
+        ("exp_avg_scale", ctypes.c_void_p),
+        ("exp_avg_sq_scale", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("param_dt", ctypes.c_int),
+        ("grad_dt", ctypes.c_int),
+    ]
+
+
+class moe_adamw_args(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("weight_decays", ctypes.c_void_p),
+        ("step", ctypes.c_int64),
+        ("d_lr", ctypes.c_void_p),
+        ("d_step", ctypes.c_void_p),
+        ("norm", ctypes.c_void_p),
+        ("max_norm", ctypes.c_float),
+        ("state", ctypes.c_int),
     ]
 
 
@@ -89,6 +135,8 @@ def _load():
             "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "moe_expert_range": (ctypes.c_int, [I32, I32, I32, ctypes.POINTER(I32), ctypes.POINTER(I32)]),
             "moe_route_topk": (ctypes.c_int, [S, P, P, P, P]),
+            "moe_route_experts": (ctypes.c_int, [S, ctypes.POINTER(moe_router), P, P, P, P]),
+            "moe_route_experts_backward": (ctypes.c_int, [S, ctypes.POINTER(moe_router), P, P, P, P, P]),
             "moe_dispatch_workspace_bytes": (SZ, [S]),
             "moe_dispatch_debug_word_offset": (SZ, []),
             "moe_dispatch": (ctypes.c_int, [S, ctypes.c_int, P, P, P, P, P, P, P, P, P]),
@@ -110,13 +158,19 @@ def _load():
             "moe_layer_norm_backward_workspace_bytes": (SZ, [S]),
             "moe_layer_norm_backward": (ctypes.c_int,
                                         [S, ctypes.c_int, P, P, ctypes.c_int, P, P, P, P, P, P, P, P, P]),
+            "moe_rms_norm": (ctypes.c_int,
+                             [S, ctypes.c_int, P, P, ctypes.c_int, P, ctypes.c_float, P, P, P, P, P, P]),
+            "moe_rms_norm_backward_workspace_bytes": (SZ, [S]),
+            "moe_rms_norm_backward": (ctypes.c_int, [S, ctypes.c_int, P, P, ctypes.c_int, P, P, P, P, P, P, P]),
             "moe_quantize_experts": (ctypes.c_int, [S, ctypes.c_int, P, P, P, P, P, P, P]),
             "moe_grouped_gemm_int8_workspace_bytes": (SZ, [S]),
             "moe_grouped_gemm_int8": (ctypes.c_int, [S, ctypes.c_int, P, P, P, P, P, P, P, P, P, P]),
+            "moe_grouped_gemm_int8_rows": (ctypes.c_int, [S, P, P, P, P, P, P, P, P, P, P, P]),
             "moe_grad_norm_workspace_bytes": (SZ, [I32]),
             "moe_grad_norm": (ctypes.c_int, [P, I32, P, P, P]),
             "moe_clip_grads": (ctypes.c_int, [P, P, I32, P, ctypes.c_float, P]),
             "moe_clip_grad_norm": (ctypes.c_int, [P, P, I32, ctypes.c_float, P, P, P]),
+            "moe_adamw": (ctypes.c_int, [P, I32, ctypes.POINTER(moe_adamw_args), P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -376,6 +430,74 @@ def route_topk(logits, k: int, topk_idx=None, topk_w=None, stream=None):
     return topk_idx, topk_w
 
 
+@dataclass(frozen=True)
+class Router:
+    """How route_experts scores and chooses. score: "softmax" over all experts or
+    "sigmoid" of each. bias [E] fp32 is added to the scores for the choice only. The
+    experts' `groups` equal blocks are ranked by the sum of their two largest values
+    (group_score "top2") or their largest ("max"), and a token chooses from the first
+    top_groups. With renormalize, a token's weights add up to scale; without, they
+    are scale times the scores."""
+    score: str = "softmax"
+    bias: object = None
+    groups: int = 1
+    top_groups: int = 1
+    group_score: str = "top2"
+    renormalize: bool = True
+    scale: float = 1.0
+
+
+_SCORES = {"softmax": MOE_SOFTMAX, "sigmoid": MOE_SIGMOID}
+_GROUP_TOPS = {"max": 1, "top2": 2}
+
+
+def _router_struct(router: Router) -> moe_router:
+    if router.score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {router.score!r}")
+    if router.group_score not in _GROUP_TOPS:
+        raise ValueError(f"group_score must be one of {sorted(_GROUP_TOPS)}, got {router.group_score!r}")
+    if not abs(router.scale) < 3.4e38:
+        raise ValueError(f"scale must be finite, got {router.scale}")
+    return moe_router(_SCORES[router.score], router.groups, router.top_groups, _GROUP_TOPS[router.group_score],
+                      1 if router.renormalize else 0, router.scale, _addr(router.bias))
+
+
+def route_experts(logits, k: int, router: Router, topk_idx=None, topk_w=None, stream=None):
+    """logits [T, E] fp32 -> (topk_idx [T, k] int32, topk_w [T, k] fp32): the k experts
+    with the largest scores (plus bias) in the groups that stay, ties to the lower
+    id, and their weights."""
+    torch = _torch()
+    _want(logits, "logits", torch.float32)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E], got {list(logits.shape)}")
+    T, E = logits.shape
+    if not (1 <= router.top_groups <= router.groups <= E and E % router.groups == 0):
+        raise ValueError(f"need groups that divide E = {E} and 1 <= top_groups <= groups, got {router.groups} groups, "
+                         f"{router.top_groups} chosen")
+    if not 1 <= k <= router.top_groups * (E // router.groups):
+        raise ValueError(f"need 1 <= k <= {router.top_groups * (E // router.groups)} (the experts of the chosen "
+                         f"groups), got k={k}")
+    _like(router.bias, "bias", torch.float32, (E,))
+    _like(topk_idx, "topk_idx", torch.int32, (T, k))
+    _like(topk_w, "topk_w", torch.float32, (T, k))
+    r = _router_struct(router)
+    st, ctx = _dense(stream, (logits, router.bias, topk_idx, topk_w))
+    s = shape(T, 8, 8, E, k, 0, E)
+    with ctx:
+        if topk_idx is None:
+            topk_idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        if topk_w is None:
+            topk_w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        ctx.give(topk_idx, topk_w)
+        _check(_load().moe_route_experts(ctypes.byref(s), ctypes.byref(r), logits.data_ptr(), topk_idx.data_ptr(),
+                                         topk_w.data_ptr(), st), "moe_route_experts")
+    return topk_idx, topk_w
+
+
+def _route(logits, k: int, router: Router | None, stream):
+    return route_topk(logits, k, stream=stream) if router is None else route_experts(logits, k, router, stream=stream)
+
+
 @dataclass
 class Dispatch:
     counts: object
@@ -604,15 +726,17 @@ def combine(y, pair_pos, topk_w, T: int, k: int, E: int, e_begin: int, e_end: in
 
 
 def layer(x, logits, w_gate_up, w_down, k: int, e_begin: int, e_end: int, stream=None, fused: bool = False,
-          save: bool = False, norm=None) -> dict:
+          save: bool = False, norm=None, router: Router | None = None, residual=None) -> dict:
     """The whole forward of one rank: route -> dispatch -> grouped GEMM -> combine.
     With `fused`, the dispatch writes indices only and the GEMM gathers the rows.
     With `save` (fused path), the gate/up pre-activations are kept in the result
     as "gu", for layer_backward to use instead of recomputing them.
-    With `norm` = (weight, bias or None, eps), out is added to the residual x and
-    normalised (layer_norm): the result has "sum" = x + out, "normed", "mean" and
-    "rstd" as well. On a rank that holds a share of the experts, out is a partial
-    sum over ranks: join the ranks' first and call layer_norm then."""
+    With `norm` = (weight, bias or None, eps), out is added to `residual` (x unless
+    given) and normalised (layer_norm): the result has "sum" = residual + out,
+    "normed", "mean" and "rstd" as well. With `norm` an RmsNorm, by rms_norm ("mean"
+    is None). On a rank that holds a share of the experts, out is a partial sum over
+    ranks: join the ranks' first and normalise then.
+    With `router`, the experts are chosen by route_experts instead of route_topk."""
     torch = _torch()
     T = x.shape[0]
     if logits.dim() != 2 or logits.shape[0] != T:
@@ -620,8 +744,8 @@ def layer(x, logits, w_gate_up, w_down, k: int, e_begin: int, e_end: int, stream
     E = logits.shape[1]
     if save and not fused:
         raise ValueError("save needs the fused path")
-    _check_layer_norm_arg(norm, E, e_begin, e_end)
-    idx, w = route_topk(logits, k, stream=stream)
+    _check_layer_norm_arg(norm, residual, E, e_begin, e_end)
+    idx, w = _route(logits, k, router, stream)
     disp = dispatch(x, idx, E, e_begin, e_end, stream=stream, gather=not fused)
     gu = None
     if fused:
@@ -638,23 +762,38 @@ def layer(x, logits, w_gate_up, w_down, k: int, e_begin: int, e_end: int, stream
     out = combine(y, disp.pair_pos, w, T, k, E, e_begin, e_end, stream=stream)
     res = dict(idx=idx, w=w, counts=disp.counts, offsets=disp.offsets, perm=disp.perm,
                pair_pos=disp.pair_pos, x_perm=disp.x_perm, h=h, y=y, out=out, gu=gu)
-    return _with_norm(res, x, E, e_begin, e_end, norm, stream)
+    if router is not None:
+        res["logits"] = logits
+    return _with_norm(res, x if residual is None else residual, norm, stream)
 
 
-def _check_layer_norm_arg(norm, E: int, e_begin: int, e_end: int):
+@dataclass(frozen=True)
+class RmsNorm:
+    """The RMS norm that a layer's output ends with: weight [d] and eps."""
+    weight: object
+    eps: float = 1e-6
+
+
+def _check_layer_norm_arg(norm, residual, E: int, e_begin: int, e_end: int):
     if norm is None:
+        if residual is not None:
+            raise ValueError("residual is added with norm only")
         return
-    if len(norm) != 3:
-        raise ValueError("norm must be (weight, bias or None, eps)")
+    if not isinstance(norm, RmsNorm) and len(norm) != 3:
+        raise ValueError("norm must be (weight, bias or None, eps) or an RmsNorm")
     if (e_begin, e_end) != (0, E):
         raise ValueError(f"norm needs the whole layer output; experts [{e_begin}, {e_end}) of {E} give a partial sum")
 
 
-def _with_norm(res: dict, x, E: int, e_begin: int, e_end: int, norm, stream) -> dict:
-    if norm is not None:
+def _with_norm(res: dict, residual, norm, stream) -> dict:
+    if isinstance(norm, RmsNorm):
+        res["normed"], res["sum"], res["rstd"] = rms_norm(res["out"], norm.weight, norm.eps, residual=residual,
+                                                          stream=stream)
+        res["mean"] = None
+    elif norm is not None:
         weight, bias, eps = norm
-        res["normed"], res["sum"], res["mean"], res["rstd"] = layer_norm(res["out"], weight, bias, eps, residual=x,
-                                                                         stream=stream)
+        res["normed"], res["sum"], res["mean"], res["rstd"] = layer_norm(res["out"], weight, bias, eps,
+                                                                         residual=residual, stream=stream)
     return res
 
 
@@ -804,22 +943,58 @@ def route_topk_backward(topk_idx, topk_w, d_topk_w, E: int, d_logits=None, strea
     return d_logits
 
 
+def route_experts_backward(logits, topk_idx, d_topk_w, router: Router, d_logits=None, stream=None):
+    """d_logits [T, E] fp32: the gradient of route_experts' weights w.r.t. the logits,
+    for its ids. The choice, and so the bias, passes none."""
+    torch = _torch()
+    _want(logits, "logits", torch.float32)
+    _want(topk_idx, "topk_idx", torch.int32)
+    if logits.dim() != 2 or topk_idx.dim() != 2 or topk_idx.shape[0] != logits.shape[0]:
+        raise ValueError(f"logits must be [T, E] and topk_idx [T, k], got {list(logits.shape)}, {list(topk_idx.shape)}")
+    (T, E), k = logits.shape, topk_idx.shape[1]
+    if not 1 <= k <= E:
+        raise ValueError(f"need 1 <= k <= E, got k={k}, E={E}")
+    _want(d_topk_w, "d_topk_w", torch.float32, (T, k))
+    _like(d_logits, "d_logits", torch.float32, (T, E))
+    r = _router_struct(router)
+    r.bias = None  # not looked at
+    st, ctx = _dense(stream, (logits, topk_idx, d_topk_w, d_logits))
+    s = shape(T, 8, 8, E, k, 0, E)
+    with ctx:
+        if d_logits is None:
+            d_logits = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+        ctx.give(d_logits)
+        _check(_load().moe_route_experts_backward(ctypes.byref(s), ctypes.byref(r), logits.data_ptr(),
+                                                  topk_idx.data_ptr(), d_topk_w.data_ptr(), d_logits.data_ptr(), st),
+               "moe_route_experts_backward")
+    return d_logits
+
+
 def layer_backward(x, w_gate_up, w_down, fwd: dict, d_out, k: int, e_begin: int, e_end: int, stream=None,
-                   norm=None, d_sum=None) -> dict:
+                   norm=None, d_sum=None, router: Router | None = None) -> dict:
     """The whole backward of one rank, given the forward's dict (from layer()):
     combine -> experts -> row gather -> router softmax. The gate/up
     pre-activations come from the forward's "gu" when it kept them.
     With the forward's `norm`, d_out is the gradient of "normed" (and d_sum, if
     given, that of "sum"): the result has "d_norm_weight", "d_norm_bias" (None
-    without a bias) and "d_sum", the gradient of x + out. d_x is then still the
-    gradient through the experts alone; x's whole gradient adds d_sum (the
-    residual) and what comes through the logits."""
+    without a bias) and "d_sum", the gradient of residual + out. d_x is then still
+    the gradient through the experts alone; the residual's gradient (x's, unless
+    the forward was given another) adds d_sum, and x's what comes through the logits.
+    `router` is the forward's."""
+    if (router is None) != ("logits" not in fwd):
+        raise ValueError("router must be the forward's")
     T = x.shape[0]
     E = fwd["counts"].shape[0]
     extra = {}
     if norm is not None:
         if "sum" not in fwd:
             raise ValueError("the forward was run without norm")
+        if isinstance(norm, RmsNorm) != (fwd["mean"] is None):
+            raise ValueError("norm must be the forward's")
+    if isinstance(norm, RmsNorm):
+        d_out, d_nw = rms_norm_backward(d_out, fwd["sum"], norm.weight, fwd["rstd"], d_s=d_sum, stream=stream)
+        extra = dict(d_sum=d_out, d_norm_weight=d_nw, d_norm_bias=None)
+    elif norm is not None:
         weight, bias, _ = norm
         d_out, d_nw, d_nb = layer_norm_backward(d_out, fwd["sum"], weight, fwd["mean"], fwd["rstd"], d_s=d_sum,
                                                 bias=bias is not None, stream=stream)
@@ -830,7 +1005,10 @@ def layer_backward(x, w_gate_up, w_down, fwd: dict, d_out, k: int, e_begin: int,
     d_x_perm, d_wgu, d_wdn = grouped_gemm_backward(x, fwd["perm"], fwd["offsets"], w_gate_up, w_down, fwd["h"], d_y,
                                                    k, E, e_begin, e_end, stream=stream, gu=fwd.get("gu"))
     d_x = dispatch_backward(d_x_perm, fwd["pair_pos"], T, k, E, e_begin, e_end, stream=stream)
-    d_logits = route_topk_backward(fwd["idx"], fwd["w"], d_w, E, stream=stream)
+    if router is None:
+        d_logits = route_topk_backward(fwd["idx"], fwd["w"], d_w, E, stream=stream)
+    else:
+        d_logits = route_experts_backward(fwd["logits"], fwd["idx"], d_w, router, stream=stream)
     return dict(d_y=d_y, d_w=d_w, d_x_perm=d_x_perm, d_w_gate_up=d_wgu, d_w_down=d_wdn, d_x=d_x, d_logits=d_logits,
                 **extra)
 
@@ -944,6 +1122,115 @@ def layer_norm_backward(d_y, s, weight, mean, rstd, d_s=None, bias: bool = True,
     return d_x, d_weight, d_bias
 
 
+# ----------------------------------------------------------------------------- residual add and RMS norm
+
+@dataclass
+class Int8Rows:
+    """Rows of tokens in 8 bits, as the experts in 8-bit integers take them: codes int8
+    [ceil(d / 64), T, 64] (zero past column d) and scale [T] fp32. Element [t, j] is
+    codes[j // 64, t, j % 64] * scale[t]."""
+    codes: object
+    scale: object
+
+
+def _rms_norm(x, weight, eps, residual, y, s, rstd, keep_y, rows, stream):
+    torch = _torch()
+    T, d = size = _rows(x, "x")
+    _norm_params(x, weight, None, d)
+    if residual is None and s is not None:
+        raise ValueError("s is written only with a residual")
+    _like(residual, "residual", x.dtype, size)
+    _like(y, "y", x.dtype, size)
+    _like(s, "s", x.dtype, size)
+    _like(rstd, "rstd", torch.float32, (T,))
+    codes, scale = (None, None) if rows is None else (rows.codes, rows.scale)
+    _like(codes, "codes", torch.int8, (_kblocks(d), T, 64))
+    _like(scale, "scale", torch.float32, (T,))
+    sh = shape(T, d, 8, 1, 1, 0, 1)
+    h, ctx = _ready(stream, (x, weight, residual, y, s, codes), [t for t in (rstd, scale) if t is not None])
+    if residual is None and not (y is not None and T > 0 and y.data_ptr() == x.data_ptr()):
+        s = x
+    with ctx:
+        if y is None and keep_y:
+            y = torch.empty_like(x)
+        if residual is not None and s is None:
+            s = torch.empty_like(x)
+        if rstd is None:
+            rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        if rows is not None and codes is None:
+            rows.codes = codes = torch.empty((_kblocks(d), T, 64), dtype=torch.int8, device=x.device)
+            rows.scale = scale = torch.empty(T, dtype=torch.float32, device=x.device)
+        ctx.give(y, s, rstd, codes, scale)
+        _check(_load().moe_rms_norm(ctypes.byref(sh), _CODES[x.dtype], x.data_ptr(), _addr(residual),
+                                    _CODES[weight.dtype], weight.data_ptr(), eps, _addr(y),
+                                    None if residual is None else s.data_ptr(), rstd.data_ptr(), _addr(codes),
+                                    _addr(scale), h), "moe_rms_norm")
+    return y, s, rstd
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, y=None, s=None, rstd=None, stream=None):
+    """(y, s, rstd): s = x + residual (x itself without one), normalised to
+    y = s * rstd * weight with rstd = 1 / sqrt(mean(s^2) + eps) [T] fp32. weight [d] is
+    of x's dtype or fp32. y may be x or residual, and so may s. With y = x and no
+    residual, s is None (as for layer_norm)."""
+    return _rms_norm(x, weight, eps, residual, y, s, rstd, True, None, stream)
+
+
+def rms_norm_int8(x, weight, eps: float = 1e-6, residual=None, keep_y: bool = True, rows: Int8Rows | None = None,
+                  y=None, s=None, rstd=None, stream=None):
+    """(rows, y, s, rstd): rms_norm of bf16 rows, and the normalised rows in 8 bits for
+    the experts (layer_int8). Without keep_y, y is neither made nor written (None)."""
+    _want(x, "x", _torch().bfloat16)
+    if rows is not None and (rows.codes is None or rows.scale is None):
+        raise ValueError("rows must hold codes and scale")
+    if y is not None and not keep_y:
+        raise ValueError("y is written only with keep_y")
+    if rows is None:
+        rows = Int8Rows(None, None)
+    y, s, rstd = _rms_norm(x, weight, eps, residual, y, s, rstd, keep_y, rows, stream)
+    return rows, y, s, rstd
+
+
+def rms_norm_backward_workspace_bytes(T: int, d: int) -> int:
+    sh = shape(T, d, 8, 1, 1, 0, 1)
+    return int(_load().moe_rms_norm_backward_workspace_bytes(ctypes.byref(sh)))
+
+
+def rms_norm_backward(d_y, s, weight, rstd, d_s=None, d_x=None, d_weight=None, workspace=None, stream=None):
+    """(d_x, d_weight): the gradient of rms_norm, given the forward's s and rstd. d_s,
+    the gradient that reaches s on other ways, is added to d_x. d_x may be d_y or d_s."""
+    torch = _torch()
+    T, d = size = _rows(d_y, "d_y")
+    if s is None or rstd is None:
+        raise ValueError("s and rstd of the forward are required")
+    _like(s, "s", d_y.dtype, size)
+    _norm_params(d_y, weight, None, d)
+    _like(rstd, "rstd", torch.float32, (T,))
+    _like(d_s, "d_s", d_y.dtype, size)
+    _like(d_x, "d_x", d_y.dtype, size)
+    _like(d_weight, "d_weight", weight.dtype, (d,))
+    sh = shape(T, d, 8, 1, 1, 0, 1)
+    ws_bytes = _load().moe_rms_norm_backward_workspace_bytes(ctypes.byref(sh))
+    if workspace is not None:
+        _want(workspace, "workspace", torch.uint8)
+        if workspace.numel() < ws_bytes:
+            raise ValueError(f"workspace must hold at least {ws_bytes} bytes, got {workspace.numel()}")
+    h, ctx = _ready(stream, (d_y, s, weight, d_s, d_x, d_weight, workspace), (rstd,))
+    with ctx:
+        if d_x is None:
+            d_x = torch.empty_like(d_y)
+        if d_weight is None:
+            d_weight = torch.empty_like(weight)
+        ctx.give(d_x, d_weight)
+        if workspace is None and ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=d_y.device)
+        _check(_load().moe_rms_norm_backward(ctypes.byref(sh), _CODES[d_y.dtype], d_y.data_ptr(), s.data_ptr(),
+                                             _CODES[weight.dtype], weight.data_ptr(), rstd.data_ptr(), _addr(d_s),
+                                             d_x.data_ptr(), d_weight.data_ptr(), _addr(workspace), h),
+               "moe_rms_norm_backward")
+    return d_x, d_weight
+
+
 # ----------------------------------------------------------------------------- experts in 8-bit integers
 
 @dataclass
@@ -1014,17 +1301,30 @@ def grouped_gemm_int8_workspace_bytes(T: int, d: int, d_ff: int, E: int, k: int,
 def grouped_gemm_int8(x, perm, offsets, experts: Int8Experts, k: int, E: int, e_begin: int, e_end: int, y=None,
                       workspace=None, stream=None):
     """y [N_max, d]: the local experts' SwiGLU FFN in 8-bit integers, on rows of x
-    (bf16) quantised as they are gathered through perm."""
+    (bf16) quantised as they are gathered through perm, or on x in 8 bits already
+    (Int8Rows, from rms_norm_int8; d is then the experts')."""
     torch = _torch()
     _range(E, k, e_begin, e_end)
-    _want(x, "x", torch.bfloat16)
-    T, d = _rows(x, "x")
+    rows = x if isinstance(x, Int8Rows) else None
+    if rows is None:
+        _want(x, "x", torch.bfloat16)
+        T, d = _rows(x, "x")
+    else:
+        _want(rows.codes, "codes", torch.int8)
+        _want(rows.scale, "scale", torch.float32)
+        _want(experts.down_scale, "down_scale", torch.float32)
+        if experts.down_scale.dim() != 2 or rows.scale.dim() != 1:
+            raise ValueError(f"down_scale must be [E_loc, d] and scale [T], got {list(experts.down_scale.shape)}, "
+                             f"{list(rows.scale.shape)}")
+        T, d = rows.scale.shape[0], experts.down_scale.shape[1]
+        _want(rows.codes, "codes", torch.int8, (_kblocks(d), T, 64))
+        x = rows.codes
     n_max = _n_max(T, k, e_begin, e_end)
     _want(perm, "perm", torch.int32, (T * k,))
     _want(offsets, "offsets", torch.int32, (E + 1,))
     d_ff = _want_int8_experts(experts, d, e_end - e_begin)
     if y is not None:
-        _want(y, "y", x.dtype, (n_max, d), min_rows=n_max)
+        _want(y, "y", torch.bfloat16, (n_max, d), min_rows=n_max)
     s = shape(T, d, d_ff, E, k, e_begin, e_end)
     ws_bytes = _load().moe_grouped_gemm_int8_workspace_bytes(ctypes.byref(s))
     if workspace is not None:
@@ -1032,36 +1332,60 @@ def grouped_gemm_int8(x, perm, offsets, experts: Int8Experts, k: int, E: int, e_
         if workspace.numel() < ws_bytes:
             raise ValueError(f"workspace must hold at least {ws_bytes} bytes, got {workspace.numel()}")
     wgu, sgu, wdn, sdn = experts.w_gate_up, experts.gate_up_scale, experts.w_down, experts.down_scale
-    h, ctx = _ready(stream, (x, wgu, wdn, y, workspace), (perm, offsets, sgu, sdn))
+    h, ctx = _ready(stream, (x, wgu, wdn, y, workspace),
+                    (perm, offsets, sgu, sdn) if rows is None else (perm, offsets, sgu, sdn, rows.scale))
     with ctx:
         if y is None:
-            y = torch.empty((n_max, d), dtype=x.dtype, device=x.device)
+            y = torch.empty((n_max, d), dtype=torch.bfloat16, device=x.device)
         ctx.give(y)
         if workspace is None and ws_bytes:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
-        _check(_load().moe_grouped_gemm_int8(ctypes.byref(s), MOE_BF16, x.data_ptr(), perm.data_ptr(),
-                                             offsets.data_ptr(), wgu.data_ptr(), sgu.data_ptr(), wdn.data_ptr(),
-                                             sdn.data_ptr(), y.data_ptr(), _addr(workspace), h),
-               "moe_grouped_gemm_int8")
+        if rows is None:
+            _check(_load().moe_grouped_gemm_int8(ctypes.byref(s), MOE_BF16, x.data_ptr(), perm.data_ptr(),
+                                                 offsets.data_ptr(), wgu.data_ptr(), sgu.data_ptr(), wdn.data_ptr(),
+                                                 sdn.data_ptr(), y.data_ptr(), _addr(workspace), h),
+                   "moe_grouped_gemm_int8")
+        else:
+            _check(_load().moe_grouped_gemm_int8_rows(ctypes.byref(s), x.data_ptr(), rows.scale.data_ptr(),
+                                                      perm.data_ptr(), offsets.data_ptr(), wgu.data_ptr(),
+                                                      sgu.data_ptr(), wdn.data_ptr(), sdn.data_ptr(), y.data_ptr(),
+                                                      _addr(workspace), h), "moe_grouped_gemm_int8_rows")
     return y
 
 
-def layer_int8(x, logits, experts: Int8Experts, k: int, e_begin: int, e_end: int, stream=None, norm=None) -> dict:
+def layer_int8(x, logits, experts: Int8Experts, k: int, e_begin: int, e_end: int, stream=None, norm=None,
+               router: Router | None = None, residual=None) -> dict:
     """layer() for serving, with the experts in 8-bit integers: route -> dispatch
     (indices) -> grouped_gemm_int8 -> combine, and with `norm` the residual add
-    and layer norm."""
-    T = x.shape[0]
+    and norm. x is bf16 rows or Int8Rows (then `norm` needs `residual`)."""
+    rows = isinstance(x, Int8Rows)
+    if rows:
+        _want(x.scale, "scale", _torch().float32)
+        if norm is not None and residual is None:
+            raise ValueError("rows in 8 bits are no residual: norm needs residual")
+    T = x.scale.shape[0] if rows else x.shape[0]
     if logits.dim() != 2 or logits.shape[0] != T:
         raise ValueError(f"logits must be [T={T}, E], got {list(logits.shape)}")
     E = logits.shape[1]
-    _check_layer_norm_arg(norm, E, e_begin, e_end)
-    idx, w = route_topk(logits, k, stream=stream)
-    disp = dispatch(x, idx, E, e_begin, e_end, stream=stream, gather=False)
+    _check_layer_norm_arg(norm, residual, E, e_begin, e_end)
+    idx, w = _route(logits, k, router, stream)
+    disp = _dispatch_ids(idx, E, e_begin, e_end, stream) if rows else dispatch(x, idx, E, e_begin, e_end, stream=stream,
+                                                                               gather=False)
     y = grouped_gemm_int8(x, disp.perm, disp.offsets, experts, k, E, e_begin, e_end, stream=stream)
     out = combine(y, disp.pair_pos, w, T, k, E, e_begin, e_end, stream=stream)
     res = dict(idx=idx, w=w, counts=disp.counts, offsets=disp.offsets, perm=disp.perm, pair_pos=disp.pair_pos, y=y,
                out=out)
-    return _with_norm(res, x, E, e_begin, e_end, norm, stream)
+    return _with_norm(res, x if residual is None else residual, norm, stream)
+
+
+def _dispatch_ids(topk_idx, E: int, e_begin: int, e_end: int, stream) -> Dispatch:
+    """dispatch without the hidden states: their dtype and width do not matter to the indices."""
+    torch = _torch()
+    _, ctx = _dense(stream, (topk_idx,))
+    with ctx:
+        x = torch.empty((topk_idx.shape[0], 8), dtype=torch.bfloat16, device=topk_idx.device)
+        ctx.give(x)
+    return dispatch(x, topk_idx, E, e_begin, e_end, stream=stream, gather=False)
 
 
 # ----------------------------------------------------------------------------- gradient norm and clipping
@@ -1172,3 +1496,133 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm=None, workspace=None, 
         _check(_load().moe_clip_grad_norm(src.buffer_info()[0], dst.buffer_info()[0] if outs else None, len(ts),
                                           max_norm, norm.data_ptr(), workspace.data_ptr(), h), "moe_clip_grad_norm")
     return norm
+
+
+# ----------------------------------------------------------------------------- AdamW
+
+@dataclass
+class Float8State:
+    """A tensor's AdamW state in 8 bits: codes (float8_e4m3fn) of the tensor's shape and
+    scale [ceil(numel / 128)] fp32. Element i stands for codes[i] * scale[i // 128]; the
+    second state holds the square root of the mean square."""
+    codes: object
+    scale: object
+
+
+def adamw_states(params, bits: int = 32):
+    """(exp_avg, exp_avg_sq) of a list of parameters before the first step: zeros, as
+    fp32 tensors or (bits = 8) Float8State."""
+    torch = _torch()
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, got {bits}")
+
+    def one(p):
+        if bits == 32:
+            return torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+        codes = torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(torch.float8_e4m3fn)
+        return Float8State(codes, torch.zeros(-(-p.numel() // MOE_STATE_BLOCK), dtype=torch.float32, device=p.device))
+
+    return [one(p) for p in params], [one(p) for p in params]
+
+
+def _same_list(ts, name: str, like, dtype):
+    """A list of tensors of the shapes of another list, all of one dtype."""
+    ts = list(ts)
+    if len(ts) != len(like):
+        raise ValueError(f"{name} must hold {len(like)} tensors, got {len(ts)}")
+    for i, (t, p) in enumerate(zip(ts, like)):
+        if t is None or t.dtype is not dtype or t.shape != p.shape:
+            _want(t, f"{name}[{i}]", dtype, tuple(p.shape))
+    return ts
+
+
+def _state_list(ts, name: str, params):
+    """(tensors, scales or None) of a list of states."""
+    torch = _torch()
+    ts = list(ts)
+    if not any(isinstance(t, Float8State) for t in ts):
+        return _same_list(ts, name, params, torch.float32), None
+    if not all(isinstance(t, Float8State) for t in ts):
+        raise TypeError(f"{name} must hold fp32 tensors or Float8State, not both")
+    codes = _same_list([t.codes for t in ts], name, params, torch.float8_e4m3fn)
+    scales = [t.scale for t in ts]
+    for i, (t, p) in enumerate(zip(scales, params)):
+        n = -(-p.numel() // MOE_STATE_BLOCK)
+        if t is None or t.dtype is not torch.float32 or t.shape != (n,):
+            _want(t, f"{name}[{i}].scale", torch.float32, (n,))
+    return codes, scales
+
+
+def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
+          weight_decay=0.0, masters=None, norm=None, max_norm: float = 0.0, stream=None) -> None:
+    """One AdamW step, in place, over lists of params (bf16 or fp32), grads (bf16 or
+    fp32) and states (fp32 or Float8State, from adamw_states). masters: fp32 copies of
+    bf16 params, which the step then reads and writes (None for the list or for single
+    entries; an fp32 param has none). weight_decay: a number, or one for each param.
+    step (the number of this step, from 1) and lr are numbers, or tensors [1] (int64,
+    fp32) that a captured graph reads at each replay. With norm [1] fp32 (grad_norm), the
+    gradients are clipped to max_norm on the way, without being written."""
+    torch = _torch()
+    params, numels, kinds = _tensor_list(params, "params")
+    grads = list(grads)
+    if len(grads) != len(params):
+        raise ValueError(f"grads must hold {len(params)} tensors, got {len(grads)}")
+    for i, (g, p) in enumerate(zip(grads, params)):
+        if g is None or g.dtype not in _CODES or g.shape != p.shape:
+            _want(g, f"grads[{i}]", _act_dtypes(), tuple(p.shape))
+    m, m_scale = _state_list(exp_avg, "exp_avg", params)
+    v, v_scale = _state_list(exp_avg_sq, "exp_avg_sq", params)
+    if (m_scale is None) != (v_scale is None):
+        raise TypeError("exp_avg and exp_avg_sq must both be fp32 or both Float8State")
+    n = len(params)
+    w = [None] * n if masters is None else list(masters)
+    if len(w) != n:
+        raise ValueError(f"masters must hold {n} tensors, got {len(w)}")
+    for i, (t, p) in enumerate(zip(w, params)):
+        if t is not None:
+            if p.dtype is not torch.bfloat16:
+                raise ValueError(f"masters[{i}]: an fp32 param has no master")
+            if t.dtype is not torch.float32 or t.shape != p.shape:
+                _want(t, f"masters[{i}]", torch.float32, tuple(p.shape))
+    args = moe_adamw_args(beta1=betas[0], beta2=betas[1], eps=eps, state=MOE_STATE_F32 if m_scale is None else MOE_STATE_E4M3)
+    scalars = []
+    for name, value, dtype in (("step", step, torch.int64), ("lr", lr, torch.float32)):
+        if torch.is_tensor(value):
+            _want(value, name, dtype, (1,))
+            setattr(args, "d_" + name, value.data_ptr())
+            scalars.append(value)
+        elif name == "step" and not 1 <= value < 1 << 63:
+            raise ValueError(f"step counts from 1, got {value}")
+        else:
+            setattr(args, name, value)
+    if isinstance(weight_decay, (int, float)):
+        args.weight_decay = weight_decay
+    else:
+        decays = array.array("d", weight_decay)
+        if len(decays) != n:
+            raise ValueError(f"weight_decay must hold {n} numbers, got {len(decays)}")
+        args.weight_decays = decays.buffer_info()[0]
+    if norm is not None:
+        _want(norm, "norm", torch.float32, (1,))
+        args.norm, args.max_norm = norm.data_ptr(), max_norm
+        scalars.append(norm)
+    elif max_norm:
+        raise ValueError("max_norm needs norm (grad_norm's result)")
+    held = [t for t in w if t is not None]
+    h, ctx = _dense(stream, [*params, *grads, *m, *v, *(m_scale or ()), *(v_scale or ()), *held, *scalars])
+    ptr = torch.Tensor.data_ptr
+    flat = [0] * (9 * n)  # moe_adamw_tensor, eight bytes a field (the two dtypes share one)
+    flat[0::9] = map(ptr, params)
+    flat[1::9] = map(ptr, grads)
+    if held:
+        flat[2::9] = [0 if t is None else t.data_ptr() for t in w]
+    flat[3::9] = map(ptr, m)
+    flat[4::9] = map(ptr, v)
+    if m_scale is not None:
+        flat[5::9] = map(ptr, m_scale)
+        flat[6::9] = map(ptr, v_scale)
+    flat[7::9] = numels
+    flat[8::9] = [kind | _CODES[g.dtype] << 32 for kind, g in zip(kinds, grads)]
+    host = array.array("q", flat)
+    with ctx:
+        _check(_load().moe_adamw(host.buffer_info()[0], n, ctypes.byref(args), h), "moe_adamw")

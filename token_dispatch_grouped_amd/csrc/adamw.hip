@@ -1,0 +1,403 @@
+// One AdamW step over a list of tensors, with states in fp32 or in 8 bits.
+//
+//   g = grad * min(1, max_norm / (norm + 1e-6))
+//   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Bound by HBM: every array is read and written once (28 bytes an element for bf16
+// weights with masters and fp32 states, 16 with 8-bit states). The tensors of a list are
+// cut into pieces of kPiece elements, numbered through; workgroup i takes pieces i,
+// i + grid, ... . A launch carries its tensors' addresses in the kernel arguments (no
+// table to copy, so a captured graph keeps them), up to kList of them.
+//
+// 8-bit states hold m and sqrt(v), whose range is half of v's in powers of two, as e4m3
+// with an fp32 scale per 128 elements: relative errors of 2^-4 down to 2^-15 of the block's
+// largest, where codes of equal steps would lose all small elements. sqrt(v) > 0 never
+// becomes 0 (m / eps would be the step); its smallest code, 2^-9 / 448 of the largest, is
+// too large then, which makes the step smaller. The step itself uses m and v before the rounding.
+#include <math.h>
+
+#include "row_group.h"
+
+namespace moe {
+namespace {
+
+using rows::kStreamBytes;
+
+constexpr int kThreads = 256;
+constexpr int kList = 32;
+constexpr int kPiece = 4096;  // elements
+constexpr int kBlocks = 2048;
+constexpr int kStateBlock = MOE_STATE_BLOCK;
+constexpr float kClipEps = 1e-6f;
+constexpr float kCodeStep = 1.f / 448.f;  // of the largest code
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
+
+struct Entry {
+  void* p;
+  const void* g;
+  float* w;  // the master, or null
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  int64_t numel;
+  double decay;  // the weight decay
+  uint8_t p_bf16, g_bf16;
+};
+struct List {
+  Entry t[kList];
+  int64_t piece0[kList + 1];  // first piece of each tensor
+  int n;
+};
+
+struct Scalars {
+  const float* d_lr;
+  const int64_t* d_step;
+  const float* norm;
+  double lr, step, log_b1, log_b2;
+  float b1, b2, one_b1, one_b2;  // 1 - b from the fp64 b
+  float eps, max_norm;
+};
+
+// Of one call: the rate over the first bias correction, the root's factor, the clip factor.
+struct Step {
+  double lr;
+  float rate, root, coef;
+};
+
+__device__ __forceinline__ Step step_of(const Scalars& a) {
+  Step s;
+  const double lr = a.d_lr != nullptr ? static_cast<double>(*a.d_lr) : a.lr;
+  double t = a.step;
+  if (a.d_step != nullptr) t = static_cast<double>(*a.d_step < 1 ? 1 : *a.d_step);
+  s.lr = lr;
+  s.rate = static_cast<float>(lr / -expm1(t * a.log_b1));
+  s.root = static_cast<float>(1.0 / sqrt(-expm1(t * a.log_b2)));
+  s.coef = 1.f;
+  if (a.norm != nullptr) {
+    const float c = a.max_norm * (1.f / (*a.norm + kClipEps));
+    s.coef = c >= 1.f ? 1.f : c;  // a NaN norm gives NaN
+  }
+  return s;
+}
+
+// N consecutive elements, of which `n` (<= N) exist; the others read as 0 (FULL: all exist).
+// Vectors are aligned to their elements only, which global memory takes.
+template <typename T, int N>
+struct Pack {
+  typedef T type __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+};
+
+template <bool STREAM, bool FULL, typename T, int N>
+__device__ __forceinline__ void load_n(const T* p, int n, T* out) {
+  using P = typename Pack<T, N>::type;
+  if (FULL || n == N) {
+    P v;
+    if constexpr (STREAM) v = __builtin_nontemporal_load(reinterpret_cast<const P*>(p));
+    else v = *reinterpret_cast<const P*>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = i < n ? p[i] : T{};
+  }
+}
+
+template <bool STREAM, bool FULL, typename T, int N>
+__device__ __forceinline__ void store_n(T* p, int n, const T* in) {
+  using P = typename Pack<T, N>::type;
+  if (FULL || n == N) {
+    P v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = in[i];
+    if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<P*>(p));
+    else *reinterpret_cast<P*>(p) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) p[i] = in[i];
+  }
+}
+
+template <bool STREAM, bool FULL, int N, bool BF16>
+__device__ __forceinline__ void load_f(const void* base, int64_t a, int n, float* f) {
+  if constexpr (BF16) {
+    uint16_t h[N];
+    load_n<STREAM, FULL, uint16_t, N>(static_cast<const uint16_t*>(base) + a, n, h);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = bf16_to_f32(h[i]);
+  } else {
+    load_n<STREAM, FULL, float, N>(static_cast<const float*>(base) + a, n, f);
+  }
+}
+
+template <bool STREAM, bool FULL, int N, bool BF16>
+__device__ __forceinline__ void store_f(void* base, int64_t a, int n, const float* f) {
+  if constexpr (BF16) {
+    uint16_t h[N];
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint32_t u = rows::Vec16<true>::round2(f[i], f[i + 1]);
+      h[i] = static_cast<uint16_t>(u);
+      h[i + 1] = static_cast<uint16_t>(u >> 16);
+    }
+    store_n<STREAM, FULL, uint16_t, N>(static_cast<uint16_t*>(base) + a, n, h);
+  } else {
+    store_n<STREAM, FULL, float, N>(static_cast<float*>(base) + a, n, f);
+  }
+}
+
+// Every product and sum is rounded by itself: which of them a compiler joins would decide, for a
+// state near the middle between two codes, which of the two it gets.
+__device__ __forceinline__ void update(float& p, float g, float& m, float& v, float& root, const Scalars& a,
+                                       const Step& s, float decay) {
+#pragma clang fp contract(off)
+  g = g * s.coef;
+  m = m * a.b1 + g * a.one_b1;
+  v = v * a.b2 + g * g * a.one_b2;
+  root = sqrtf(v);
+  p = p * decay - s.rate * (m / (root * s.root + a.eps));
+}
+
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max_u32(v, static_cast<uint32_t>(
+                        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, false)));
+}
+
+// The largest of each aligned 16 lanes, to all of them.
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = dpp_max<0xB1>(v);   // quad_perm [1,0,3,2]
+  v = dpp_max<0x4E>(v);   // quad_perm [2,3,0,1]
+  v = dpp_max<0x141>(v);  // row_half_mirror
+  return dpp_max<0x140>(v);  // row_mirror
+}
+
+// N codes (a multiple of 4) of one lane, one to four in a word, and the values of such a word.
+__device__ __forceinline__ uint32_t codes4(const float* f) {
+  int w = 0;
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], w, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
+  return static_cast<uint32_t>(w);
+}
+__device__ __forceinline__ void values4(uint32_t w, float* f) {
+  f[0] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 0);
+  f[1] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 1);
+  f[2] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 2);
+  f[3] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 3);
+}
+
+// The block's scale from its lanes' values (16 lanes of N = 8), and the lane's codes.
+template <int N, bool ROOT>
+__device__ __forceinline__ float encode(const float* f, uint8_t* codes) {
+  static_assert(N * 16 == kStateBlock, "a block is 16 lanes");
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = max_u32(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+  top = row_max(top);
+  const bool finite = top < 0x7F800000u;
+  const float scale = fmaxf(__uint_as_float(top) * kCodeStep, kMinScale);
+  const float inv = 1.f / scale;
+#pragma unroll
+  for (int j = 0; j < N; j += 4) {
+    float a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = finite ? f[j + i] * inv : 0.f;
+    uint32_t w = codes4(a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint8_t b = static_cast<uint8_t>(w >> (8 * i));
+      if (ROOT) b = finite && f[j + i] > 0.f && b == 0 ? 1 : b;
+      codes[j + i] = b;
+    }
+  }
+  return finite ? scale : __uint_as_float(0x7FC00000u);
+}
+
+// A piece with fp32 states: 4 elements of every array at a time, all loads of a thread's
+// four such groups before the first is used.
+template <bool P_BF16, bool G_BF16, bool MASTER, bool STREAM, bool FULL>
+__device__ __forceinline__ void piece_f32(const Entry& e, int64_t first, const Scalars& a, const Step& s, float decay) {
+  constexpr int N = 4, kU = kPiece / (kThreads * N);
+  float p[kU][N], g[kU][N], m[kU][N], v[kU][N];
+  int n[kU];
+#pragma unroll
+  for (int q = 0; q < kU; ++q) {
+    const int64_t i = first + (q * kThreads + static_cast<int>(threadIdx.x)) * N;
+    const int64_t left = e.numel - i;
+    n[q] = FULL || left >= N ? N : left > 0 ? static_cast<int>(left) : 0;
+    load_f<STREAM, FULL, N, G_BF16>(e.g, i, n[q], g[q]);
+    if (MASTER) load_f<STREAM, FULL, N, false>(e.w, i, n[q], p[q]);
+    else load_f<STREAM, FULL, N, P_BF16>(e.p, i, n[q], p[q]);
+    load_f<STREAM, FULL, N, false>(e.m, i, n[q], m[q]);
+    load_f<STREAM, FULL, N, false>(e.v, i, n[q], v[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < kU; ++q) {
+    const int64_t i = first + (q * kThreads + static_cast<int>(threadIdx.x)) * N;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float root;
+      update(p[q][j], g[q][j], m[q][j], v[q][j], root, a, s, decay);
+    }
+    if (MASTER) store_f<STREAM, FULL, N, false>(e.w, i, n[q], p[q]);
+    store_f<STREAM, FULL, N, P_BF16>(e.p, i, n[q], p[q]);
+    store_f<STREAM, FULL, N, false>(e.m, i, n[q], m[q]);
+    store_f<STREAM, FULL, N, false>(e.v, i, n[q], v[q]);
+  }
+}
+
+// A piece with 8-bit states: 8 elements of every array, a block of them in 16 lanes.
+template <bool P_BF16, bool G_BF16, bool MASTER, bool STREAM, bool FULL>
+__device__ __forceinline__ void piece_e4m3(const Entry& e, int64_t first, const Scalars& a, const Step& s, float decay) {
+  constexpr int N = 8, kU = kPiece / (kThreads * N);
+  float p[kU][N], g[kU][N], ms[kU], vs[kU];
+  uint8_t mc[kU][N], vc[kU][N];
+  int n[kU];
+#pragma unroll
+  for (int q = 0; q < kU; ++q) {
+    const int64_t i = first + (q * kThreads + static_cast<int>(threadIdx.x)) * N;
+    const int64_t left = e.numel - i;
+    n[q] = FULL || left >= N ? N : left > 0 ? static_cast<int>(left) : 0;
+    load_f<STREAM, FULL, N, G_BF16>(e.g, i, n[q], g[q]);
+    if (MASTER) load_f<STREAM, FULL, N, false>(e.w, i, n[q], p[q]);
+    else load_f<STREAM, FULL, N, P_BF16>(e.p, i, n[q], p[q]);
+    load_n<STREAM, FULL, uint8_t, N>(static_cast<const uint8_t*>(e.m) + i, n[q], mc[q]);
+    load_n<STREAM, FULL, uint8_t, N>(static_cast<const uint8_t*>(e.v) + i, n[q], vc[q]);
+    ms[q] = n[q] > 0 ? e.ms[i / kStateBlock] : 0.f;
+    vs[q] = n[q] > 0 ? e.vs[i / kStateBlock] : 0.f;
+  }
+#pragma unroll
+  for (int q = 0; q < kU; ++q) {
+    const int64_t i = first + (q * kThreads + static_cast<int>(threadIdx.x)) * N;
+    float m[N], root[N];
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      uint32_t wm = 0, wv = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        wm |= static_cast<uint32_t>(mc[q][j + b]) << (8 * b);
+        wv |= static_cast<uint32_t>(vc[q][j + b]) << (8 * b);
+      }
+      values4(wm, m + j);
+      values4(wv, root + j);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      m[j] *= ms[q];
+      const float r = root[j] * vs[q];
+      float v = r * r;
+      update(p[q][j], g[q][j], m[j], v, root[j], a, s, decay);
+      if (!FULL && j >= n[q]) m[j] = root[j] = 0.f;  // past the last element: not in the block's largest
+    }
+    const float m_scale = encode<N, false>(m, mc[q]), v_scale = encode<N, true>(root, vc[q]);
+    if (MASTER) store_f<STREAM, FULL, N, false>(e.w, i, n[q], p[q]);
+    store_f<STREAM, FULL, N, P_BF16>(e.p, i, n[q], p[q]);
+    store_n<STREAM, FULL, uint8_t, N>(static_cast<uint8_t*>(e.m) + i, n[q], mc[q]);
+    store_n<STREAM, FULL, uint8_t, N>(static_cast<uint8_t*>(e.v) + i, n[q], vc[q]);
+    if (n[q] > 0 && i % kStateBlock == 0) {
+      e.ms[i / kStateBlock] = m_scale;
+      e.vs[i / kStateBlock] = v_scale;
+    }
+  }
+}
+
+template <bool E4M3, bool P_BF16, bool G_BF16, bool MASTER, bool STREAM>
+__device__ __forceinline__ void piece(const Entry& e, int64_t first, const Scalars& a, const Step& s, float decay) {
+  // only a tensor's last piece looks where the tensor ends
+  if (first + kPiece <= e.numel) {
+    if constexpr (E4M3) piece_e4m3<P_BF16, G_BF16, MASTER, STREAM, true>(e, first, a, s, decay);
+    else piece_f32<P_BF16, G_BF16, MASTER, STREAM, true>(e, first, a, s, decay);
+  } else {
+    if constexpr (E4M3) piece_e4m3<P_BF16, G_BF16, MASTER, STREAM, false>(e, first, a, s, decay);
+    else piece_f32<P_BF16, G_BF16, MASTER, STREAM, false>(e, first, a, s, decay);
+  }
+}
+
+template <bool E4M3, bool STREAM>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(const List l, const Scalars a) {
+  const Step s = step_of(a);
+  const int64_t total = l.piece0[l.n];
+  int i = 0;
+  for (int64_t at = blockIdx.x; at < total; at += gridDim.x) {
+    while (l.piece0[i + 1] <= at) ++i;
+    const Entry& e = l.t[i];
+    const int64_t first = (at - l.piece0[i]) * kPiece;
+    const float decay = static_cast<float>(1.0 - s.lr * e.decay);
+    if (!e.p_bf16) {
+      if (e.g_bf16) piece<E4M3, false, true, false, STREAM>(e, first, a, s, decay);
+      else piece<E4M3, false, false, false, STREAM>(e, first, a, s, decay);
+    } else if (e.w != nullptr) {
+      if (e.g_bf16) piece<E4M3, true, true, true, STREAM>(e, first, a, s, decay);
+      else piece<E4M3, true, false, true, STREAM>(e, first, a, s, decay);
+    } else {
+      if (e.g_bf16) piece<E4M3, true, true, false, STREAM>(e, first, a, s, decay);
+      else piece<E4M3, true, false, false, STREAM>(e, first, a, s, decay);
+    }
+  }
+}
+
+int64_t bytes_of(const moe_adamw_tensor& t, bool e4m3) {
+  const int64_t p = t.param_dt == MOE_BF16 ? (t.master != nullptr ? 10 : 4) : 8;
+  return t.numel * (p + (t.grad_dt == MOE_BF16 ? 2 : 4) + (e4m3 ? 4 : 16));
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const moe_adamw_tensor* t, int n, const moe_adamw_args& args, hipStream_t stream) {
+  const bool e4m3 = args.state == MOE_STATE_E4M3;
+  Scalars a;
+  a.d_lr = args.d_lr;
+  a.d_step = args.d_step;
+  a.norm = args.norm;
+  a.lr = args.lr;
+  a.step = static_cast<double>(args.step);
+  a.log_b1 = log(args.beta1);
+  a.log_b2 = log(args.beta2);
+  a.b1 = static_cast<float>(args.beta1);
+  a.b2 = static_cast<float>(args.beta2);
+  a.one_b1 = static_cast<float>(1.0 - args.beta1);
+  a.one_b2 = static_cast<float>(1.0 - args.beta2);
+  a.eps = static_cast<float>(args.eps);
+  a.max_norm = args.max_norm;
+  int64_t bytes = 0;
+  for (int i = 0; i < n; ++i) bytes += bytes_of(t[i], e4m3);
+  const bool big = bytes > kStreamBytes;
+  for (int i0 = 0; i0 < n;) {
+    List l;
+    l.n = 0;
+    l.piece0[0] = 0;
+    for (; l.n < kList && i0 < n; ++i0) {
+      if (t[i0].numel == 0) continue;
+      Entry& e = l.t[l.n];
+      e.p = t[i0].param;
+      e.g = t[i0].grad;
+      e.w = t[i0].master;
+      e.m = t[i0].exp_avg;
+      e.v = t[i0].exp_avg_sq;
+      e.ms = t[i0].exp_avg_scale;
+      e.vs = t[i0].exp_avg_sq_scale;
+      e.numel = t[i0].numel;
+      e.decay = args.weight_decays != nullptr ? args.weight_decays[i0] : args.weight_decay;
+      e.p_bf16 = t[i0].param_dt == MOE_BF16;
+      e.g_bf16 = t[i0].grad_dt == MOE_BF16;
+      l.piece0[l.n + 1] = l.piece0[l.n] + (t[i0].numel + kPiece - 1) / kPiece;
+      ++l.n;
+    }
+    if (l.n == 0) break;
+    const int64_t pieces = l.piece0[l.n];
+    const dim3 grid(static_cast<unsigned>(pieces < kBlocks ? pieces : kBlocks));
+    if (e4m3 && big) hipLaunchKernelGGL((adamw_kernel<true, true>), grid, dim3(kThreads), 0, stream, l, a);
+    else if (e4m3) hipLaunchKernelGGL((adamw_kernel<true, false>), grid, dim3(kThreads), 0, stream, l, a);
+    else if (big) hipLaunchKernelGGL((adamw_kernel<false, true>), grid, dim3(kThreads), 0, stream, l, a);
+    else hipLaunchKernelGGL((adamw_kernel<false, false>), grid, dim3(kThreads), 0, stream, l, a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe

@@ -84,6 +84,43 @@ moe_status check_int8(const moe_shape* s) {
   return MOE_OK;
 }
 
+// The FFN on bf16 rows x, or (scale_x != nullptr) on rows that are codes already
+moe_status run_int8(const moe_shape* s, const void* x, const float* scale_x, const int32_t* perm, const int32_t* offsets,
+                    const void* q_gate_up, const float* scale_gate_up, const void* q_down, const float* scale_down,
+                    void* y, void* workspace, hipStream_t stream) {
+  if (s->T == 0) return MOE_OK;
+  if (any_null(x, q_gate_up, q_down, static_cast<const void*>(y), static_cast<const void*>(workspace)) ||
+      perm == nullptr || offsets == nullptr || scale_gate_up == nullptr || scale_down == nullptr)
+    return MOE_EINVAL;
+  if (!aligned16(x, q_gate_up, q_down, static_cast<const void*>(y), static_cast<const void*>(workspace)) ||
+      !aligned(perm, 4) || !aligned(offsets, 4) || !aligned(scale_gate_up, 4) || !aligned(scale_down, 4))
+    return MOE_EINVAL;
+  const int64_t n_max = n_max_of(s);
+  const int e_loc = s->e_end - s->e_begin, d = s->d, d_ff = s->d_ff;
+  const Int8Workspace ws(s);
+  char* p = static_cast<char*>(workspace);
+  float* xs = reinterpret_cast<float*>(p + ws.xs);
+  float* hs = reinterpret_cast<float*>(p + ws.hs);
+  if (ws.tile_rows == moe::kInt8FewRows)
+    return from_hip(moe::launch_int8_few(x, scale_x, perm, offsets, q_gate_up, scale_gate_up, q_down, scale_down,
+                                         p + ws.h, y, d, d_ff, s->E, s->e_begin, e_loc, s->k, s->T, n_max, stream));
+  hipError_t e = scale_x != nullptr
+                     ? moe::launch_gather_codes(x, scale_x, perm, offsets, p + ws.xq, xs, s->e_begin, s->e_end, s->k,
+                                                s->T, d, n_max, p + ws.plan, ws.tile_rows, stream)
+                     : moe::launch_quantize_rows(x, perm, offsets, p + ws.xq, xs, s->e_begin, s->e_end, s->k, s->T, d,
+                                                 n_max, p + ws.plan, ws.tile_rows, stream);
+  if (e == hipSuccess)
+    e = moe::launch_grouped_gemm_int8(p + ws.xq, xs, q_gate_up, scale_gate_up, p + ws.h, p + ws.plan, ws.tile_rows, e_loc, d,
+                                      d_ff, n_max, true, stream);
+  if (e == hipSuccess)
+    e = moe::launch_quantize_rows(p + ws.h, nullptr, offsets, p + ws.hq, hs, s->e_begin, s->e_end, s->k, s->T, d_ff,
+                                  n_max, nullptr, 0, stream);
+  if (e == hipSuccess)
+    e = moe::launch_grouped_gemm_int8(p + ws.hq, hs, q_down, scale_down, y, p + ws.plan, ws.tile_rows, e_loc, d_ff, d,
+                                      n_max, false, stream);
+  return from_hip(e);
+}
+
 // ------------------------------------------------------------------- gradients
 
 size_t elem_bytes(moe_dtype dt) { return dt == MOE_BF16 ? 2 : 4; }
@@ -218,34 +255,17 @@ moe_status moe_grouped_gemm_int8(const moe_shape* s, moe_dtype dt, const void* x
   if (st != MOE_OK) return st;
   if (!valid_dtype(dt)) return MOE_EINVAL;
   if (dt != MOE_BF16) return MOE_EUNSUPPORTED;
-  if (s->T == 0) return MOE_OK;
-  if (any_null(x, q_gate_up, q_down, static_cast<const void*>(y), static_cast<const void*>(workspace)) ||
-      perm == nullptr || offsets == nullptr || scale_gate_up == nullptr || scale_down == nullptr)
-    return MOE_EINVAL;
-  if (!aligned16(x, q_gate_up, q_down, static_cast<const void*>(y), static_cast<const void*>(workspace)) ||
-      !aligned(perm, 4) || !aligned(offsets, 4) || !aligned(scale_gate_up, 4) || !aligned(scale_down, 4))
-    return MOE_EINVAL;
-  const int64_t n_max = n_max_of(s);
-  const int e_loc = s->e_end - s->e_begin, d = s->d, d_ff = s->d_ff;
-  const Int8Workspace ws(s);
-  char* p = static_cast<char*>(workspace);
-  float* xs = reinterpret_cast<float*>(p + ws.xs);
-  float* hs = reinterpret_cast<float*>(p + ws.hs);
-  if (ws.tile_rows == moe::kInt8FewRows)
-    return from_hip(moe::launch_int8_few(x, perm, offsets, q_gate_up, scale_gate_up, q_down, scale_down, p + ws.h, y, d,
-                                         d_ff, s->E, s->e_begin, e_loc, s->k, s->T, n_max, stream));
-  hipError_t e = moe::launch_quantize_rows(x, perm, offsets, p + ws.xq, xs, s->e_begin, s->e_end, s->k, s->T, d, n_max,
-                                           p + ws.plan, ws.tile_rows, stream);
-  if (e == hipSuccess)
-    e = moe::launch_grouped_gemm_int8(p + ws.xq, xs, q_gate_up, scale_gate_up, p + ws.h, p + ws.plan, ws.tile_rows, e_loc, d,
-                                      d_ff, n_max, true, stream);
-  if (e == hipSuccess)
-    e = moe::launch_quantize_rows(p + ws.h, nullptr, offsets, p + ws.hq, hs, s->e_begin, s->e_end, s->k, s->T, d_ff,
-                                  n_max, nullptr, 0, stream);
-  if (e == hipSuccess)
-    e = moe::launch_grouped_gemm_int8(p + ws.hq, hs, q_down, scale_down, y, p + ws.plan, ws.tile_rows, e_loc, d_ff, d,
-                                      n_max, false, stream);
-  return from_hip(e);
+  return run_int8(s, x, nullptr, perm, offsets, q_gate_up, scale_gate_up, q_down, scale_down, y, workspace, stream);
+}
+
+moe_status moe_grouped_gemm_int8_rows(const moe_shape* s, const void* q_x, const float* scale_x, const int32_t* perm,
+                                      const int32_t* offsets, const void* q_gate_up, const float* scale_gate_up,
+                                      const void* q_down, const float* scale_down, void* y, void* workspace,
+                                      hipStream_t stream) {
+  const moe_status st = check_int8(s);
+  if (st != MOE_OK) return st;
+  if (s->T > 0 && (scale_x == nullptr || !aligned(scale_x, 4))) return MOE_EINVAL;
+  return run_int8(s, q_x, scale_x, perm, offsets, q_gate_up, scale_gate_up, q_down, scale_down, y, workspace, stream);
 }
 
 size_t moe_grad_norm_workspace_bytes(int32_t n) { return n < 0 ? 0 : moe::grad_norm_workspace_bytes(n); }

@@ -108,10 +108,11 @@ __device__ __forceinline__ void finish(const i32x4* part, const float* row_scale
   }
 }
 
-// The workgroup quantises its rows, G threads a row. Three waves per SIMD.
-template <bool SWIGLU, int FRAGS, int AHEAD, int G>
+// The workgroup quantises its rows, G threads a row, or (CODES) finds them in 8 bits already: src
+// then holds codes [kblocks][T][64], src_scale their scales. Three waves per SIMD.
+template <bool SWIGLU, int FRAGS, int AHEAD, int G, bool CODES>
 __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
-    const uint4* __restrict__ src, const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets,
+    const uint4* __restrict__ src, const float* __restrict__ src_scale, const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets,
     const uint8_t* __restrict__ w, const float* __restrict__ w_scale, __bf16* __restrict__ out, int e_begin, int k,
     int64_t T, int cols_vec, int kblocks, int N, int64_t n_max) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -147,6 +148,13 @@ __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
       int64_t from = r0 + r;
       if (perm != nullptr) from = perm[seg0 + r0 + r] / k;
       const int n = perm == nullptr || (from >= 0 && from < T) ? cols_vec : 0;
+      if constexpr (CODES) {
+        if (li == 0) scales[r] = n != 0 ? src_scale[from] : kMinScale;
+        for (int c = li; c < kblocks * 4; c += G)
+          *reinterpret_cast<uint4*>(smem + r * stride + c * 16) =
+              n != 0 ? src[((c >> 2) * T + from) * 4 + (c & 3)] : make_uint4(0, 0, 0, 0);
+        continue;
+      }
       const uint4* row = src + from * cols_vec;
       uint4 v[kHeld];
       uint32_t top = 0;
@@ -267,8 +275,8 @@ __global__ __launch_bounds__(kThreads, 3) void int8_thin_kernel(
   finish<SWIGLU, FRAGS, RT>(part, scales, wt.scale, out, r0, R, n0, N);
 }
 
-template <bool SWIGLU, int FRAGS, int AHEAD, int G>
-hipError_t launch_one(const void* src, const int32_t* perm, const int32_t* offsets, const void* w,
+template <bool SWIGLU, int FRAGS, int AHEAD, int G, bool CODES = false>
+hipError_t launch_one(const void* src, const float* src_scale, const int32_t* perm, const int32_t* offsets, const void* w,
                       const float* w_scale, void* out, int E, int e_begin, int e_loc, int k, int64_t T, int K, int N,
                       int64_t n_max, hipStream_t stream) {
   constexpr int cols = 16 * (SWIGLU ? FRAGS / 2 : FRAGS);
@@ -280,21 +288,30 @@ hipError_t launch_one(const void* src, const int32_t* perm, const int32_t* offse
   const int64_t likely = min(max((2 * T * k + E - 1) / E, (T + 3) / 4), T);
   const dim3 grid(static_cast<unsigned>((N + cols - 1) / cols), static_cast<unsigned>(e_loc),
                   static_cast<unsigned>((likely + rows - 1) / rows));
-  hipLaunchKernelGGL((int8_few_kernel<SWIGLU, FRAGS, AHEAD, G>), grid, dim3(kThreads),
-                     static_cast<unsigned>(rows * code_stride(kblocks)), stream, static_cast<const uint4*>(src), perm,
+  hipLaunchKernelGGL((int8_few_kernel<SWIGLU, FRAGS, AHEAD, G, CODES>), grid, dim3(kThreads),
+                     static_cast<unsigned>(rows * code_stride(kblocks)), stream, static_cast<const uint4*>(src), src_scale, perm,
                      offsets, static_cast<const uint8_t*>(w), w_scale, static_cast<__bf16*>(out), e_begin, k, T, K / 8,
                      kblocks, N, n_max);
   return hipGetLastError();
 }
 
 template <bool SWIGLU>
-hipError_t launch_product(const void* src, const int32_t* perm, const int32_t* offsets, const void* w,
+hipError_t launch_product(const void* src, const float* src_scale, const int32_t* perm, const int32_t* offsets, const void* w,
                           const float* w_scale, void* out, int E, int e_begin, int e_loc, int k, int64_t T, int K,
                           int N, int64_t n_max, hipStream_t stream) {
   const bool narrow = int8_few_columns(T, k, e_loc, N, SWIGLU) == 16 * (SWIGLU ? 1 : 2);
 #define MOE_FEW(F, A, G)                                                                                          \
-  return launch_one<SWIGLU, F, A, G>(src, perm, offsets, w, w_scale, out, E, e_begin, e_loc, k, T, K, N, n_max, \
+  return launch_one<SWIGLU, F, A, G>(src, nullptr, perm, offsets, w, w_scale, out, E, e_begin, e_loc, k, T, K, N, n_max, \
                                      stream)
+  if constexpr (SWIGLU) {  // h is bf16
+    if (src_scale != nullptr) {
+      if (narrow)
+        return launch_one<true, 2, 6, kWave, true>(src, src_scale, perm, offsets, w, w_scale, out, E, e_begin, e_loc, k,
+                                                   T, K, N, n_max, stream);
+      return launch_one<true, 4, 4, kWave, true>(src, src_scale, perm, offsets, w, w_scale, out, E, e_begin, e_loc, k, T,
+                                                 K, N, n_max, stream);
+    }
+  }
   if (int8_few_waves(T, k, E, K)) {
     if (narrow) MOE_FEW(2, 6, kWave);
     MOE_FEW(4, 4, kWave);
@@ -331,13 +348,13 @@ bool int8_few_fits(int64_t T, int K) {
   return T <= kFewTokens && few_rows(T) * code_stride(int8_kblocks(K)) <= kMaxCodes;
 }
 
-hipError_t launch_int8_few(const void* x, const int32_t* perm, const int32_t* offsets, const void* q_gu,
+hipError_t launch_int8_few(const void* x, const float* x_scale, const int32_t* perm, const int32_t* offsets, const void* q_gu,
                            const float* s_gu, const void* q_dn, const float* s_dn, void* h, void* y, int d, int d_ff,
                            int E, int e_begin, int e_loc, int k, int64_t T, int64_t n_max, hipStream_t stream) {
   const hipError_t e =
-      launch_product<true>(x, perm, offsets, q_gu, s_gu, h, E, e_begin, e_loc, k, T, d, d_ff, n_max, stream);
+      launch_product<true>(x, x_scale, perm, offsets, q_gu, s_gu, h, E, e_begin, e_loc, k, T, d, d_ff, n_max, stream);
   if (e != hipSuccess) return e;
-  return launch_product<false>(h, nullptr, offsets, q_dn, s_dn, y, E, e_begin, e_loc, k, T, d_ff, d, n_max, stream);
+  return launch_product<false>(h, nullptr, nullptr, offsets, q_dn, s_dn, y, E, e_begin, e_loc, k, T, d_ff, d, n_max, stream);
 }
 
 hipError_t launch_int8_thin(const void* a, const float* a_scale, const void* w, const float* w_scale, void* c,

@@ -27,6 +27,17 @@ using namespace int8;
 template <int G>
 constexpr int block_threads() { return G > 256 ? G : 256; }
 
+// The tiles of a call's GEMM launches, listed by one workgroup.
+__device__ __forceinline__ void list_tiles(void* plan, const int32_t* offsets, int e_begin, int e_end, int64_t n_max,
+                                           int tile_rows) {
+  int* count = static_cast<int*>(plan);
+  RowGroup* groups = reinterpret_cast<RowGroup*>(static_cast<char*>(plan) + kPlanHeader);
+  const int e_loc = e_end - e_begin, n = static_cast<int>(n_max);
+  if (tile_rows == kTallRows) plan_tiles<kTallRows, kTallMerge>(offsets, e_begin, e_loc, n, count, groups);
+  else if (tile_rows == kShortRows) plan_tiles<kShortRows, 0>(offsets, e_begin, e_loc, n, count, groups);
+  else plan_tiles<kThinRows, 0>(offsets, e_begin, e_loc, n, count, groups);
+}
+
 // Rows [0, N_loc) of the local segment: row r is row perm[seg0 + r] / k of src
 // (perm != nullptr: the dispatch's row gather) or row r. G threads per row, VPT
 // vectors of 8 bf16 per thread; the row's K-blocks are filled up with zeros. With
@@ -41,12 +52,7 @@ __global__ __launch_bounds__(block_threads<G>()) void quantize_rows_kernel(
   int turn = 0;
   const int planners = plan != nullptr ? 1 : 0;
   if (static_cast<int>(blockIdx.x) < planners) {
-    int* count = static_cast<int*>(plan);
-    int8::RowGroup* groups = reinterpret_cast<int8::RowGroup*>(static_cast<char*>(plan) + int8::kPlanHeader);
-    const int e_loc = e_end - e_begin, n = static_cast<int>(n_max);
-    if (tile_rows == kTallRows) plan_tiles<kTallRows, kTallMerge>(offsets, e_begin, e_loc, n, count, groups);
-    else if (tile_rows == kShortRows) plan_tiles<kShortRows, 0>(offsets, e_begin, e_loc, n, count, groups);
-    else plan_tiles<kThinRows, 0>(offsets, e_begin, e_loc, n, count, groups);
+    list_tiles(plan, offsets, e_begin, e_end, n_max, tile_rows);
     return;
   }
   const int64_t block = static_cast<int64_t>(blockIdx.x) - planners;
@@ -82,6 +88,34 @@ __global__ __launch_bounds__(block_threads<G>()) void quantize_rows_kernel(
         *reinterpret_cast<uint2*>(q + (static_cast<int64_t>(c >> 3) * n_max + r) * 64 + (c & 7) * 8) = codes8(f, inv);
       }
     }
+  }
+}
+
+// The same rows where tokens are in 8 bits already: codes [kblocks][T][64] and scales gathered
+// through perm. 16 threads copy a row's K-blocks, four of them one block.
+__global__ __launch_bounds__(256) void gather_codes_kernel(const uint4* __restrict__ codes,
+                                                           const float* __restrict__ codes_scale,
+                                                           const int32_t* __restrict__ perm,
+                                                           const int32_t* __restrict__ offsets, uint4* __restrict__ q,
+                                                           float* __restrict__ scale, int e_begin, int e_end, int k,
+                                                           int64_t T, int kblocks, int64_t n_max,
+                                                           void* __restrict__ plan, int tile_rows) {
+  constexpr int kRows = 16;
+  if (blockIdx.x == 0) {
+    list_tiles(plan, offsets, e_begin, e_end, n_max, tile_rows);
+    return;
+  }
+  const int seg0 = offsets[e_begin];
+  const int64_t n_loc = min(static_cast<int64_t>(offsets[e_end] - seg0), n_max);
+  const int li = static_cast<int>(threadIdx.x) % 16;
+  for (int64_t r = (static_cast<int64_t>(blockIdx.x) - 1) * kRows + threadIdx.x / 16; r < n_loc;
+       r += (static_cast<int64_t>(gridDim.x) - 1) * kRows) {
+    const int64_t from = perm[seg0 + r] / k;
+    const bool live = from >= 0 && from < T;
+    if (li == 0) scale[r] = live ? codes_scale[from] : kMinScale;
+    for (int c = li; c < kblocks * 4; c += 16)
+      q[(static_cast<int64_t>(c >> 2) * n_max + r) * 4 + (c & 3)] =
+          live ? codes[((c >> 2) * T + from) * 4 + (c & 3)] : make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -241,6 +275,16 @@ hipError_t launch_quantize_rows(const void* src, const int32_t* perm, const int3
   if (vec <= 4096) MOE_QROWS(1024, 4);
   MOE_QROWS(1024, 8);
 #undef MOE_QROWS
+}
+
+hipError_t launch_gather_codes(const void* codes, const float* codes_scale, const int32_t* perm, const int32_t* offsets,
+                               void* q, float* scale, int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max,
+                               void* plan, int tile_rows, hipStream_t stream) {
+  const int64_t blocks = (n_max + 15) / 16;
+  hipLaunchKernelGGL(gather_codes_kernel, dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048) + 1u), dim3(256), 0,
+                     stream, static_cast<const uint4*>(codes), codes_scale, perm, offsets, static_cast<uint4*>(q), scale,
+                     e_begin, e_end, k, T, int8_kblocks(cols), n_max, plan, tile_rows);
+  return hipGetLastError();
 }
 
 hipError_t launch_quantize_weights(const void* w, void* q, float* scale, int e_loc, int K, int N, bool bf16,

@@ -57,6 +57,13 @@ __device__ __forceinline__ void buffer_store16(uint4 v, __amdgpu_buffer_rsrc_t r
 hipError_t launch_route_topk(const float* logits, int32_t* idx, float* w, int64_t T, int E, int k,
                              hipStream_t stream);
 
+// Routing by scores (r.bias is a device pointer) and the gradient of its weights
+hipError_t launch_route_experts(const moe_router& r, const float* logits, int32_t* idx, float* w, int64_t T, int E,
+                                int k, hipStream_t stream);
+hipError_t launch_route_experts_backward(const moe_router& r, const float* logits, const int32_t* idx,
+                                         const float* d_w, float* d_logits, int64_t T, int E, int k,
+                                         hipStream_t stream);
+
 size_t dispatch_workspace_bytes(int64_t T, int k, int E);
 // byte offset of the debug error word in the dispatch workspace; SIZE_MAX in release builds
 size_t dispatch_debug_word_offset();
@@ -140,6 +147,14 @@ hipError_t launch_layer_norm_backward(const void* dy, const void* s, const void*
                                       const float* rstd, const void* ds, void* dx, void* dw, void* db, void* ws,
                                       int64_t T, int d, bool bf16, bool wbf16, hipStream_t stream);
 
+// Residual add and RMS norm (r, y, q may be null; s is written only with r), and its gradient (ds may be null)
+hipError_t launch_rms_norm(const void* x, const void* r, const void* w, float eps, void* y, void* s, float* rstd,
+                           void* q, float* q_scale, int64_t T, int d, bool bf16, bool wbf16, hipStream_t stream);
+size_t rms_norm_backward_workspace_bytes(int64_t T, int d);
+hipError_t launch_rms_norm_backward(const void* dy, const void* s, const void* w, const float* rstd, const void* ds,
+                                    void* dx, void* dw, void* ws, int64_t T, int d, bool bf16, bool wbf16,
+                                    hipStream_t stream);
+
 // Quantised matrices are stored in K-blocks of 64: [int8_kblocks(K)][rows][64] bytes
 int int8_kblocks(int K);
 int64_t int8_max_k();  // int32 sums of 127 * 127 * K, and rows held in registers
@@ -152,6 +167,10 @@ size_t int8_plan_bytes(int64_t n_max, int e_loc);
 hipError_t launch_quantize_rows(const void* src, const int32_t* perm, const int32_t* offsets, void* q, float* scale,
                                 int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max, void* plan,
                                 int tile_rows, hipStream_t stream);
+// the same of tokens that are codes [int8_kblocks(cols)][T][64] already
+hipError_t launch_gather_codes(const void* codes, const float* codes_scale, const int32_t* perm, const int32_t* offsets,
+                               void* q, float* scale, int e_begin, int e_end, int k, int64_t T, int cols, int64_t n_max,
+                               void* plan, int tile_rows, hipStream_t stream);
 // [e_loc, K, N] weights as codes [e_loc][int8_kblocks(K)][N][64] and scales [e_loc, N]
 hipError_t launch_quantize_weights(const void* w, void* q, float* scale, int e_loc, int K, int N, bool bf16,
                                    hipStream_t stream);
@@ -166,7 +185,8 @@ hipError_t launch_int8_thin(const void* a, const float* a_scale, const void* w, 
 int int8_few_columns(int64_t T, int k, int e_loc, int N, bool swiglu);
 bool int8_few_waves(int64_t T, int k, int E, int K);
 bool int8_few_fits(int64_t T, int K);
-hipError_t launch_int8_few(const void* x, const int32_t* perm, const int32_t* offsets, const void* q_gu,
+// (x_scale != nullptr: x is codes [kblocks][T][64] already)
+hipError_t launch_int8_few(const void* x, const float* x_scale, const int32_t* perm, const int32_t* offsets, const void* q_gu,
                            const float* s_gu, const void* q_dn, const float* s_dn, void* h, void* y, int d, int d_ff,
                            int E, int e_begin, int e_loc, int k, int64_t T, int64_t n_max, hipStream_t stream);
 
@@ -176,5 +196,8 @@ hipError_t launch_clip_grads(const moe_tensor* t, const moe_tensor* out, int n, 
                              hipStream_t stream);
 hipError_t launch_clip_grad_norm(const moe_tensor* t, const moe_tensor* out, int n, float max_norm, float* norm,
                                  void* ws, hipStream_t stream);
+
+
+hipError_t launch_adamw(const moe_adamw_tensor* t, int n, const moe_adamw_args& a, hipStream_t stream);
 
 }  // namespace moe
