@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import os
 import re
 from dataclasses import dataclass
@@ -485,9 +486,9 @@ def route_experts(logits, k: int, router: Router, topk_idx=None, topk_w=None, st
     s = shape(T, 8, 8, E, k, 0, E)
     with ctx:
         if topk_idx is None:
-            topk_idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+            topk_idx = logits.new_empty((T, k), dtype=torch.int32)
         if topk_w is None:
-            topk_w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+            topk_w = logits.new_empty((T, k))
         ctx.give(topk_idx, topk_w)
         _check(_load().moe_route_experts(ctypes.byref(s), ctypes.byref(r), logits.data_ptr(), topk_idx.data_ptr(),
                                          topk_w.data_ptr(), st), "moe_route_experts")
@@ -962,7 +963,7 @@ def route_experts_backward(logits, topk_idx, d_topk_w, router: Router, d_logits=
     s = shape(T, 8, 8, E, k, 0, E)
     with ctx:
         if d_logits is None:
-            d_logits = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+            d_logits = torch.empty_like(logits)
         ctx.give(d_logits)
         _check(_load().moe_route_experts_backward(ctypes.byref(s), ctypes.byref(r), logits.data_ptr(),
                                                   topk_idx.data_ptr(), d_topk_w.data_ptr(), d_logits.data_ptr(), st),
@@ -1525,26 +1526,35 @@ def adamw_states(params, bits: int = 32):
     return [one(p) for p in params], [one(p) for p in params]
 
 
-def _same_list(ts, name: str, like, dtype):
-    """A list of tensors of the shapes of another list, all of one dtype."""
+_dtype_of = operator.attrgetter("dtype")
+
+
+def _same_list(ts, name: str, params, sizes, dtypes):
+    """A list of tensors of the sizes of `params` and of one of the dtypes."""
+    size = _torch().Tensor.size
     ts = list(ts)
-    if len(ts) != len(like):
-        raise ValueError(f"{name} must hold {len(like)} tensors, got {len(ts)}")
-    for i, (t, p) in enumerate(zip(ts, like)):
-        if t is None or t.dtype is not dtype or t.shape != p.shape:
-            _want(t, f"{name}[{i}]", dtype, tuple(p.shape))
+    if len(ts) != len(params):
+        raise ValueError(f"{name} must hold {len(params)} tensors, got {len(ts)}")
+    try:
+        if dtypes.issuperset(map(_dtype_of, ts)) and list(map(size, ts)) == sizes:
+            return ts
+    except (AttributeError, TypeError):  # something else than tensors
+        pass
+    for i, (t, p) in enumerate(zip(ts, params)):
+        _want(t, f"{name}[{i}]", tuple(dtypes), tuple(p.shape))
     return ts
 
 
-def _state_list(ts, name: str, params):
+def _state_list(ts, name: str, params, sizes):
     """(tensors, scales or None) of a list of states."""
     torch = _torch()
     ts = list(ts)
-    if not any(isinstance(t, Float8State) for t in ts):
-        return _same_list(ts, name, params, torch.float32), None
-    if not all(isinstance(t, Float8State) for t in ts):
+    kinds = set(map(type, ts))
+    if Float8State not in kinds:
+        return _same_list(ts, name, params, sizes, {torch.float32}), None
+    if len(kinds) > 1:
         raise TypeError(f"{name} must hold fp32 tensors or Float8State, not both")
-    codes = _same_list([t.codes for t in ts], name, params, torch.float8_e4m3fn)
+    codes = _same_list([t.codes for t in ts], name, params, sizes, {torch.float8_e4m3fn})
     scales = [t.scale for t in ts]
     for i, (t, p) in enumerate(zip(scales, params)):
         n = -(-p.numel() // MOE_STATE_BLOCK)
@@ -1564,19 +1574,15 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps:
     gradients are clipped to max_norm on the way, without being written."""
     torch = _torch()
     params, numels, kinds = _tensor_list(params, "params")
-    grads = list(grads)
-    if len(grads) != len(params):
-        raise ValueError(f"grads must hold {len(params)} tensors, got {len(grads)}")
-    for i, (g, p) in enumerate(zip(grads, params)):
-        if g is None or g.dtype not in _CODES or g.shape != p.shape:
-            _want(g, f"grads[{i}]", _act_dtypes(), tuple(p.shape))
-    m, m_scale = _state_list(exp_avg, "exp_avg", params)
-    v, v_scale = _state_list(exp_avg_sq, "exp_avg_sq", params)
+    sizes = list(map(torch.Tensor.size, params))
+    grads = _same_list(grads, "grads", params, sizes, set(_CODES))
+    m, m_scale = _state_list(exp_avg, "exp_avg", params, sizes)
+    v, v_scale = _state_list(exp_avg_sq, "exp_avg_sq", params, sizes)
     if (m_scale is None) != (v_scale is None):
         raise TypeError("exp_avg and exp_avg_sq must both be fp32 or both Float8State")
     n = len(params)
-    w = [None] * n if masters is None else list(masters)
-    if len(w) != n:
+    w = () if masters is None else list(masters)
+    if masters is not None and len(w) != n:
         raise ValueError(f"masters must hold {n} tensors, got {len(w)}")
     for i, (t, p) in enumerate(zip(w, params)):
         if t is not None:
@@ -1622,7 +1628,7 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps:
         flat[5::9] = map(ptr, m_scale)
         flat[6::9] = map(ptr, v_scale)
     flat[7::9] = numels
-    flat[8::9] = [kind | _CODES[g.dtype] << 32 for kind, g in zip(kinds, grads)]
+    flat[8::9] = [kind | code << 32 for kind, code in zip(kinds, map(_CODES.__getitem__, map(_dtype_of, grads)))]
     host = array.array("q", flat)
     with ctx:
         _check(_load().moe_adamw(host.buffer_info()[0], n, ctypes.byref(args), h), "moe_adamw")
