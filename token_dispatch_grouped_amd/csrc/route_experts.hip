@@ -9,6 +9,7 @@
 // computed in fp64 and rounded to fp32 once: two ways to compute it then agree but for
 // a value within 2^-52 of the middle between two fp32 numbers. Equal c go to the
 // lower id. Without a bias the scores rise with the logits, and these are compared.
+#include <limits.h>
 #include <math.h>
 
 #include "moe_internal.h"
@@ -241,18 +242,20 @@ __device__ __forceinline__ int key_id(double k) { return kMaxExperts - 1 - (__do
 
 __device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
 __device__ __forceinline__ double smaller(double a, double b) { return __builtin_fmin(a, b); }
+__device__ __forceinline__ int larger(int a, int b) { return max(a, b); }
+__device__ __forceinline__ int smaller(int a, int b) { return min(a, b); }
 
 // The pair (a[i], a[j]) in descending order.
-template <int N>
-__device__ __forceinline__ void order(double (&a)[N], int i, int j) {
-  const double hi = larger(a[i], a[j]), lo = smaller(a[i], a[j]);
+template <typename T, int N>
+__device__ __forceinline__ void order(T (&a)[N], int i, int j) {
+  const T hi = larger(a[i], a[j]), lo = smaller(a[i], a[j]);
   a[i] = hi;
   a[j] = lo;
 }
 
 // A bitonic list in descending order.
-template <int N>
-__device__ __forceinline__ void sort_bitonic(double (&a)[N]) {
+template <typename T, int N>
+__device__ __forceinline__ void sort_bitonic(T (&a)[N]) {
 #pragma unroll
   for (int stride = N / 2; stride > 0; stride >>= 1)
 #pragma unroll
@@ -261,8 +264,8 @@ __device__ __forceinline__ void sort_bitonic(double (&a)[N]) {
 }
 
 // Any list in descending order: Batcher's odd-even merge sort.
-template <int N>
-__device__ __forceinline__ void sort_any(double (&a)[N]) {
+template <typename T, int N>
+__device__ __forceinline__ void sort_any(T (&a)[N]) {
 #pragma unroll
   for (int p = 1; p < N; p <<= 1)
 #pragma unroll
@@ -275,9 +278,9 @@ __device__ __forceinline__ void sort_any(double (&a)[N]) {
 }
 
 // a := the N largest of two descending lists, descending.
-template <int N>
-__device__ __forceinline__ void merge(double (&a)[N], const double (&b)[N]) {
-  double m[N];
+template <typename T, int N>
+__device__ __forceinline__ void merge(T (&a)[N], const T (&b)[N]) {
+  T m[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) m[i] = larger(a[i], b[N - 1 - i]);
   sort_bitonic(m);
@@ -288,18 +291,41 @@ __device__ __forceinline__ void merge(double (&a)[N], const double (&b)[N]) {
 // The value of the lane that differs in the bit OFF of its number, where all lanes of a
 // smaller block hold the same (the mirrors reach another lane of the same block).
 template <int OFF>
-__device__ __forceinline__ uint32_t from_partner(uint32_t v) {
-  const int i = static_cast<int>(v);
-  if constexpr (OFF == 1) return __builtin_amdgcn_update_dpp(0, i, 0xB1, 0xF, 0xF, false);        // quad_perm [1,0,3,2]
-  else if constexpr (OFF == 2) return __builtin_amdgcn_update_dpp(0, i, 0x4E, 0xF, 0xF, false);   // quad_perm [2,3,0,1]
-  else if constexpr (OFF == 4) return __builtin_amdgcn_update_dpp(0, i, 0x141, 0xF, 0xF, false);  // row_half_mirror
-  else if constexpr (OFF == 8) return __builtin_amdgcn_update_dpp(0, i, 0x140, 0xF, 0xF, false);  // row_mirror
+__device__ __forceinline__ int from_partner(int v) {
+  if constexpr (OFF == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);        // quad_perm [1,0,3,2]
+  else if constexpr (OFF == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);   // quad_perm [2,3,0,1]
+  else if constexpr (OFF == 4) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);  // row_half_mirror
+  else if constexpr (OFF == 8) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);  // row_mirror
   else return __shfl_xor(v, OFF);
 }
 template <int OFF>
+__device__ __forceinline__ uint32_t from_partner(uint32_t v) {
+  return static_cast<uint32_t>(from_partner<OFF>(static_cast<int>(v)));
+}
+template <int OFF>
 __device__ __forceinline__ double from_partner(double v) {
-  return __hiloint2double(static_cast<int>(from_partner<OFF>(static_cast<uint32_t>(__double2hiint(v)))),
-                          static_cast<int>(from_partner<OFF>(static_cast<uint32_t>(__double2loint(v)))));
+  return __hiloint2double(from_partner<OFF>(__double2hiint(v)), from_partner<OFF>(__double2loint(v)));
+}
+
+// The value of the lane whose number differs in the bits of M.
+template <int M>
+__device__ __forceinline__ int xor_lane(int v) {
+  if constexpr (M == 0) return v;
+  else if constexpr (M == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);
+  else if constexpr (M == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);
+  else if constexpr (M == 3) return __builtin_amdgcn_mov_dpp(v, 0x1B, 0xF, 0xF, true);  // quad_perm [3,2,1,0]
+  else if constexpr (M < 8) return xor_lane<7 ^ M>(__builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true));
+  else if constexpr (M < 16) return xor_lane<15 ^ M>(__builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true));
+  else return __shfl_xor(v, M);
+}
+
+// Calls f(value, group) for every other lane of the token's G.
+template <int G, int M = 1, typename F>
+__device__ __forceinline__ void other_lanes(int v, int g, int log_p, F&& f) {
+  if constexpr (M < G) {
+    f(xor_lane<M>(v), (g ^ M) >> log_p);
+    other_lanes<G, M + 1>(v, g, log_p, f);
+  }
 }
 
 template <int G, int OFF = 1, typename T>
@@ -316,24 +342,24 @@ __device__ __forceinline__ float group_top(float v) {
   return v;
 }
 
-template <int G, int L, int OFF = 1>
-__device__ __forceinline__ void merge_lanes(double (&a)[L]) {
+template <int G, int OFF = 1, typename T, int L>
+__device__ __forceinline__ void merge_lanes(T (&a)[L]) {
   if constexpr (OFF < G) {
-    double b[L];
+    T b[L];
 #pragma unroll
     for (int i = 0; i < L; ++i) b[i] = from_partner<OFF>(a[i]);
     merge(a, b);
-    merge_lanes<G, L, 2 * OFF>(a);
+    merge_lanes<G, 2 * OFF>(a);
   }
 }
 
 // The two largest of the P lanes of a group, to all of them.
-template <int G, int OFF = 1>
-__device__ __forceinline__ void merge_two(uint32_t& first, uint32_t& second, int P) {
+template <int G, int OFF = 1, typename T>
+__device__ __forceinline__ void merge_two(T& first, T& second, int P) {
   if constexpr (OFF < G) {
-    const uint32_t f = from_partner<OFF>(first), s = from_partner<OFF>(second);
+    const T f = from_partner<OFF>(first), s = from_partner<OFF>(second);
     if (OFF < P) {
-      const uint32_t rest = min(first, f);
+      const T rest = min(first, f);
       first = max(first, f);
       second = max(rest, max(second, s));
     }
@@ -345,161 +371,381 @@ __device__ __forceinline__ void merge_two(uint32_t& first, uint32_t& second, int
 // weights of the chosen ones need; or turn each into its score.
 enum class Route { kLogits, kLogitsTotal, kSigmoid, kSoftmax };
 
+// The tokens of a wave: their rows as one buffer, from which a lane reads VPL values from its first
+// expert on, whoever's they are (0 past the last token), and uses its own.
+template <int G, int VPL>
+struct Rows {
+  static constexpr int kTokens = kWave / G;  // of a wave
+  __amdgpu_buffer_rsrc_t buffer;
+  uint32_t row;      // of this lane's token, in bytes
+  int64_t t;
+  bool live, fours;  // fours: no four values of a lane lie across the end of the buffer
+  int g, group, own, e0;
+
+  __device__ Rows(const RouteArgs& a, int P, int per, int64_t t0) {
+    const int lane = lane_id(), size = a.E / a.groups;
+    g = lane % G;
+    group = g / P;
+    const int first = g % P * per;                                // of this lane, in its group
+    own = group < a.groups ? max(min(per, size - first), 0) : 0;  // experts of this lane
+    e0 = group * size + first;
+    fours = (size | per) % 4 == 0;
+    t = t0 + lane / G;
+    live = t < a.T;
+    row = static_cast<uint32_t>(lane / G * a.E) * 4u;
+    buffer = make_rsrc(a.logits + t0 * a.E,
+                       static_cast<uint32_t>(min(a.T - t0, static_cast<int64_t>(kTokens)) * a.E * 4));
+  }
+  __device__ void load(__amdgpu_buffer_rsrc_t from, uint32_t at, float (&to)[VPL]) const {
+    if (fours) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += 4) {
+        const uint4 q = buffer_load16(from, at + i * 4u);
+        to[i] = __uint_as_float(q.x);
+        to[i + 1] = __uint_as_float(q.y);
+        to[i + 2] = __uint_as_float(q.z);
+        to[i + 3] = __uint_as_float(q.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) to[i] = one(from, at + i * 4u);
+    }
+  }
+  __device__ static float one(__amdgpu_buffer_rsrc_t from, uint32_t at) {
+    return __uint_as_float(
+        static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b32(from, static_cast<int>(at), 0, 0)));
+  }
+  __device__ void logits(float (&v)[VPL]) const { load(buffer, row + e0 * 4u, v); }
+  __device__ float logit(int e) const { return one(buffer, row + e * 4u); }
+  // no bias: a buffer of no bytes, all zeros
+  __device__ static __amdgpu_buffer_rsrc_t bias_buffer(const RouteArgs& a) {
+    return make_rsrc(a.bias, a.bias != nullptr ? static_cast<uint32_t>(a.E) * 4u : 0u);
+  }
+};
+
+// Where a wave keeps its tokens' candidates.
+template <int G, int L>
+struct Candidates {
+  static constexpr int kMost = G < 2 * L ? 2 * L : G;  // of a token
+  double key[kWave / G][kMost];
+  uint16_t id[kWave / G][kMost];
+};
+
+// The wave's tokens, with every score in fp64.
 template <int G, int VPL, int L, Route MODE>
-__global__ __launch_bounds__(kThreads) void route_kernel(const RouteArgs a, int P, int per) {
-  constexpr int kTokens = kWave / G;   // of a wave
+__device__ __forceinline__ void route_exact(const RouteArgs& a, const Rows<G, VPL>& in, int P) {
   constexpr int kSlots = (L + G - 1) / G;
   constexpr int kRun = VPL < L ? VPL : L;
   constexpr float kLog2e = 1.44269504f;
   constexpr bool kScores = MODE == Route::kSigmoid || MODE == Route::kSoftmax;
-  const int lane = lane_id(), g = lane % G;
-  const int size = a.E / a.groups, group = g / P, first = g % P * per;  // of this lane, in its group
-  const int own = group < a.groups ? min(per, size - first) : 0;        // experts of this lane (may be < 0)
-  const int e0 = group * size + first;
-  const bool fours = (size | per) % 4 == 0;  // no four of a lane lie across the end of the buffer
-  const int64_t wave = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + uniform(static_cast<int>(threadIdx.x) / kWave);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kWavesPerBlock * kTokens;
-  for (int64_t t0 = wave * kTokens; t0 < a.T; t0 += step) {
-    const int64_t t = t0 + lane / G;
-    const bool live = t < a.T;
-    // The wave's rows as one buffer: a lane reads VPL values from its first expert on, whoever's they are (0 past
-    // the last token), and uses its own.
-    const __amdgpu_buffer_rsrc_t rows = make_rsrc(
-        a.logits + t0 * a.E, static_cast<uint32_t>(min(a.T - t0, static_cast<int64_t>(kTokens)) * a.E * 4));
-    const uint32_t row = static_cast<uint32_t>(lane / G * a.E) * 4u;
-    float v[VPL], bias[kScores ? VPL : 1];
-    auto load = [&](__amdgpu_buffer_rsrc_t from, uint32_t at, float* to) {
-      if (fours) {
+  const int lane = lane_id(), g = in.g, own = in.own, e0 = in.e0, group = in.group, size = a.E / a.groups;
+  const bool live = in.live;
+  const int64_t t = in.t;
+  float v[VPL], bias[kScores ? VPL : 1];
+  in.logits(v);
+  if constexpr (kScores) in.load(in.bias_buffer(a), e0 * 4u, bias);
+  float top = 0.f;
+  double total = 1.0;  // its inverse for kSoftmax
+  if constexpr (MODE == Route::kLogitsTotal || MODE == Route::kSoftmax) {
+    top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPL; i += 4) {
-          const uint4 q = buffer_load16(from, at + i * 4u);
-          to[i] = __uint_as_float(q.x);
-          to[i + 1] = __uint_as_float(q.y);
-          to[i + 2] = __uint_as_float(q.z);
-          to[i + 3] = __uint_as_float(q.w);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          to[i] = __uint_as_float(static_cast<uint32_t>(
-              __builtin_amdgcn_raw_buffer_load_b32(from, static_cast<int>(at + i * 4u), 0, 0)));
-      }
-    };
-    load(rows, row + e0 * 4u, v);
-    if constexpr (kScores)  // no bias: a buffer of no bytes, all zeros
-      load(make_rsrc(a.bias, a.bias != nullptr ? static_cast<uint32_t>(a.E) * 4u : 0u), e0 * 4u, bias);
-    float top = 0.f;
-    double total = 1.0;  // its inverse for kSoftmax
-    if constexpr (MODE == Route::kLogitsTotal || MODE == Route::kSoftmax) {
-      top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) top = i < own && v[i] > top ? v[i] : top;
-      top = group_top<G>(top);
-      if constexpr (MODE == Route::kSoftmax) {
-        total = 0.0;
+    for (int i = 0; i < VPL; ++i) top = i < own && v[i] > top ? v[i] : top;
+    top = group_top<G>(top);
+    if constexpr (MODE == Route::kSoftmax) {
+      total = 0.0;
 #pragma unroll 4
-        for (int i = 0; i < VPL; ++i) total += i < own ? exp64(static_cast<double>(v[i]) - top) : 0.0;
-        total = inverse64(group_sum<G>(total));
-      } else {  // fp32 is enough for the weights
-        float sum = 0.f;
+      for (int i = 0; i < VPL; ++i) total += i < own ? exp64(static_cast<double>(v[i]) - top) : 0.0;
+      total = inverse64(group_sum<G>(total));
+    } else {  // fp32 is enough for the weights
+      float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) sum += i < own ? __builtin_amdgcn_exp2f((v[i] - top) * kLog2e) : 0.f;
-        total = group_sum<G>(sum);
+      for (int i = 0; i < VPL; ++i) sum += i < own ? __builtin_amdgcn_exp2f((v[i] - top) * kLog2e) : 0.f;
+      total = group_sum<G>(sum);
+    }
+  }
+  double best[L];
+#pragma unroll
+  for (int i = kRun; i < L; ++i) best[i] = 1.0;
+  // runs of L values, each sorted alone, then the L largest of it and those before
+#pragma unroll
+  for (int r = 0; r < VPL; r += kRun) {
+    __builtin_amdgcn_sched_barrier(0);  // one run's scores at a time: all at once take 300 registers
+    double run[kRun];
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      float c = v[r + i];
+      if constexpr (kScores) {
+        const double s = MODE == Route::kSigmoid ? sigmoid64(c) : exp64(static_cast<double>(c) - top) * total;
+        c = static_cast<float>(s + static_cast<double>(bias[r + i]));
       }
+      run[i] = r + i < own ? key_of(orderable(c), e0 + r + i) : 1.0;
     }
-    double best[L];
+    sort_any(run);
+    if constexpr (VPL > L) {
+      if (r > 0) merge(best, run);
+      else
 #pragma unroll
-    for (int i = kRun; i < L; ++i) best[i] = 1.0;
-    // runs of L values, each sorted alone, then the L largest of it and those before
+        for (int i = 0; i < L; ++i) best[i] = run[i];
+    } else {
 #pragma unroll
-    for (int r = 0; r < VPL; r += kRun) {
-      __builtin_amdgcn_sched_barrier(0);  // one run's scores at a time: all at once take 300 registers
-      double run[kRun];
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        float c = v[r + i];
-        if constexpr (kScores) {
-          const double s = MODE == Route::kSigmoid ? sigmoid64(c) : exp64(static_cast<double>(c) - top) * total;
-          c = static_cast<float>(s + static_cast<double>(bias[r + i]));
-        }
-        run[i] = r + i < own ? key_of(orderable(c), e0 + r + i) : 1.0;
-      }
-      sort_any(run);
-      if constexpr (VPL > L) {
-        if (r > 0) merge(best, run);
-        else
-#pragma unroll
-          for (int i = 0; i < L; ++i) best[i] = run[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) best[i] = run[i];
-      }
+      for (int i = 0; i < kRun; ++i) best[i] = run[i];
     }
-    if (a.top_groups < a.groups) {
-      uint32_t one = key_ord(best[0]), two = L > 1 ? key_ord(best[1]) : 0;
-      merge_two<G>(one, two, P);
-      const uint32_t mine = a.group_top == 2 && size > 1 ? orderable(from_orderable(one) + from_orderable(two)) : one;
-      int before = 0;
-      for (int i = 0; i < a.groups; ++i) {
-        const uint32_t other = __shfl(mine, lane - g + i * P);
-        before += other > mine || (other == mine && i < group);
-      }
-      if (before >= a.top_groups)
+  }
+  if (a.top_groups < a.groups) {
+    uint32_t one = key_ord(best[0]), two = L > 1 ? key_ord(best[1]) : 0;
+    merge_two<G>(one, two, P);
+    const uint32_t mine = a.group_top == 2 && size > 1 ? orderable(from_orderable(one) + from_orderable(two)) : one;
+    int before = 0;  // lanes of groups before this one
+    other_lanes<G>(static_cast<int>(mine), g, __ffs(P) - 1, [&](int value, int of) {
+      const uint32_t other = static_cast<uint32_t>(value);
+      before += other > mine || (other == mine && of < group);
+    });
+    if (before >= a.top_groups * P)
 #pragma unroll
-        for (int i = 0; i < L; ++i) best[i] = 1.0;
-    }
-    merge_lanes<G>(best);
-    // chosen expert s * G + g to lane g
-    int id[kSlots];
-    float z[kSlots];
+      for (int i = 0; i < L; ++i) best[i] = 1.0;
+  }
+  merge_lanes<G>(best);
+  // chosen expert s * G + g to lane g
+  int id[kSlots];
+  float z[kSlots];
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
-      double mine = best[s * G < L ? s * G : 0];
+  for (int s = 0; s < kSlots; ++s) {
+    double mine = best[s * G < L ? s * G : 0];
 #pragma unroll
-      for (int i = 1; i < G; ++i)
-        if (s * G + i < L) mine = g == i ? best[s * G + i] : mine;
-      const int j = s * G + g;
-      id[s] = key_id(mine);
-      const int bits = __builtin_amdgcn_raw_buffer_load_b32(rows, static_cast<int>(row + id[s] * 4u), 0, 0);
-      z[s] = live && j < a.k ? __uint_as_float(static_cast<uint32_t>(bits)) : -INFINITY;
-    }
-    double w[kSlots], sum = 0.0;
-    if (!a.sigmoid && a.renormalize) {  // softmax over the chosen
-      top = z[0];
+    for (int i = 1; i < G; ++i)
+      if (s * G + i < L) mine = g == i ? best[s * G + i] : mine;
+    const int j = s * G + g;
+    id[s] = key_id(mine);
+    const float x = in.logit(id[s]);
+    z[s] = live && j < a.k ? x : -INFINITY;
+  }
+  double w[kSlots], sum = 0.0;
+  if (!a.sigmoid && a.renormalize) {  // softmax over the chosen
+    top = z[0];
 #pragma unroll
-      for (int s = 1; s < kSlots; ++s) top = z[s] > top ? z[s] : top;
-      top = group_top<G>(top);
-    }
+    for (int s = 1; s < kSlots; ++s) top = z[s] > top ? z[s] : top;
+    top = group_top<G>(top);
+  }
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
-      w[s] = a.sigmoid ? sigmoid64(z[s]) : exp64(static_cast<double>(z[s]) - top);
-      sum += s * G + g < a.k ? w[s] : 0.0;
-    }
-    if (a.renormalize) sum = group_sum<G>(sum) + (a.sigmoid ? 1e-20 : 0.0);
-    else sum = MODE == Route::kLogitsTotal ? total : MODE == Route::kSoftmax ? 1.0 / total : 1.0;
+  for (int s = 0; s < kSlots; ++s) {
+    w[s] = a.sigmoid ? sigmoid64(z[s]) : exp64(static_cast<double>(z[s]) - top);
+    sum += s * G + g < a.k ? w[s] : 0.0;
+  }
+  if (a.renormalize) sum = group_sum<G>(sum) + (a.sigmoid ? 1e-20 : 0.0);
+  else sum = MODE == Route::kLogitsTotal ? total : MODE == Route::kSoftmax ? 1.0 / total : 1.0;
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
-      const int j = s * G + g;
-      if (live && j < a.k) {
-        a.idx[t * a.k + j] = id[s];
-        a.w[t * a.k + j] = static_cast<float>(a.scale * (w[s] / sum));
-      }
+  for (int s = 0; s < kSlots; ++s) {
+    const int j = s * G + g;
+    if (live && j < a.k) {
+      a.idx[t * a.k + j] = id[s];
+      a.w[t * a.k + j] = static_cast<float>(a.scale * (w[s] / sum));
     }
   }
 }
 
-template <int G, int VPL, int L, Route MODE>
+// Signed integers that order like the values (of which none is -0.0); a NaN is above all or below all.
+__device__ __forceinline__ int signed_order(float v) {
+  const int b = static_cast<int>(__float_as_uint(v));
+  return b ^ static_cast<int>(static_cast<uint32_t>(b >> 31) >> 1);
+}
+__device__ __forceinline__ float from_signed(int o) {
+  return __uint_as_float(static_cast<uint32_t>(o ^ static_cast<int>(static_cast<uint32_t>(o >> 31) >> 1)));
+}
+
+// How far the fp32 form of a sigmoid's choice value can be from the exact one, doubled. In units of
+// 2^-24: the exponential's argument |x| s (1 - s) <= 0.23, its value 2 s (1 - s) <= 0.5, the sum with
+// one 1, the inverse 2: 4; the sum with the bias, and the exact value's rounding to fp32, |c| each.
+__device__ __forceinline__ float margin(float c) { return 0x1p-21f + fabsf(c) * 0x1p-22f; }
+
+// Sigmoid scores on fp32 values alone, 32 bits a comparison: the k-th largest of a token's values is
+// found (not whose it is), every expert from it on (less the values' error) becomes a candidate
+// in LDS, and the candidates, hardly ever more than k, are ranked by their exact choice values.
+// Groups that are too close to each other for fp32 are ranked by the exact values of their lanes' best
+// two. False where that does not decide: a NaN, or more candidates than there is room for (many
+// equal values).
+template <int G, int VPL, int L>
+__device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VPL>& in, int P,
+                                            Candidates<G, L>& room) {
+  static_assert(G >= 8 && G <= 32, "a lane has room for all of a token's candidates otherwise");
+  constexpr int kSlots = Candidates<G, L>::kMost / G;
+  constexpr int kRun = VPL < L ? VPL : L;
+  constexpr float kLog2e = 1.44269504f;
+  const int lane = lane_id(), g = in.g, token = lane / G, size = a.E / a.groups;
+  int own = in.own;
+  float v[VPL], bias[VPL];
+  in.logits(v);
+  in.load(in.bias_buffer(a), in.e0 * 4u, bias);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    v[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v[i] * -kLog2e)) + bias[i];
+  // the exact choice value of one expert
+  auto exact = [&](int e) {
+    return static_cast<float>(sigmoid64(in.logit(e)) + static_cast<double>(in.one(in.bias_buffer(a), e * 4u)));
+  };
+  int o[VPL], best[L];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) o[i] = i < own ? signed_order(v[i]) : INT_MIN;
+#pragma unroll
+  for (int i = kRun; i < L; ++i) best[i] = INT_MIN;
+#pragma unroll
+  for (int r = 0; r < VPL; r += kRun) {
+    int run[kRun];
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) run[i] = o[r + i];
+    sort_any(run);
+    if constexpr (VPL > L) {
+      if (r > 0) merge(best, run);
+      else
+#pragma unroll
+        for (int i = 0; i < L; ++i) best[i] = run[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) best[i] = run[i];
+    }
+  }
+  bool sure = best[0] <= signed_order(INFINITY);
+  if (a.top_groups < a.groups) {
+    int one = best[0], two = best[1];
+    merge_two<G>(one, two, P);
+    float mine = a.group_top == 2 && size > 1 ? from_signed(one) + from_signed(two) : from_signed(one);
+    if (in.group >= a.groups) mine = -INFINITY;
+    const float slack = 2.f * margin(mine);  // of a sum of two
+    int above = 0, beside = 0;  // lanes of groups before this one for sure, and perhaps
+    other_lanes<G>(static_cast<int>(__float_as_uint(mine)), g, __ffs(P) - 1, [&](int value, int of) {
+      const float other = __uint_as_float(static_cast<uint32_t>(value));
+      above += other > mine + slack;
+      beside += of != in.group && !(other < mine - slack);
+    });
+    const bool close = in.group < a.groups && above < a.top_groups * P && beside >= a.top_groups * P;
+    if (__any(in.live && close)) {
+      const float second = best[1] != INT_MIN ? from_signed(best[1]) : -INFINITY;
+      const int from = signed_order(second - margin(second));
+      uint32_t near = 0, first_ord = 0, second_ord = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) near |= static_cast<uint32_t>(i < own && o[i] >= from) << i;
+      while (near != 0) {
+        const int e = in.e0 + __ffs(near) - 1;
+        near &= near - 1;
+        const uint32_t c = orderable(exact(e));
+        second_ord = max(second_ord, min(first_ord, c));
+        first_ord = max(first_ord, c);
+      }
+      merge_two<G>(first_ord, second_ord, P);
+      const uint32_t rank_by = in.group >= a.groups ? 0u
+                               : a.group_top == 2 && size > 1
+                                   ? orderable(from_orderable(first_ord) + from_orderable(second_ord))
+                                   : first_ord;
+      above = 0;
+      other_lanes<G>(static_cast<int>(rank_by), g, __ffs(P) - 1, [&](int value, int of) {
+        const uint32_t other = static_cast<uint32_t>(value);
+        above += other > rank_by || (other == rank_by && of < in.group);
+      });
+    }
+    if (above >= a.top_groups * P) {
+      own = 0;
+#pragma unroll
+      for (int i = 0; i < L; ++i) best[i] = INT_MIN;
+    }
+  }
+  merge_lanes<G>(best);
+  int least = best[0];
+#pragma unroll
+  for (int i = 1; i < L; ++i) least = i == a.k - 1 ? best[i] : least;
+  least = signed_order(from_signed(least) - margin(from_signed(least)));
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) mine |= static_cast<uint32_t>(o[i] >= least) << i;
+  if (own == 0) mine = 0;
+  // candidates in the order of their ids
+  int at = __popc(mine);
+#pragma unroll
+  for (int off = 1; off < G; off *= 2) {
+    const int other = __shfl_up(at, off, G);
+    at += g >= off ? other : 0;
+  }
+  const int count = __shfl(at, lane | (G - 1));
+  at -= __popc(mine);
+  sure = sure && count >= a.k && count <= Candidates<G, L>::kMost;
+  if (__any(in.live && !sure)) return false;
+  while (mine != 0) {
+    const int i = __ffs(mine) - 1;
+    mine &= mine - 1;
+    if (at < Candidates<G, L>::kMost) room.id[token][at] = static_cast<uint16_t>(in.e0 + i);
+    ++at;
+  }
+  wave_sync();
+  int id[kSlots], rank[kSlots];
+  double s[kSlots], key[kSlots];
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const int j = q * G + g;
+    id[q] = j < count ? room.id[token][j] : 0;
+    s[q] = sigmoid64(in.logit(id[q]));
+    const float c = static_cast<float>(s[q] + static_cast<double>(in.one(in.bias_buffer(a), id[q] * 4u)));
+    key[q] = j < count ? key_of(orderable(c), id[q]) : 1.0;
+    room.key[token][j] = key[q];
+    rank[q] = 0;
+  }
+  wave_sync();
+  auto rank_against = [&](int first) {
+#pragma unroll
+    for (int j = first; j < first + G; ++j) {
+      const double other = room.key[token][j];
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) rank[q] += other > key[q];
+    }
+  };
+  rank_against(0);
+#pragma unroll
+  for (int q = 1; q < kSlots; ++q)
+    if (__any(in.live && count > q * G)) rank_against(q * G);
+  wave_sync();  // the next tokens' candidates are written over these
+  double sum = 0.0;
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    rank[q] = q * G + g < count ? rank[q] : a.k;
+    sum += rank[q] < a.k ? s[q] : 0.0;
+  }
+  sum = a.renormalize ? group_sum<G>(sum) + 1e-20 : 1.0;
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    if (in.live && rank[q] < a.k) {
+      a.idx[in.t * a.k + rank[q]] = id[q];
+      a.w[in.t * a.k + rank[q]] = static_cast<float>(a.scale * (s[q] / sum));
+    }
+  }
+  return true;
+}
+
+template <int G, int VPL, int L, Route MODE, bool QUICK>
+__global__ __launch_bounds__(kThreads) void route_kernel(const RouteArgs a, int P, int per) {
+  using In = Rows<G, VPL>;
+  const int wv = uniform(static_cast<int>(threadIdx.x) / kWave);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWavesPerBlock * In::kTokens;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + wv) * In::kTokens; t0 < a.T; t0 += step) {
+    const In in(a, P, per, t0);
+    if constexpr (QUICK) {
+      __shared__ Candidates<G, L> room[kWavesPerBlock];
+      if (route_quick<G, VPL, L>(a, in, P, room[wv])) continue;
+    }
+    route_exact<G, VPL, L, MODE>(a, in, P);
+  }
+}
+
+template <int G, int VPL, int L, Route MODE, bool QUICK = false>
 hipError_t launch_route(const RouteArgs& a, int P, int per, hipStream_t stream) {
   const int64_t tokens = kWavesPerBlock * (kWave / G);
   const int64_t blocks = min((a.T + tokens - 1) / tokens, int64_t{1} << 20);
-  hipLaunchKernelGGL((route_kernel<G, VPL, L, MODE>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a,
-                     P, per);
+  hipLaunchKernelGGL((route_kernel<G, VPL, L, MODE, QUICK>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
+                     stream, a, P, per);
   return hipGetLastError();
 }
 
 template <int G, int VPL, int L>
 hipError_t launch_route_mode(const RouteArgs& a, int P, int per, hipStream_t stream) {
-  if (a.by_score && a.sigmoid) return launch_route<G, VPL, L, Route::kSigmoid>(a, P, per, stream);
+  // what comes after the search for candidates costs as much as 16 scores a lane
+  constexpr bool kQuick = G >= 8 && G <= 32 && VPL >= 16;
+  if (a.by_score && a.sigmoid) return launch_route<G, VPL, L, Route::kSigmoid, kQuick>(a, P, per, stream);
   if (a.by_score) return launch_route<G, VPL, L, Route::kSoftmax>(a, P, per, stream);
   if (!a.sigmoid && !a.renormalize) return launch_route<G, VPL, L, Route::kLogitsTotal>(a, P, per, stream);
   return launch_route<G, VPL, L, Route::kLogits>(a, P, per, stream);
