@@ -717,8 +717,10 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
   return true;
 }
 
+// Waves per SIMD (registers: 128 or 170) where tokens are many: 131072 x 256 sigmoids in 8 groups 72 us
+// with two, 58 with three, 55 with four; softmax scores 125, 106, 114; logits with their sum three 43, four 50.
 template <int G, int VPL, int L, Route MODE, bool QUICK>
-__global__ __launch_bounds__(kThreads) void route_kernel(const RouteArgs a, int P, int per) {
+__global__ __launch_bounds__(kThreads, MODE == Route::kSoftmax || MODE == Route::kLogitsTotal ? 3 : 4) void route_kernel(const RouteArgs a, int P, int per) {
   using In = Rows<G, VPL>;
   const int wv = uniform(static_cast<int>(threadIdx.x) / kWave);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWavesPerBlock * In::kTokens;
@@ -763,26 +765,81 @@ hipError_t launch_route_top(const RouteArgs& a, int P, int per, hipStream_t stre
 //   softmax                 p_e ([e chosen] u_e - sum u p) for every expert
 //   sigmoid, renormalised   S = sum s + 1e-20:  (u_j - sum u s / S) / S * s_j (1 - s_j)
 //   sigmoid                 u_j s_j (1 - s_j)
-// One wave per token, the row assembled in LDS and copied out.
+// Bound by writing d_logits. Rows are put together in LDS and leave as one run.
+
+// n floats from LDS by one wave.
+__device__ __forceinline__ void write_run(const float* __restrict__ from, float* __restrict__ to, int n) {
+  typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
+  const int lane = lane_id();
+  for (int i = lane * 4; i + 4 <= n; i += kWave * 4) {
+    const float4 v = *reinterpret_cast<const float4*>(from + i);
+    *reinterpret_cast<f32x4*>(to + i) = f32x4{v.x, v.y, v.z, v.w};
+  }
+  const int i = (n & ~3) + lane;
+  if (i < n) to[i] = from[i];
+}
+
+// Every gradient but that of the plain softmax is 0 outside the chosen experts. S lanes (a power
+// of two, k <= S) share a token, a wave takes as many tokens as their rows fit its LDS.
+// 16384 tokens x 8 of 256: 6.3 us (a wave for each token: 10.4); 131072: 30 us, 4.4 TB/s.
+constexpr int kRunFloats = 2048;
+
+template <int S>
+__global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteArgs a, const float* __restrict__ d_w,
+                                                                  float* __restrict__ d_logits) {
+  __shared__ __attribute__((aligned(16))) float runs[kWavesPerBlock][kRunFloats];
+  const int lane = lane_id(), wv = uniform(static_cast<int>(threadIdx.x) / kWave);
+  const int token = lane / S, j = lane % S;
+  float* run = runs[wv];
+  const int tokens = min(kWave / S, kRunFloats / a.E);  // E <= 1024
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWavesPerBlock * tokens;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + wv) * tokens; t0 < a.T; t0 += step) {
+    const int here = static_cast<int>(min(a.T - t0, static_cast<int64_t>(tokens)));
+    const int64_t t = t0 + token;
+    int e = -1;
+    float u = 0.f, x = 0.f;
+    if (token < here && j < a.k) {
+      e = a.idx[t * a.k + j];
+      u = a.scale * d_w[t * a.k + j];
+      if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(a.E)) e = -1;
+      if (e >= 0) x = a.logits[t * a.E + e];
+    }
+    for (int i = lane * 4; i < here * a.E; i += kWave * 4) *reinterpret_cast<float4*>(run + i) = make_float4(0, 0, 0, 0);
+    float s = 0.f, top = 0.f;
+    if (a.sigmoid) {
+      s = e >= 0 ? 1.f / (1.f + expf(-x)) : 0.f;
+    } else {
+      top = group_top<S>(e >= 0 ? x : -INFINITY);
+      s = e >= 0 ? expf(x - top) : 0.f;
+    }
+    float grad = u * s / (1.f + expf(x));  // sigmoid, not renormalised
+    if (a.renormalize) {
+      const float by = group_sum<S>(s) + (a.sigmoid ? 1e-20f : 0.f), dot = group_sum<S>(u * s);
+      grad = a.sigmoid ? (u - dot / by) / by * s / (1.f + expf(x)) : s / by * (u - dot / by);
+    }
+    wave_sync();
+    if (e >= 0) run[token * a.E + e] = grad;
+    wave_sync();
+    write_run(run, d_logits + t0 * a.E, here * a.E);
+    wave_sync();
+  }
+}
+
+// More than a wave of chosen experts: one wave per token, in turns.
 __global__ __launch_bounds__(kThreads) void route_any_backward_kernel(const RouteArgs a, const float* __restrict__ d_w,
                                                                       float* __restrict__ d_logits) {
-  __shared__ float rows[kWavesPerBlock][kMaxExperts];
+  __shared__ __attribute__((aligned(16))) float rows[kWavesPerBlock][kMaxExperts];
   const int lane = lane_id(), wv = static_cast<int>(threadIdx.x) / kWave;
   float* row = rows[wv];
-  const bool dense = !a.sigmoid && !a.renormalize;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + wv; t < a.T;
        t += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
     const float* x = a.logits + t * a.E;
     const int32_t* idx = a.idx + t * a.k;
     const float* up = d_w + t * a.k;
     for (int e = lane; e < a.E; e += kWave) row[e] = 0.f;
-    float top = -INFINITY, total = 0.f;
-    if (dense) {
-      for (int e = lane; e < a.E; e += kWave) top = fmaxf(top, x[e]);
-      top = wave_max(top);
-      for (int e = lane; e < a.E; e += kWave) total += expf(x[e] - top);
-      total = wave_sum(total);
-    } else if (!a.sigmoid) {
+    float top = 0.f;
+    if (!a.sigmoid) {
+      top = -INFINITY;
       for (int j = lane; j < a.k; j += kWave)
         if (static_cast<uint32_t>(idx[j]) < static_cast<uint32_t>(a.E)) top = fmaxf(top, x[idx[j]]);
       top = wave_max(top);
@@ -795,28 +852,75 @@ __global__ __launch_bounds__(kThreads) void route_any_backward_kernel(const Rout
       sum += s;
       dot = fmaf(a.scale * up[j], s, dot);
     }
-    sum = wave_sum(sum);
+    const float by = wave_sum(sum) + (a.sigmoid ? 1e-20f : 0.f);
     dot = wave_sum(dot);
-    const float by = dense ? total : a.sigmoid ? sum + 1e-20f : sum;
     wave_sync();
     for (int j = lane; j < a.k; j += kWave) {
       const int e = idx[j];
       if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(a.E)) continue;
       const float v = x[e], u = a.scale * up[j], s = score(v);
-      if (dense) row[e] = u;
-      else if (!a.sigmoid) row[e] = s / by * (u - dot / by);
+      if (!a.sigmoid) row[e] = s / by * (u - dot / by);
       else row[e] = (a.renormalize ? (u - dot / by) / by : u) * s / (1.f + expf(v));
     }
     wave_sync();
-    for (int e = lane; e < a.E; e += kWave)
-      d_logits[t * a.E + e] = dense ? score(x[e]) / by * (row[e] - dot / by) : row[e];
+    write_run(row, d_logits + t * a.E, a.E);
     wave_sync();
   }
 }
 
-// a launch holds fewer than 2^32 threads; tokens past these take turns
-unsigned wave_blocks(int64_t T) {
-  return static_cast<unsigned>(min((T + kWavesPerBlock - 1) / kWavesPerBlock, int64_t{1} << 20));
+// The plain softmax: G lanes hold a token's row, VPL experts each.
+template <int G, int VPL>
+__global__ __launch_bounds__(kThreads) void route_softmax_backward_kernel(const RouteArgs a,
+                                                                          const float* __restrict__ d_w,
+                                                                          float* __restrict__ d_logits, int per) {
+  using In = Rows<G, VPL>;
+  __shared__ __attribute__((aligned(16))) float runs[kWavesPerBlock][kWave * VPL];
+  const int wv = uniform(static_cast<int>(threadIdx.x) / kWave);
+  float* run = runs[wv];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWavesPerBlock * In::kTokens;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + wv) * In::kTokens; t0 < a.T; t0 += step) {
+    const In in(a, G, per, t0);
+    float v[VPL];
+    in.logits(v);
+    float top = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) top = i < in.own ? fmaxf(top, v[i]) : top;
+    top = group_top<G>(top);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      v[i] = expf(v[i] - top);
+      total += i < in.own ? v[i] : 0.f;
+    }
+    total = group_sum<G>(total);
+    const float inv = 1.f / total;
+    float dot = 0.f;
+    auto chosen = [&](int j) {  // -1: none of this token's
+      const int e = in.live && j < a.k ? a.idx[in.t * a.k + j] : -1;
+      return static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E) ? e : -1;
+    };
+    for (int j = in.g; j < a.k; j += G) {
+      const int e = chosen(j);
+      if (e >= 0) dot = fmaf(a.scale * d_w[in.t * a.k + j], expf(in.logit(e) - top) * inv, dot);
+    }
+    dot = group_sum<G>(dot);
+    float* row = run + in.row / 4;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (i < in.own) row[in.e0 + i] = -(v[i] * inv) * dot;
+    wave_sync();
+    for (int j = in.g; j < a.k; j += G) {
+      const int e = chosen(j);
+      if (e >= 0) row[e] = expf(in.logit(e) - top) * inv * (a.scale * d_w[in.t * a.k + j] - dot);
+    }
+    wave_sync();
+    write_run(run, d_logits + t0 * a.E, static_cast<int>(min(a.T - t0, static_cast<int64_t>(In::kTokens))) * a.E);
+    wave_sync();
+  }
+}
+
+// a launch holds fewer than 2^32 threads; waves' tokens past these take turns
+unsigned wave_blocks(int64_t waves) {
+  return static_cast<unsigned>(min((waves + kWavesPerBlock - 1) / kWavesPerBlock, int64_t{1} << 20));
 }
 
 }  // namespace
@@ -862,7 +966,38 @@ hipError_t launch_route_experts_backward(const moe_router& r, const float* logit
                                          const float* d_w, float* d_logits, int64_t T, int E, int k,
                                          hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  const RouteArgs a = make_args(r, logits, const_cast<int32_t*>(idx), nullptr, T, E, k);
+  moe_router whole = r;  // the choice is made: no groups
+  whole.groups = whole.top_groups = whole.group_top = 1;
+  const RouteArgs a = make_args(whole, logits, const_cast<int32_t*>(idx), nullptr, T, E, k);
+  if (!a.sigmoid && !a.renormalize) {
+#define MOE_ROUTE(G, VPL)                                                                                         \
+  do {                                                                                                            \
+    const int64_t waves = (T * G + kWave - 1) / kWave;                                                            \
+    hipLaunchKernelGGL((route_softmax_backward_kernel<G, VPL>), dim3(wave_blocks(waves)), dim3(kThreads), 0,      \
+                       stream, a, d_w, d_logits, (E + G - 1) / G);                                                \
+    return hipGetLastError();                                                                                     \
+  } while (0)
+    if (E <= 8) MOE_ROUTE(1, 8);
+    if (E <= 16) MOE_ROUTE(2, 8);
+    if (E <= 32) MOE_ROUTE(4, 8);
+    if (E <= 64) MOE_ROUTE(8, 8);
+    if (E <= 128) MOE_ROUTE(16, 8);
+    if (E <= 256) MOE_ROUTE(32, 8);
+    if (E <= 512) MOE_ROUTE(64, 8);
+    MOE_ROUTE(64, 16);
+#undef MOE_ROUTE
+  }
+#define MOE_ROUTE(S)                                                                                                  \
+  do {                                                                                                                \
+    const int64_t tokens = min(kWave / S, kRunFloats / E), waves = (T + tokens - 1) / tokens;                         \
+    hipLaunchKernelGGL(route_backward_kernel<S>, dim3(wave_blocks(waves)), dim3(kThreads), 0, stream, a, d_w, d_logits); \
+    return hipGetLastError();                                                                                         \
+  } while (0)
+  if (k <= 4) MOE_ROUTE(4);
+  if (k <= 8) MOE_ROUTE(8);
+  if (k <= 16) MOE_ROUTE(16);
+  if (k <= 64) MOE_ROUTE(64);
+#undef MOE_ROUTE
   hipLaunchKernelGGL(route_any_backward_kernel, dim3(wave_blocks(T)), dim3(kThreads), 0, stream, a, d_w, d_logits);
   return hipGetLastError();
 }
