@@ -175,6 +175,12 @@ def main() -> int:
                          "step's grouped GEMM is moe_grouped_gemm_int8, the quantisation of its rows included")
     ap.add_argument("--clip-norm", type=float, default=0.0,
                     help="with --train: a step ends with clip_grad_norm of the weight gradients to this norm")
+    ap.add_argument("--adamw", type=int, choices=[32, 8], default=0,
+                    help="with --train: a step ends with an AdamW step of the expert weights (fp32 masters, states in "
+                         "that many bits); with --clip-norm the clip is then part of it")
+    ap.add_argument("--router", choices=["topk", "sigmoid"], default="topk",
+                    help="topk: route_topk; sigmoid: route_experts with sigmoid scores, a balance bias and renormalised "
+                         "weights (and its gradient with --train)")
     ap.add_argument("--graph", action="store_true",
                     help="record one step in a HIP graph and time graph replays (the GEMM roofline "
                          "then comes from an eager pass after the timed replays)")
@@ -266,9 +272,13 @@ def main() -> int:
         experts = moe.quantize_experts(dgu, ddn)
         ws8 = torch.empty(moe.grouped_gemm_int8_workspace_bytes(w.T, w.d, w.d_ff, w.E, w.k, w.e_begin, w.e_end),
                           dtype=torch.uint8, device=dev)
-    if args.clip_norm > 0 and not args.train:
-        print("--clip-norm needs --train", file=sys.stderr)
+    if (args.clip_norm > 0 or args.adamw) and not args.train:
+        print("--clip-norm and --adamw need --train", file=sys.stderr)
         return 2
+    router = None
+    if args.router == "sigmoid":
+        bias = 0.05 * np.random.default_rng(w.seed + 700).standard_normal(w.E).astype(np.float32)
+        router = moe.Router("sigmoid", to_dev(bias, "f32"))
 
     def gemm():
         if args.int8:
@@ -305,7 +315,8 @@ def main() -> int:
 
     # the calls of one step, in order: (name, call)
     calls = [
-        ("route_topk", lambda: moe.route_topk(dl, w.k, idx, wts, stream=cur())),
+        ("route_topk", lambda: moe.route_topk(dl, w.k, idx, wts, stream=cur())) if router is None else
+        ("route_experts", lambda: moe.route_experts(dl, w.k, router, idx, wts, stream=cur())),
         ("dispatch", lambda: moe.dispatch(dx, idx, w.E, w.e_begin, w.e_end, out=disp, stream=cur(),
                                           gather=not fused)),
         ("grouped_gemm", gemm),
@@ -320,13 +331,31 @@ def main() -> int:
             ("dispatch_backward", lambda: moe.dispatch_backward(d_xp, disp.pair_pos, w.T, w.k, w.E, w.e_begin,
                                                                 w.e_end, d_x=d_x, stream=cur())),
             ("route_topk_backward", lambda: moe.route_topk_backward(idx, wts, d_w, w.E, d_logits=d_logits,
-                                                                    stream=cur())),
+                                                                    stream=cur())) if router is None else
+            ("route_experts_backward", lambda: moe.route_experts_backward(dl, idx, d_w, router, d_logits=d_logits,
+                                                                          stream=cur())),
         ]
         if args.clip_norm > 0:
             norm = torch.empty(1, dtype=torch.float32, device=dev)
             ws_norm = torch.empty(moe.grad_norm_workspace_bytes(2), dtype=torch.uint8, device=dev)
-            calls.append(("clip_grad_norm", lambda: moe.clip_grad_norm([d_wgu, d_wdn], args.clip_norm, norm=norm,
-                                                                       workspace=ws_norm, stream=cur())))
+            if args.adamw:
+                calls.append(("grad_norm", lambda: moe.grad_norm([d_wgu, d_wdn], norm=norm, workspace=ws_norm,
+                                                                 stream=cur())))
+            else:
+                calls.append(("clip_grad_norm", lambda: moe.clip_grad_norm([d_wgu, d_wdn], args.clip_norm, norm=norm,
+                                                                           workspace=ws_norm, stream=cur())))
+        if args.adamw:
+            params = [dgu, ddn]
+            masters = [p.float() for p in params]
+            state_m, state_v = moe.adamw_states(params, args.adamw)
+            at = torch.zeros(1, dtype=torch.int64, device=dev)
+
+            def adamw():
+                at.add_(1)
+                clip = dict(norm=norm, max_norm=args.clip_norm) if args.clip_norm > 0 else {}
+                moe.adamw(params, [d_wgu, d_wdn], state_m, state_v, at, 1e-5, masters=masters, stream=cur(), **clip)
+
+            calls.append(("adamw", adamw))
     timed = "grouped_gemm_backward" if train else "grouped_gemm"  # the roofline's kernel
 
     def step(i=None):
@@ -453,7 +482,9 @@ def main() -> int:
                    "local_experts": [w.e_begin, w.e_end], "N_loc": n_loc, "active_local_experts": active,
                    "parallelism": "one rank's share on 1 GPU", "path": "fused" if fused else "staged",
                    "launch": "hip graph" if args.graph else "eager",
-                   "step": ("forward + backward" + (" + clip" if args.clip_norm > 0 else "")) if args.train
+                   **({"router": args.router} if router is not None else {}),
+                   "step": ("forward + backward" + (" + clip" if args.clip_norm > 0 else "") +
+                            (f" + adamw, {args.adamw}-bit states" if args.adamw else "")) if args.train
                            else "forward, int8 experts" if args.int8 else "forward"},
         "local_pairs_per_s": round(n_loc / (ms_step * 1e-3), 1),
         "timing": {"per_step": f"median of {args.steps} per-step event times, each step after a "

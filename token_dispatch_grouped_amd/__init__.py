@@ -1157,10 +1157,10 @@ def _rms_norm(x, weight, eps, residual, y, s, rstd, keep_y, rows, stream):
         if residual is not None and s is None:
             s = torch.empty_like(x)
         if rstd is None:
-            rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+            rstd = x.new_empty(T, dtype=torch.float32)
         if rows is not None and codes is None:
-            rows.codes = codes = torch.empty((_kblocks(d), T, 64), dtype=torch.int8, device=x.device)
-            rows.scale = scale = torch.empty(T, dtype=torch.float32, device=x.device)
+            rows.codes = codes = x.new_empty((_kblocks(d), T, 64), dtype=torch.int8)
+            rows.scale = scale = x.new_empty(T, dtype=torch.float32)
         ctx.give(y, s, rstd, codes, scale)
         _check(_load().moe_rms_norm(ctypes.byref(sh), _CODES[x.dtype], x.data_ptr(), _addr(residual),
                                     _CODES[weight.dtype], weight.data_ptr(), eps, _addr(y),
@@ -1545,7 +1545,7 @@ def _same_list(ts, name: str, params, sizes, dtypes):
     return ts
 
 
-def _state_list(ts, name: str, params, sizes):
+def _state_list(ts, name: str, params, sizes, numels):
     """(tensors, scales or None) of a list of states."""
     torch = _torch()
     ts = list(ts)
@@ -1556,10 +1556,14 @@ def _state_list(ts, name: str, params, sizes):
         raise TypeError(f"{name} must hold fp32 tensors or Float8State, not both")
     codes = _same_list([t.codes for t in ts], name, params, sizes, {torch.float8_e4m3fn})
     scales = [t.scale for t in ts]
-    for i, (t, p) in enumerate(zip(scales, params)):
-        n = -(-p.numel() // MOE_STATE_BLOCK)
-        if t is None or t.dtype is not torch.float32 or t.shape != (n,):
-            _want(t, f"{name}[{i}].scale", torch.float32, (n,))
+    blocks = [(-(-n // MOE_STATE_BLOCK),) for n in numels]
+    try:
+        if {torch.float32}.issuperset(map(_dtype_of, scales)) and list(map(torch.Tensor.size, scales)) == blocks:
+            return codes, scales
+    except (AttributeError, TypeError):  # something else than tensors
+        pass
+    for i, (t, n) in enumerate(zip(scales, blocks)):
+        _want(t, f"{name}[{i}].scale", torch.float32, n)
     return codes, scales
 
 
@@ -1576,8 +1580,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps:
     params, numels, kinds = _tensor_list(params, "params")
     sizes = list(map(torch.Tensor.size, params))
     grads = _same_list(grads, "grads", params, sizes, set(_CODES))
-    m, m_scale = _state_list(exp_avg, "exp_avg", params, sizes)
-    v, v_scale = _state_list(exp_avg_sq, "exp_avg_sq", params, sizes)
+    m, m_scale = _state_list(exp_avg, "exp_avg", params, sizes, numels)
+    v, v_scale = _state_list(exp_avg_sq, "exp_avg_sq", params, sizes, numels)
     if (m_scale is None) != (v_scale is None):
         raise TypeError("exp_avg and exp_avg_sq must both be fp32 or both Float8State")
     n = len(params)
