@@ -436,8 +436,8 @@ moe_status moe_layer_norm_backward(const moe_shape* s, moe_dtype dt, const void*
  *   q        [ceil(d / 64)][T][64] int8 with q_scale [T] fp32 (4-byte aligned), written, or
  *            both NULL: the rows in 8 bits, as the experts below take them: codes and scale
  *            of the fp32 y, before its rounding to dt (MOE_EUNSUPPORTED unless dt = MOE_BF16).
- * A row with a NaN gets NaN; an infinity gives rstd 0 and so NaN for itself, 0 for the
- * others, and a scale of NaN. Uses s->T and s->d only. Errors as moe_layer_norm. */
+ * A row with a NaN gets NaN, a row of zeros with eps 0 as well; an infinity gives rstd 0 and
+ * so NaN for itself, 0 for the others, and a scale of NaN. Uses s->T and s->d only. Errors as moe_layer_norm. */
 moe_status moe_rms_norm(const moe_shape* s, moe_dtype dt, const void* x, const void* residual,
                         moe_dtype wdt, const void* weight, float eps, void* y, void* sum, float* rstd,
                         void* q, float* q_scale, hipStream_t stream);

@@ -299,6 +299,73 @@ def test_streams_and_graph():
         assert torch.equal(f[0], want[0]) and torch.equal(f[1], want[1]) and torch.equal(g, gw), i
 
 
+def _in_few(lx, k, router, rows=1000):
+    """The same tokens in calls of a few, which compare every score in fp64."""
+    parts = [moe.route_experts(lx[at:at + rows], k, router) for at in range(0, lx.shape[0], rows)]
+    return tuple(torch.cat(p) for p in zip(*parts))
+
+
+BIASES = {"small": lambda r, E: 0.05 * r.standard_normal(E), "zero": lambda r, E: np.zeros(E),
+          "far apart": lambda r, E: r.choice([-1000.0, 1000.0, 3.0], E) + 0.01 * r.standard_normal(E),
+          "large": lambda r, E: 1e6 + r.integers(0, 4, E)}
+
+
+@pytest.mark.parametrize("bias", sorted(BIASES))
+@pytest.mark.parametrize("E,groups,top_groups,k", [(128, 1, 1, 4), (100, 1, 1, 8), (200, 8, 3, 6), (256, 8, 4, 8), (256, 8, 4, 16), (256, 16, 5, 3),
+                                                   (264, 1, 1, 8), (384, 3, 2, 12), (512, 8, 4, 8), (512, 32, 8, 16), (1000, 4, 2, 8),
+                                                   (1024, 1, 1, 2)])
+def test_many_tokens_choose_as_few_do(E, groups, top_groups, k, bias):
+    """Sizes at which candidates are found on fp32 values: ids as in calls of a few tokens bit for
+    bit, weights to a rounding, and 60 rows against the plain form."""
+    T = 16391 if E <= 256 else 8209
+    rng = np.random.default_rng(E + groups + k)
+    x, _ = _inputs(T, E, seed=E + k)
+    x[::3] = torch.from_numpy(x[::3]).bfloat16().float().numpy()  # ties
+    x[5] = 0.25  # all equal
+    x[6, : E // 2] = x[6, E // 2: 2 * (E // 2)]
+    x[7] = -30.0 - np.arange(E) % 7  # sigmoids near 0
+    x[8] = 30.0 + np.arange(E) % 5  # that round to 1
+    x[9, ::2] = -np.inf
+    x[10, 3], x[11, E - 1], x[12, 1] = np.nan, np.inf, -np.nan
+    b = BIASES[bias](rng, E).astype(np.float32)
+    print(f"case E={E} groups={groups} of which {top_groups} k={k} bias {bias}", flush=True)
+    lx = _gpu(x)
+    at = np.r_[0:20, T - 20:T, rng.integers(0, T, 20)]
+    for group_score in ("top2", "max"):
+        router = moe.Router("sigmoid", _gpu(b), groups, top_groups, group_score, True, 1.5)
+        idx, w = moe.route_experts(lx, k, router)
+        few, fw = _in_few(lx, k, router)
+        torch.cuda.synchronize()
+        assert torch.equal(idx, few)
+        ok = torch.isfinite(fw)
+        assert torch.equal(torch.isfinite(w), ok) and ((w - fw).abs()[ok] <= 4 * U * fw.abs()[ok]).all()
+        with np.errstate(invalid="ignore"):
+            want, _ = st.route_experts(x[at], k, "sigmoid", b, groups, top_groups, 2 if group_score == "top2" else 1, True, 1.5)
+        np.testing.assert_array_equal(idx.cpu().numpy()[at], want)
+
+
+@pytest.mark.parametrize("score,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", False)])
+@pytest.mark.parametrize("E,k", [(128, 4), (250, 8), (256, 16), (512, 8), (1024, 8)])
+def test_many_tokens_by_their_logits(E, k, score, renormalize):
+    T = 16391 if E <= 256 else 8209
+    x, bias = _inputs(T, E, seed=E, held="bf16")
+    x[3] = 1.0
+    lx = _gpu(x)
+    for b in (None, bias):
+        router = moe.Router(score, None if b is None else _gpu(b), renormalize=renormalize)
+        idx, w = moe.route_experts(lx, k, router)
+        few, fw = _in_few(lx, k, router)
+        torch.cuda.synchronize()
+        assert torch.equal(idx, few) and ((w - fw).abs() <= 16 * U * fw.abs()).all()
+        want, _ = st.route_experts(x[:30], k, score, b, 1, 1, 1, renormalize)
+        np.testing.assert_array_equal(idx.cpu().numpy()[:30], want)
+        d_w = torch.randn(T, k, device=dev, generator=torch.Generator(device=dev).manual_seed(1))
+        g = moe.route_experts_backward(lx, idx, d_w, router)
+        gf = torch.cat([moe.route_experts_backward(lx[a:a + 1000], idx[a:a + 1000], d_w[a:a + 1000], router) for a in range(0, T, 1000)])
+        torch.cuda.synchronize()
+        assert torch.equal(g, gf)
+
+
 def test_many_tokens_past_32_bit_offsets():
     """Rows whose elements lie past 2^31 and 2^32 bytes; one expert a token and a whole row."""
     T, E = (1 << 23) + 5, 264

@@ -555,7 +555,7 @@ __device__ __forceinline__ float from_signed(int o) {
 // How far the fp32 form of a sigmoid's choice value can be from the exact one, doubled. In units of
 // 2^-24: the exponential's argument |x| s (1 - s) <= 0.23, its value 2 s (1 - s) <= 0.5, the sum with
 // one 1, the inverse 2: 4; the sum with the bias, and the exact value's rounding to fp32, |c| each.
-__device__ __forceinline__ float margin(float c) { return 0x1p-21f + fabsf(c) * 0x1p-22f; }
+__device__ __forceinline__ float margin(float c) { return 0x1.2p-21f + fabsf(c) * 0x1.2p-22f; }  // and an eighth more
 
 // Sigmoid scores on fp32 values alone, 32 bits a comparison: the k-th largest of a token's values is
 // found (not whose it is), every expert from it on (less the values' error) becomes a candidate
@@ -607,14 +607,18 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
   if (a.top_groups < a.groups) {
     int one = best[0], two = best[1];
     merge_two<G>(one, two, P);
-    float mine = a.group_top == 2 && size > 1 ? from_signed(one) + from_signed(two) : from_signed(one);
-    if (in.group >= a.groups) mine = -INFINITY;
-    const float slack = 2.f * margin(mine);  // of a sum of two
+    // the group's value lies between low and high: its values' errors, and the roundings of both sums
+    const bool pair = a.group_top == 2 && size > 1;
+    const float c1 = from_signed(one), c2 = from_signed(two), value = pair ? c1 + c2 : c1;
+    const float off = 0.5f * (margin(c1) + (pair ? margin(c2) : 0.f)) + fabsf(value) * 0x1p-22f;
+    const bool real = in.group < a.groups;
+    const float low = real ? value - off : -INFINITY, high = real ? value + off : -INFINITY;
     int above = 0, beside = 0;  // lanes of groups before this one for sure, and perhaps
-    other_lanes<G>(static_cast<int>(__float_as_uint(mine)), g, __ffs(P) - 1, [&](int value, int of) {
-      const float other = __uint_as_float(static_cast<uint32_t>(value));
-      above += other > mine + slack;
-      beside += of != in.group && !(other < mine - slack);
+    other_lanes<G>(static_cast<int>(__float_as_uint(low)), g, __ffs(P) - 1, [&](int bits, int of) {
+      above += of != in.group && __uint_as_float(static_cast<uint32_t>(bits)) > high;
+    });
+    other_lanes<G>(static_cast<int>(__float_as_uint(high)), g, __ffs(P) - 1, [&](int bits, int of) {
+      beside += of != in.group && !(__uint_as_float(static_cast<uint32_t>(bits)) < low);
     });
     const bool close = in.group < a.groups && above < a.top_groups * P && beside >= a.top_groups * P;
     if (__any(in.live && close)) {
@@ -719,8 +723,11 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
 
 // Waves per SIMD (registers: 128 or 170) where tokens are many: 131072 x 256 sigmoids in 8 groups 72 us
 // with two, 58 with three, 55 with four; softmax scores 125, 106, 114; logits with their sum three 43, four 50.
+template <int G, Route MODE>
+constexpr int route_waves() { return MODE == Route::kSoftmax || MODE == Route::kLogitsTotal || G == 32 ? 3 : 4; }
+
 template <int G, int VPL, int L, Route MODE, bool QUICK>
-__global__ __launch_bounds__(kThreads, MODE == Route::kSoftmax || MODE == Route::kLogitsTotal ? 3 : 4) void route_kernel(const RouteArgs a, int P, int per) {
+__global__ __launch_bounds__(kThreads, (route_waves<G, MODE>())) void route_kernel(const RouteArgs a, int P, int per) {
   using In = Rows<G, VPL>;
   const int wv = uniform(static_cast<int>(threadIdx.x) / kWave);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWavesPerBlock * In::kTokens;
