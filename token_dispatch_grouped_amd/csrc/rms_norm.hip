@@ -317,6 +317,8 @@ constexpr int64_t kForwardBlocks = int64_t{1} << 21;  // a launch holds fewer th
   else if (row_vec <= 2048) F(512, 4); \
   else F(1024, 4)
 
+// few: a workgroup has a few rows, so that a row's own time counts (512 x 2 and 256 x 3 of 5120 bf16: 777 rows
+// 12.5 and 14.0 us, 4096 rows 32.7 and 32.0, 16384 rows 123 and 116)
 #define MOE_RMS_BWD_SHAPES(F)           \
   if (row_vec <= 16) F(16, 1);          \
   else if (row_vec <= 32) F(32, 1);     \
@@ -325,6 +327,7 @@ constexpr int64_t kForwardBlocks = int64_t{1} << 21;  // a launch holds fewer th
   else if (row_vec <= 192) F(64, 3);    \
   else if (row_vec <= 256) F(256, 1);   \
   else if (row_vec <= 512) F(512, 1);   \
+  else if (row_vec <= 768 && few) F(512, 2); \
   else if (row_vec <= 768) F(256, 3);   \
   else if (row_vec <= 1024) F(512, 2);  \
   else if (row_vec <= 1536) F(512, 3);  \
@@ -406,6 +409,7 @@ unsigned launch_backward_shape(const Backward& b, hipStream_t stream) {
 template <bool BF16, bool WBF16>
 unsigned launch_backward(const Backward& b, hipStream_t stream) {
   const int row_vec = b.row_vec;
+  const bool few = b.T <= 2048;
 #define MOE_RMS(G, VPT) return launch_backward_shape<BF16, WBF16, G, VPT>(b, stream)
   if constexpr (!BF16) {
     if (row_vec > 4096) MOE_RMS(1024, 8);
