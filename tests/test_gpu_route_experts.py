@@ -310,11 +310,12 @@ BIASES = {"small": lambda r, E: 0.05 * r.standard_normal(E), "zero": lambda r, E
           "large": lambda r, E: 1e6 + r.integers(0, 4, E)}
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("bias", sorted(BIASES))
 @pytest.mark.parametrize("E,groups,top_groups,k", [(128, 1, 1, 4), (100, 1, 1, 8), (200, 8, 3, 6), (256, 8, 4, 8), (256, 8, 4, 16), (256, 16, 5, 3),
                                                    (264, 1, 1, 8), (384, 3, 2, 12), (512, 8, 4, 8), (512, 32, 8, 16), (1000, 4, 2, 8),
                                                    (1024, 1, 1, 2)])
-def test_many_tokens_choose_as_few_do(E, groups, top_groups, k, bias):
+def test_many_tokens_choose_as_few_do(E, groups, top_groups, k, bias, score):
     """Sizes at which candidates are found on fp32 values: ids as in calls of a few tokens bit for
     bit, weights to a rounding, and 60 rows against the plain form."""
     T = 16391 if E <= 256 else 8209
@@ -328,11 +329,11 @@ def test_many_tokens_choose_as_few_do(E, groups, top_groups, k, bias):
     x[9, ::2] = -np.inf
     x[10, 3], x[11, E - 1], x[12, 1] = np.nan, np.inf, -np.nan
     b = BIASES[bias](rng, E).astype(np.float32)
-    print(f"case E={E} groups={groups} of which {top_groups} k={k} bias {bias}", flush=True)
+    print(f"case E={E} groups={groups} of which {top_groups} k={k} bias {bias} {score}", flush=True)
     lx = _gpu(x)
     at = np.r_[0:20, T - 20:T, rng.integers(0, T, 20)]
     for group_score in ("top2", "max"):
-        router = moe.Router("sigmoid", _gpu(b), groups, top_groups, group_score, True, 1.5)
+        router = moe.Router(score, _gpu(b), groups, top_groups, group_score, True, 1.5)
         idx, w = moe.route_experts(lx, k, router)
         few, fw = _in_few(lx, k, router)
         torch.cuda.synchronize()
@@ -340,7 +341,7 @@ def test_many_tokens_choose_as_few_do(E, groups, top_groups, k, bias):
         ok = torch.isfinite(fw)
         assert torch.equal(torch.isfinite(w), ok) and ((w - fw).abs()[ok] <= 4 * U * fw.abs()[ok]).all()
         with np.errstate(invalid="ignore"):
-            want, _ = st.route_experts(x[at], k, "sigmoid", b, groups, top_groups, 2 if group_score == "top2" else 1, True, 1.5)
+            want, _ = st.route_experts(x[at], k, score, b, groups, top_groups, 2 if group_score == "top2" else 1, True, 1.5)
         np.testing.assert_array_equal(idx.cpu().numpy()[at], want)
 
 

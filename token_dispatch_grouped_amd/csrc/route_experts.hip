@@ -41,7 +41,7 @@ __device__ __forceinline__ float from_orderable(uint32_t o) {
 // e^x in fp64, to about 2^-52: x = n ln 2 + r with |r| <= ln 2 / 2, and e^r by its power series
 // (the term r^13 / 13! is below 2^-52). x is held to +-700, so that 1 + e^x and its inverse are
 // finite; a NaN stays one. A few instructions fewer than the library's, made for any argument, and its
-// division (131072 x 256 softmax scores: 105 us against 111).
+// division (131072 x 256 softmax scores, all in fp64: 105 us against 111).
 __device__ __forceinline__ double exp64(double x) {
   const double y = fmin(fmax(x, -700.0), 700.0);
   const double n = rint(y * 1.4426950408889634);
@@ -414,6 +414,19 @@ struct Rows {
       for (int i = 0; i < VPL; ++i) to[i] = one(from, at + i * 4u);
     }
   }
+  // The sum of e^(logit - top) over the token's experts, in fp64, for a wave that does not hold them any more.
+  __device__ double exponentials(float top) const {
+    double sum = 0.0;
+#pragma unroll 2
+    for (int i = 0; i < VPL; i += 4) {
+      float z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = one(buffer, row + (e0 + i + j) * 4u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum += i + j < own ? exp64(static_cast<double>(z[j]) - top) : 0.0;
+    }
+    return group_sum<G>(sum);
+  }
   __device__ static float one(__amdgpu_buffer_rsrc_t from, uint32_t at) {
     return __uint_as_float(
         static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b32(from, static_cast<int>(at), 0, 0)));
@@ -431,6 +444,7 @@ template <int G, int L>
 struct Candidates {
   static constexpr int kMost = G < 2 * L ? 2 * L : G;  // of a token
   double key[kWave / G][kMost];
+  float logit[kWave / G][kMost], bias[kWave / G][kMost];  // softmax scores only
   uint16_t id[kWave / G][kMost];
 };
 
@@ -555,35 +569,60 @@ __device__ __forceinline__ float from_signed(int o) {
   return __uint_as_float(static_cast<uint32_t>(o ^ static_cast<int>(static_cast<uint32_t>(o >> 31) >> 1)));
 }
 
-// How far the fp32 form of a sigmoid's choice value can be from the exact one, doubled. In units of
-// 2^-24: the exponential's argument |x| s (1 - s) <= 0.23, its value 2 s (1 - s) <= 0.5, the sum with
-// one 1, the inverse 2: 4; the sum with the bias, and the exact value's rounding to fp32, |c| each.
-__device__ __forceinline__ float margin(float c) { return 0x1.2p-21f + fabsf(c) * 0x1.2p-22f; }  // and an eighth more
-
-// Sigmoid scores on fp32 values alone, 32 bits a comparison: the k-th largest of a token's values is
-// found (not whose it is), every expert from it on (less the values' error) becomes a candidate
-// in LDS, and the candidates, hardly ever more than k, are ranked by their exact choice values.
-// Groups that are too close to each other for fp32 are ranked by the exact values of their lanes' best
-// two. False where that does not decide: a NaN, or more candidates than there is room for (many
-// equal values).
-template <int G, int VPL, int L>
+// Scores on fp32 values alone, 32 bits a comparison: the k-th largest of a token's values is found (not
+// whose it is), every expert from it on (less the values' error) becomes a candidate in LDS, and
+// the candidates, hardly ever more than k, are ranked by their exact choice values. Softmax scores are
+// ranked by the fp32 values where no two are close, as their exact ones take the fp64 sum
+// over all experts. Groups that are too close to each other for fp32 are ranked by the exact values of
+// their lanes' best two. False where that does not decide: a NaN, or more candidates than there
+// is room for (many equal values).
+template <int G, int VPL, int L, Route MODE>
 __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VPL>& in, int P,
                                             Candidates<G, L>& room) {
   static_assert(G >= 8 && G <= 32, "a lane has room for all of a token's candidates otherwise");
   constexpr int kSlots = Candidates<G, L>::kMost / G;
   constexpr int kRun = VPL < L ? VPL : L;
   constexpr float kLog2e = 1.44269504f;
+  constexpr bool kSoftmax = MODE == Route::kSoftmax;
   const int lane = lane_id(), g = in.g, token = lane / G, size = a.E / a.groups;
   int own = in.own;
-  float v[VPL], bias[VPL];
+  float v[VPL], bias[VPL], top = 0.f, inv = 0.f;
+  double inv64 = 0.0;  // softmax: of the exact sum, once a wave has needed it
   in.logits(v);
   in.load(in.bias_buffer(a), in.e0 * 4u, bias);
+  if constexpr (kSoftmax) {
+    top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    v[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v[i] * -kLog2e)) + bias[i];
+    for (int i = 0; i < VPL; ++i) top = i < own && v[i] > top ? v[i] : top;
+    top = group_top<G>(top);
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // short chains of additions: a tighter margin
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      v[i] = __builtin_amdgcn_exp2f((v[i] - top) * kLog2e);
+      sum[i % 8] += i < own ? v[i] : 0.f;
+    }
+    inv = __builtin_amdgcn_rcpf(
+        group_sum<G>(((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]))));
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    if constexpr (kSoftmax) v[i] = v[i] * inv + bias[i];
+    else v[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v[i] * -kLog2e)) + bias[i];
+  }
+  // How far a value can be from the exact one, doubled, with an eighth more. In units of 2^-24:
+  //   sigmoid  the exponential's argument |x| s (1 - s) <= 0.23 x 1.3, its value 2 s (1 - s) <= 0.5, the sum with one 1,
+  //            the inverse 2: 4
+  //   softmax  with z = max - x: the difference and the argument 2.3 z, the exponential 2; the sum has these (its
+  //            terms' mean z is below 4.5 for 1024 experts) and 12 additions, the inverse and the product 3: 2.3 z
+  //            + 30 of p = inv e^-z, at most 30 of inv
+  // and the sum with the bias, and the exact value's rounding to fp32, |c| each.
+  const float base = kSoftmax ? inv * 0x1.2p-18f : 0x1.2p-21f;
+  auto margin = [&](float c) { return base + fabsf(c) * 0x1.2p-22f; };
   // the exact choice value of one expert
   auto exact = [&](int e) {
-    return static_cast<float>(sigmoid64(in.logit(e)) + static_cast<double>(in.one(in.bias_buffer(a), e * 4u)));
+    const float x = in.logit(e);
+    const double s = kSoftmax ? exp64(static_cast<double>(x) - top) * inv64 : sigmoid64(x);
+    return static_cast<float>(s + static_cast<double>(in.one(in.bias_buffer(a), e * 4u)));
   };
   int o[VPL], best[L];
 #pragma unroll
@@ -625,6 +664,7 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
     });
     const bool close = in.group < a.groups && above < a.top_groups * P && beside >= a.top_groups * P;
     if (__any(in.live && close)) {
+      if constexpr (kSoftmax) inv64 = inverse64(in.exponentials(top));
       const float second = best[1] != INT_MIN ? from_signed(best[1]) : -INFINITY;
       const int from = signed_order(second - margin(second));
       uint32_t near = 0, first_ord = 0, second_ord = 0;
@@ -682,38 +722,84 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
   }
   wave_sync();
   int id[kSlots], rank[kSlots];
-  double s[kSlots], key[kSlots];
+  double s[kSlots], key[kSlots];  // s: the score, or its logit's exponential
+  auto rank_all = [&]() {
+    auto against = [&](int first) {
+#pragma unroll
+      for (int j = first; j < first + G; ++j) {
+        const double other = room.key[token][j];
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) rank[q] += other > key[q];
+      }
+    };
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) rank[q] = 0;
+    against(0);
+#pragma unroll
+    for (int q = 1; q < kSlots; ++q)
+      if (__any(in.live && count > q * G)) against(q * G);
+  };
+  auto keep = [&](int q, float c) {
+    const int j = q * G + g;
+    key[q] = j < count ? key_of(orderable(c), id[q]) : 1.0;
+    room.key[token][j] = key[q];
+  };
+  float c[kSlots], x[kSlots], add[kSlots];
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
     const int j = q * G + g;
     id[q] = j < count ? room.id[token][j] : 0;
-    s[q] = sigmoid64(in.logit(id[q]));
-    const float c = static_cast<float>(s[q] + static_cast<double>(in.one(in.bias_buffer(a), id[q] * 4u)));
-    key[q] = j < count ? key_of(orderable(c), id[q]) : 1.0;
-    room.key[token][j] = key[q];
-    rank[q] = 0;
+    x[q] = in.logit(id[q]);
+    add[q] = in.one(in.bias_buffer(a), id[q] * 4u);
+    if constexpr (kSoftmax) {
+      s[q] = exp64(static_cast<double>(x[q]) - top);
+      c[q] = __builtin_amdgcn_exp2f((x[q] - top) * kLog2e) * inv + add[q];
+      room.logit[token][j] = x[q];
+      room.bias[token][j] = add[q];
+    } else {
+      s[q] = sigmoid64(x[q]);
+      c[q] = static_cast<float>(s[q] + static_cast<double>(add[q]));
+    }
+    keep(q, c[q]);
   }
   wave_sync();
-  auto rank_against = [&](int first) {
+  if constexpr (kSoftmax) {
+    bool close = false;  // to another candidate that is not the very same
 #pragma unroll
-    for (int j = first; j < first + G; ++j) {
-      const double other = room.key[token][j];
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q) rank[q] += other > key[q];
+    for (int q = 0; q < kSlots; ++q) {
+      if (q > 0 && !__any(in.live && count > q * G)) break;
+      for (int j = 0; j < count; ++j) {
+        const float other = from_orderable(key_ord(room.key[token][j]));
+        const bool same = room.logit[token][j] == x[q] && room.bias[token][j] == add[q];
+        close = close || (q * G + g < count && !same && !(fabsf(other - c[q]) > margin(c[q])));
+      }
     }
-  };
-  rank_against(0);
+    wave_sync();
+    if (__any(in.live && close)) {
+      if (inv64 == 0.0) inv64 = inverse64(in.exponentials(top));
 #pragma unroll
-  for (int q = 1; q < kSlots; ++q)
-    if (__any(in.live && count > q * G)) rank_against(q * G);
+      for (int q = 0; q < kSlots; ++q) keep(q, static_cast<float>(s[q] * inv64 + static_cast<double>(add[q])));
+      wave_sync();
+    }
+  }
+  rank_all();
   wave_sync();  // the next tokens' candidates are written over these
   double sum = 0.0;
+  float most = -INFINITY;
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
     rank[q] = q * G + g < count ? rank[q] : a.k;
-    sum += rank[q] < a.k ? s[q] : 0.0;
+    if (kSoftmax) most = rank[q] < a.k && x[q] > most ? x[q] : most;
   }
-  sum = a.renormalize ? group_sum<G>(sum) + 1e-20 : 1.0;
+  if (kSoftmax && a.renormalize) {  // softmax over the chosen
+    most = group_top<G>(most);
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) s[q] = exp64(static_cast<double>(x[q]) - most);
+  }
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) sum += rank[q] < a.k ? s[q] : 0.0;
+  if (a.renormalize) sum = group_sum<G>(sum) + (kSoftmax ? 0.0 : 1e-20);
+  else sum = kSoftmax ? 1.0 / static_cast<double>(inv) : 1.0;
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
     if (in.live && rank[q] < a.k) {
@@ -725,7 +811,8 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
 }
 
 // Waves per SIMD (registers: 128 or 170) where tokens are many: 131072 x 256 sigmoids in 8 groups 72 us
-// with two, 58 with three, 55 with four; softmax scores 125, 106, 114; logits with their sum three 43, four 50.
+// with two, 58 with three, 55 with four; softmax scores, all in fp64, 125, 106, 114; logits with their sum three 43,
+// four 50.
 template <int G, Route MODE>
 constexpr int route_waves() { return MODE == Route::kSoftmax || MODE == Route::kLogitsTotal || G == 32 ? 3 : 4; }
 
@@ -738,7 +825,7 @@ __global__ __launch_bounds__(kThreads, (route_waves<G, MODE>())) void route_kern
     const In in(a, P, per, t0);
     if constexpr (QUICK) {
       __shared__ Candidates<G, L> room[kWavesPerBlock];
-      if (route_quick<G, VPL, L>(a, in, P, room[wv])) continue;
+      if (route_quick<G, VPL, L, MODE>(a, in, P, room[wv])) continue;
     }
     route_exact<G, VPL, L, MODE>(a, in, P);
   }
@@ -756,10 +843,11 @@ hipError_t launch_route(const RouteArgs& a, int P, int per, hipStream_t stream) 
 template <int G, int VPL, int L>
 hipError_t launch_route_mode(const RouteArgs& a, int P, int per, hipStream_t stream) {
   // What comes after the search for candidates costs about as much as the scores of 8 values a lane: 16384 x 256 of
-  // 32 values 11.2 us, all in fp64 16.3; 16384 x 128 of 16 values 7.1 and 8.6; 64 x 128 of 8 values 4.8 and 4.7.
+  // 32 values 11.2 us, all in fp64 16.3; 16384 x 128 of 16 values 7.1 and 8.6; 64 x 128 of 8 values 4.8 and 4.7. Softmax
+  // scores 18.9 and 20.0 (some waves need the fp64 sum after all), 131072 x 256 75 and 105.
   constexpr bool kQuick = G >= 8 && G <= 32 && VPL >= 16;
   if (a.by_score && a.sigmoid) return launch_route<G, VPL, L, Route::kSigmoid, kQuick>(a, P, per, stream);
-  if (a.by_score) return launch_route<G, VPL, L, Route::kSoftmax>(a, P, per, stream);
+  if (a.by_score) return launch_route<G, VPL, L, Route::kSoftmax, kQuick>(a, P, per, stream);
   if (!a.sigmoid && !a.renormalize) return launch_route<G, VPL, L, Route::kLogitsTotal>(a, P, per, stream);
   return launch_route<G, VPL, L, Route::kLogits>(a, P, per, stream);
 }
