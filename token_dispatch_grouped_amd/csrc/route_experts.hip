@@ -414,19 +414,6 @@ struct Rows {
       for (int i = 0; i < VPL; ++i) to[i] = one(from, at + i * 4u);
     }
   }
-  // The sum of e^(logit - top) over the token's experts, in fp64, for a wave that does not hold them any more.
-  __device__ double exponentials(float top) const {
-    double sum = 0.0;
-#pragma unroll 2
-    for (int i = 0; i < VPL; i += 4) {
-      float z[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) z[j] = one(buffer, row + (e0 + i + j) * 4u);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum += i + j < own ? exp64(static_cast<double>(z[j]) - top) : 0.0;
-    }
-    return group_sum<G>(sum);
-  }
   __device__ static float one(__amdgpu_buffer_rsrc_t from, uint32_t at) {
     return __uint_as_float(
         static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b32(from, static_cast<int>(at), 0, 0)));
@@ -618,6 +605,25 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
   // and the sum with the bias, and the exact value's rounding to fp32, |c| each.
   const float base = kSoftmax ? inv * 0x1.2p-18f : 0x1.2p-21f;
   auto margin = [&](float c) { return base + fabsf(c) * 0x1.2p-22f; };
+  // whether any lane of this lane's token says so
+  auto token_any = [&](bool said) {
+    return (__ballot(in.live && said) >> (token * G) & ((uint64_t{1} << G) - 1)) != 0;
+  };
+  // softmax: inv64 of the tokens that ask, one after the other by the whole wave (about 1 us for one of 256)
+  auto find_inverse = [&](bool asks) {
+    uint64_t todo = __ballot(asks && inv64 == 0.0);
+    while (todo != 0) {
+      const int from = __ffsll(static_cast<unsigned long long>(todo)) - 1;
+      todo &= ~(((uint64_t{1} << G) - 1) << (from / G * G));
+      const float* row = a.logits + (in.t - token + from / G) * a.E;
+      const float most = __shfl(top, from);
+      double sum = 0.0;
+#pragma unroll 1
+      for (int e = lane; e < a.E; e += kWave) sum += exp64(static_cast<double>(row[e]) - most);
+      sum = wave_sum(sum);
+      if (token == from / G) inv64 = inverse64(sum);
+    }
+  };
   // the exact choice value of one expert
   auto exact = [&](int e) {
     const float x = in.logit(e);
@@ -662,14 +668,15 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
     other_lanes<G>(static_cast<int>(__float_as_uint(high)), g, __ffs(P) - 1, [&](int bits, int of) {
       beside += of != in.group && !(__uint_as_float(static_cast<uint32_t>(bits)) < low);
     });
-    const bool close = in.group < a.groups && above < a.top_groups * P && beside >= a.top_groups * P;
-    if (__any(in.live && close)) {
-      if constexpr (kSoftmax) inv64 = inverse64(in.exponentials(top));
+    const bool close = token_any(in.group < a.groups && above < a.top_groups * P && beside >= a.top_groups * P);
+    if (__any(close)) {
+      if constexpr (kSoftmax) find_inverse(close);
       const float second = best[1] != INT_MIN ? from_signed(best[1]) : -INFINITY;
       const int from = signed_order(second - margin(second));
       uint32_t near = 0, first_ord = 0, second_ord = 0;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) near |= static_cast<uint32_t>(i < own && o[i] >= from) << i;
+      for (int i = 0; i < VPL; ++i) near |= static_cast<uint32_t>(close && i < own && o[i] >= from) << i;
+#pragma unroll 1
       while (near != 0) {
         const int e = in.e0 + __ffs(near) - 1;
         near &= near - 1;
@@ -682,11 +689,12 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
                                : a.group_top == 2 && size > 1
                                    ? orderable(from_orderable(first_ord) + from_orderable(second_ord))
                                    : first_ord;
-      above = 0;
+      int before = 0;
       other_lanes<G>(static_cast<int>(rank_by), g, __ffs(P) - 1, [&](int value, int of) {
         const uint32_t other = static_cast<uint32_t>(value);
-        above += other > rank_by || (other == rank_by && of < in.group);
+        before += other > rank_by || (other == rank_by && of < in.group);
       });
+      above = close ? before : above;
     }
     if (above >= a.top_groups * P) {
       own = 0;
@@ -702,7 +710,7 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
   uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) mine |= static_cast<uint32_t>(o[i] >= least) << i;
-  if (own == 0) mine = 0;
+  if (own == 0 || !in.live) mine = 0;  // past the last token: no candidates
   // candidates in the order of their ids
   int at = __popc(mine);
 #pragma unroll
@@ -775,10 +783,12 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
       }
     }
     wave_sync();
-    if (__any(in.live && close)) {
-      if (inv64 == 0.0) inv64 = inverse64(in.exponentials(top));
+    close = token_any(close);
+    if (__any(close)) {
+      find_inverse(close);
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) keep(q, static_cast<float>(s[q] * inv64 + static_cast<double>(add[q])));
+      for (int q = 0; q < kSlots; ++q)
+        if (close) keep(q, static_cast<float>(s[q] * inv64 + static_cast<double>(add[q])));
       wave_sync();
     }
   }
@@ -842,12 +852,14 @@ hipError_t launch_route(const RouteArgs& a, int P, int per, hipStream_t stream) 
 
 template <int G, int VPL, int L>
 hipError_t launch_route_mode(const RouteArgs& a, int P, int per, hipStream_t stream) {
-  // What comes after the search for candidates costs about as much as the scores of 8 values a lane: 16384 x 256 of
-  // 32 values 11.2 us, all in fp64 16.3; 16384 x 128 of 16 values 7.1 and 8.6; 64 x 128 of 8 values 4.8 and 4.7. Softmax
-  // scores 18.9 and 20.0 (some waves need the fp64 sum after all), 131072 x 256 75 and 105.
-  constexpr bool kQuick = G >= 8 && G <= 32 && VPL >= 16;
+  // The search for candidates pays where a lane has many values, by what follows it. Sigmoids: 16384 x 256 of 32 values,
+  // k = 8 11.2 us (all in fp64 16.3), k = 16 13 (21); 16384 x 128 of 16 values, k = 8 7.1 (8.6); 21169 x 90 of 12 values,
+  // k = 9 14.2 (13.2); 64 x 128 of 8 values 4.8 (4.7). Softmax: 131072 x 256 of 32 values, k = 8 76 (107), 16384 16.2
+  // (20.4), k = 16 20.7 (21.5); 21169 x 90 of 12 values, k = 8 13.6 (14.3), k = 9 19.0 (16.6).
+  constexpr bool kSome = G >= 8 && G <= 32;
+  constexpr bool kQuick = kSome && (VPL >= 32 || (VPL >= 16 && L <= 8)), kQuickSoftmax = kSome && VPL >= 32;
   if (a.by_score && a.sigmoid) return launch_route<G, VPL, L, Route::kSigmoid, kQuick>(a, P, per, stream);
-  if (a.by_score) return launch_route<G, VPL, L, Route::kSoftmax, kQuick>(a, P, per, stream);
+  if (a.by_score) return launch_route<G, VPL, L, Route::kSoftmax, kQuickSoftmax>(a, P, per, stream);
   if (!a.sigmoid && !a.renormalize) return launch_route<G, VPL, L, Route::kLogitsTotal>(a, P, per, stream);
   return launch_route<G, VPL, L, Route::kLogits>(a, P, per, stream);
 }
