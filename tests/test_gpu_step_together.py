@@ -181,6 +181,22 @@ def test_router_in_a_layer_is_route_topk_for_plain_softmax():
     assert g.rel_err(g.to_f64(gb["d_logits"]), g.to_f64(ga["d_logits"])) <= 1e-5
 
 
+def test_rms_norm_adds_the_experts_input_unless_told_otherwise():
+    T, d, d_ff, E, k = 40, 128, 64, 8, 2
+    x, logits, other = _normal((T, d), 1.0, 1), _normal((T, E), 1.0, 2, torch.float32), _normal((T, d), 1.0, 3)
+    w = (_normal((E, d, 2 * d_ff), d ** -0.5, 4), _normal((E, d_ff, d), d_ff ** -0.5, 5))
+    norm = moe.RmsNorm(_normal((d,), 0.2, 6, mean=1.0), EPS)
+    a = moe.layer(x, logits, *w, k, 0, E, fused=True, norm=norm)
+    b = moe.layer(x, logits, *w, k, 0, E, fused=True, norm=norm, residual=x)
+    c = moe.layer(x, logits, *w, k, 0, E, fused=True, norm=norm, residual=other)
+    layer = moe.layer(x, logits, *w, k, 0, E, fused=True, norm=(norm.weight, None, EPS), residual=other)
+    torch.cuda.synchronize()
+    assert torch.equal(a["normed"], b["normed"]) and torch.equal(a["sum"], b["sum"])
+    assert torch.equal(a["sum"], (x.float() + a["out"].float()).to(torch.bfloat16))
+    assert torch.equal(c["sum"], (other.float() + c["out"].float()).to(torch.bfloat16))
+    assert torch.equal(layer["sum"], c["sum"]) and layer["mean"] is not None
+
+
 def test_serving_block_in_a_graph():
     """Captured once, replayed on other inputs, with eager work between the replays."""
     T, d, d_ff, E, k = 24, 264, 200, 16, 4

@@ -293,6 +293,8 @@ def test_binding_adamw():
         call()
     with pytest.raises(ValueError):
         moe.adamw_states(p, bits=16)
+    with pytest.raises((TypeError, ValueError)):
+        call(weight_decay=["much"])
     first, second = moe.adamw_states([t((3, 50), bf16), t((0,), f32)], bits=8)
     assert first[0].codes.dtype is torch.float8_e4m3fn and first[0].codes.shape == (3, 50) and second[0].scale.shape == (2,)
     assert first[1].scale.shape == (0,) and not second[0].scale.any()
@@ -316,3 +318,27 @@ def test_layer_refuses_what_does_not_go_together():
         moe.layer_backward(x, *w, fwd, x, 2, 0, 8, norm=moe.RmsNorm(t((64,), bf16)))
     with pytest.raises(ValueError, match="norm"):
         moe.layer_backward(x, *w, dict(fwd, mean=None), x, 2, 0, 8, norm=(t((64,), bf16), None, 1e-5))
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Not taken modulo 2^32; tensors without memory stand for the long rows."""
+    wide = (1 << 32) + 8
+    meta = lambda shape, dtype=bf16: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    rows, w, stats = meta((0, wide)), meta(wide), meta(0, f32)
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.rms_norm(rows, w)
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.rms_norm_int8(rows, w)
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.rms_norm_backward(rows, rows, w, stats)
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.rms_norm_backward_workspace_bytes(1, wide)
+    with pytest.raises(ValueError):
+        moe.route_experts(meta((0, wide), f32), 2, moe.Router(groups=wide, top_groups=wide))
+    with pytest.raises(ValueError):
+        moe.route_experts_backward(meta((0, wide), f32), meta((0, 2), i32), meta((0, 2), f32), moe.Router())
+    experts = moe.Int8Experts(meta((1, wide // 64 + 1, 16, 64), torch.int8), meta((1, 16), f32),
+                              meta((1, 1, wide, 64), torch.int8), meta((1, wide), f32))
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.grouped_gemm_int8(moe.Int8Rows(meta((wide // 64 + 1, 0, 64), torch.int8), meta(0, f32)), meta(0, i32), meta(2, i32),
+                              experts, 1, 1, 0, 1)

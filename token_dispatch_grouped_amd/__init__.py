@@ -1605,8 +1605,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps:
             raise ValueError(f"step counts from 1, got {value}")
         else:
             setattr(args, name, value)
-    if isinstance(weight_decay, (int, float)):
-        args.weight_decay = weight_decay
+    if not hasattr(weight_decay, "__iter__"):
+        args.weight_decay = float(weight_decay)
     else:
         decays = array.array("d", weight_decay)
         if len(decays) != n:

@@ -855,9 +855,9 @@ hipError_t launch_route_mode(const RouteArgs& a, int P, int per, hipStream_t str
   // The search for candidates pays where a lane has many values, by what follows it. Sigmoids: 16384 x 256 of 32 values,
   // k = 8 11.2 us (all in fp64 16.3), k = 16 13 (21); 16384 x 128 of 16 values, k = 8 7.1 (8.6); 21169 x 90 of 12 values,
   // k = 9 14.2 (13.2); 64 x 128 of 8 values 4.8 (4.7). Softmax: 131072 x 256 of 32 values, k = 8 76 (107), 16384 16.2
-  // (20.4), k = 16 20.7 (21.5); 21169 x 90 of 12 values, k = 8 13.6 (14.3), k = 9 19.0 (16.6).
+  // (20.4), k = 16 23.1 (21.4); 21169 x 90 of 12 values, k = 8 13.6 (14.3), k = 9 19.0 (16.6).
   constexpr bool kSome = G >= 8 && G <= 32;
-  constexpr bool kQuick = kSome && (VPL >= 32 || (VPL >= 16 && L <= 8)), kQuickSoftmax = kSome && VPL >= 32;
+  constexpr bool kQuick = kSome && (VPL >= 32 || (VPL >= 16 && L <= 8)), kQuickSoftmax = kSome && VPL >= 32 && L <= 8;
   if (a.by_score && a.sigmoid) return launch_route<G, VPL, L, Route::kSigmoid, kQuick>(a, P, per, stream);
   if (a.by_score) return launch_route<G, VPL, L, Route::kSoftmax, kQuickSoftmax>(a, P, per, stream);
   if (!a.sigmoid && !a.renormalize) return launch_route<G, VPL, L, Route::kLogitsTotal>(a, P, per, stream);
