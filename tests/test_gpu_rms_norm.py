@@ -149,6 +149,24 @@ def test_rows_past_the_caches(T, d):
     _backward(case, "bf16", "bf16", s, rstd, ds=True)
 
 
+def test_rows_past_32_bit_offsets():
+    """Rows, sums, codes and gradients whose elements lie past 2^31 and 2^32, as in a call of a few rows."""
+    T, d = (1 << 20) + 3, 4096
+    few = _make(40, d, "bf16", "bf16", seed=21)
+    at = torch.randint(0, T, (40,), generator=torch.Generator().manual_seed(2)).cuda()
+    at[0], at[1], at[2], at[3] = T - 1, (1 << 31) // d + 1, (1 << 32) // d - 1, (1 << 31) // (2 * d) + 1
+    x = few["x"][:1].expand(T, d).contiguous()
+    x[at] = few["x"]
+    rows, y, s, rstd = moe.rms_norm_int8(x, few["w"], EPS, residual=x)
+    few_rows, fy, fs, frstd = moe.rms_norm_int8(x[at].contiguous(), few["w"], EPS, residual=x[at].contiguous())
+    assert torch.equal(y[at], fy) and torch.equal(s[at], fs) and torch.equal(rstd[at], frstd)
+    assert torch.equal(rows.codes[:, at], few_rows.codes) and torch.equal(rows.scale[at], few_rows.scale)
+    del rows, y
+    dx, _ = moe.rms_norm_backward(x, s, few["w"], rstd, d_s=s)
+    fdx, _ = moe.rms_norm_backward(x[at].contiguous(), fs, few["w"], frstd, d_s=fs)
+    assert torch.equal(dx[at], fdx)
+
+
 def test_no_rows():
     case = _make(0, 64, "bf16", "bf16", seed=1)
     rows, y, s, rstd = moe.rms_norm_int8(case["x"], case["w"], EPS, residual=case["r"])
