@@ -214,7 +214,7 @@ __device__ __forceinline__ float encode(const float (&f)[8], uint8_t (&codes)[2]
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint8_t b = static_cast<uint8_t>(w >> (8 * i));
-      codes[h][i] = ROOT && b == 0 && a[i] > 0.f ? 1 : b;
+      codes[h][i] = ROOT && b == 0 && finite && f[4 * h + i] > 0.f ? 1 : b;
     }
   }
   return finite ? scale : __uint_as_float(0x7FC00000u);

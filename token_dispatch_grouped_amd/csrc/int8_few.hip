@@ -109,7 +109,8 @@ __device__ __forceinline__ void finish(const i32x4* part, const float* row_scale
 }
 
 // The workgroup quantises its rows, G threads a row, or (CODES) finds them in 8 bits already: src
-// then holds codes [kblocks][T][64], src_scale their scales. Three waves per SIMD.
+// then holds codes [kblocks][T][64], src_scale their scales (32 tokens x 4 of 128 experts of 2880 x 2880: 272.6 us
+// instead of 277.2). Three waves per SIMD.
 template <bool SWIGLU, int FRAGS, int AHEAD, int G, bool CODES>
 __global__ __launch_bounds__(kThreads, 3) void int8_few_kernel(
     const uint4* __restrict__ src, const float* __restrict__ src_scale, const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets,

