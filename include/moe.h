@@ -112,8 +112,8 @@ typedef struct {
 
 /* Routing to experts by scores.
  *   s_e    = softmax of the token's E logits, or the sigmoid of each
- *   c_e    = s_e + bias_e, computed in fp64 and rounded to fp32 once; the logit itself
- *            where there is no bias and groups or group_top is 1
+ *   c_e    = s_e + bias_e, computed in fp64 and rounded to fp32 once, and -infinity where
+ *            the logit is; the logit itself where there is no bias and groups or group_top is 1
  *   groups   ranked by their largest c, or the fp32 sum of their two largest (of the
  *            only one where a group has one expert); the first top_groups stay
  *   topk_idx the k largest c of the groups that stay, in descending order
@@ -122,7 +122,7 @@ typedef struct {
  *          = scale * s / (sum of the k s + 1e-20)  MOE_SIGMOID with renormalize
  * Equal values go to the lower id; -0.0 equals +0.0; a NaN comes after every number.
  * Any logits and biases give k distinct ids of groups that stay. -infinity (of a logit or
- * a bias) puts an expert behind the others. A token with a NaN or +infinity among its
+ * a bias) puts an expert behind those without. A token with a NaN or +infinity among its
  * logits, or with k chosen logits of -infinity, may have NaN weights.
  *   logits [T, E] fp32, read only; topk_idx [T, k] int32, topk_w [T, k] fp32, written.
  *   Aligned to 4 bytes. r is a HOST struct, read before the call returns.

@@ -31,14 +31,16 @@ def _place(v):
 
 
 def choice_values(logits, score, bias=None, groups=1, group_top=2):
-    """What the choice goes by, fp32 [T, E]: the logits, or round32(score + bias)."""
+    """What the choice goes by, fp32 [T, E]: the logits, or round32(score + bias), -infinity (unless
+    that is a NaN) where the logit is."""
     logits = np.asarray(logits, dtype=np.float32)
     if bias is None and (groups == 1 or group_top == 1):
         return logits
     s = sigmoid(logits) if score == "sigmoid" else softmax(logits)
     if bias is not None:
         s = s + np.asarray(bias, dtype=np.float64)
-    return s.astype(np.float32)
+    c = s.astype(np.float32)
+    return np.where(np.isneginf(logits) & ~np.isnan(c), np.float32(-np.inf), c)
 
 
 def route_experts(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_top=2, renormalize=True,

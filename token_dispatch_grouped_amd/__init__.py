@@ -466,7 +466,7 @@ def _router_struct(router: Router) -> moe_router:
 def route_experts(logits, k: int, router: Router, topk_idx=None, topk_w=None, stream=None):
     """logits [T, E] fp32 -> (topk_idx [T, k] int32, topk_w [T, k] fp32): the k experts
     with the largest scores (plus bias) in the groups that stay, ties to the lower
-    id, and their weights."""
+    id, and their weights. A logit of -infinity masks its expert, whatever the bias."""
     torch = _torch()
     _want(logits, "logits", torch.float32)
     if logits.dim() != 2:

@@ -9,6 +9,8 @@
 // computed in fp64 and rounded to fp32 once: two ways to compute it then agree but for
 // a value within 2^-52 of the middle between two fp32 numbers. Equal c go to the
 // lower id. Without a bias the scores rise with the logits, and these are compared.
+// A logit of -infinity masks its expert: c is -infinity then, whatever the bias.
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -75,6 +77,9 @@ __device__ __forceinline__ double inverse64(double d) {
 }
 
 __device__ __forceinline__ double sigmoid64(float x) { return inverse64(1.0 + exp64(-static_cast<double>(x))); }
+
+// The choice value c of a logit x: a masked expert's is -infinity (unless it is a NaN, which comes later still).
+__device__ __forceinline__ float masked(float x, float c) { return x == -INFINITY && c == c ? -INFINITY : c; }
 
 template <typename T>
 __device__ __forceinline__ T wave_max(T v) {
@@ -158,7 +163,8 @@ __global__ __launch_bounds__(kThreads) void route_any_kernel(const RouteArgs a) 
     auto score = [&](float v) { return a.sigmoid ? sigmoid64(v) : exp64(static_cast<double>(v) - top) / total; };
     for (int e = lane; e < a.E; e += kWave) {
       float v = x[e];
-      if (a.by_score) v = static_cast<float>(score(v) + (a.bias != nullptr ? static_cast<double>(a.bias[e]) : 0.0));
+      if (a.by_score)
+        v = masked(v, static_cast<float>(score(v) + (a.bias != nullptr ? static_cast<double>(a.bias[e]) : 0.0)));
       c[e] = orderable(v);
     }
     wave_sync();
@@ -480,7 +486,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, const Rows<G, VP
       float c = v[r + i];
       if constexpr (kScores) {
         const double s = MODE == Route::kSigmoid ? sigmoid64(c) : exp64(static_cast<double>(c) - top) * total;
-        c = static_cast<float>(s + static_cast<double>(bias[r + i]));
+        c = masked(c, static_cast<float>(s + static_cast<double>(bias[r + i])));
       }
       run[i] = r + i < own ? key_of(orderable(c), e0 + r + i) : 1.0;
     }
@@ -561,8 +567,8 @@ __device__ __forceinline__ float from_signed(int o) {
 // the candidates, hardly ever more than k, are ranked by their exact choice values. Softmax scores are
 // ranked by the fp32 values where no two are close, as their exact ones take the fp64 sum
 // over all experts. Groups that are too close to each other for fp32 are ranked by the exact values of
-// their lanes' best two. False where that does not decide: a NaN, or more candidates than there
-// is room for (many equal values).
+// their lanes' best two. False where that does not decide: a NaN, a bias above 1e38, or more candidates than
+// there is room for (many equal values).
 template <int G, int VPL, int L, Route MODE>
 __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VPL>& in, int P,
                                             Candidates<G, L>& room) {
@@ -577,6 +583,15 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
   double inv64 = 0.0;  // softmax: of the exact sum, once a wave has needed it
   in.logits(v);
   in.load(in.bias_buffer(a), in.e0 * 4u, bias);
+  float least_logit = INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) least_logit = fminf(least_logit, v[i]);
+  if (__any(least_logit == -INFINITY)) {
+    // a masked expert's bias becomes -infinity, others stay (but for NaN and those near the largest number,
+    // which then lead to route_exact below)
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) bias[i] = fminf(bias[i], fmaf(v[i], 0x1p-30f, FLT_MAX));
+  }
   if constexpr (kSoftmax) {
     top = -INFINITY;
 #pragma unroll
@@ -628,7 +643,7 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
   auto exact = [&](int e) {
     const float x = in.logit(e);
     const double s = kSoftmax ? exp64(static_cast<double>(x) - top) * inv64 : sigmoid64(x);
-    return static_cast<float>(s + static_cast<double>(in.one(in.bias_buffer(a), e * 4u)));
+    return masked(x, static_cast<float>(s + static_cast<double>(in.one(in.bias_buffer(a), e * 4u))));
   };
   int o[VPL], best[L];
 #pragma unroll
@@ -651,7 +666,7 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
       for (int i = 0; i < kRun; ++i) best[i] = run[i];
     }
   }
-  bool sure = best[0] <= signed_order(INFINITY);
+  bool sure = best[0] <= signed_order(1e38f);  // no NaN, and sums and margins of values are finite
   if (a.top_groups < a.groups) {
     int one = best[0], two = best[1];
     merge_two<G>(one, two, P);
@@ -761,12 +776,12 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
     add[q] = in.one(in.bias_buffer(a), id[q] * 4u);
     if constexpr (kSoftmax) {
       s[q] = exp64(static_cast<double>(x[q]) - top);
-      c[q] = __builtin_amdgcn_exp2f((x[q] - top) * kLog2e) * inv + add[q];
+      c[q] = masked(x[q], __builtin_amdgcn_exp2f((x[q] - top) * kLog2e) * inv + add[q]);
       room.logit[token][j] = x[q];
       room.bias[token][j] = add[q];
     } else {
       s[q] = sigmoid64(x[q]);
-      c[q] = static_cast<float>(s[q] + static_cast<double>(add[q]));
+      c[q] = masked(x[q], static_cast<float>(s[q] + static_cast<double>(add[q])));
     }
     keep(q, c[q]);
   }
@@ -788,7 +803,7 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
       find_inverse(close);
 #pragma unroll
       for (int q = 0; q < kSlots; ++q)
-        if (close) keep(q, static_cast<float>(s[q] * inv64 + static_cast<double>(add[q])));
+        if (close) keep(q, masked(x[q], static_cast<float>(s[q] * inv64 + static_cast<double>(add[q]))));
       wave_sync();
     }
   }
