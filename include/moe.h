@@ -550,14 +550,24 @@ moe_status moe_clip_grad_norm(const moe_tensor* grads, const moe_tensor* out, in
  * States are fp32, or (MOE_STATE_E4M3) 8-bit: exp_avg holds m and exp_avg_sq holds sqrt(v)
  * as e4m3 codes (finite up to 448), with one fp32 scale per block of MOE_STATE_BLOCK
  * consecutive elements:
- *     scale = max(max|a| * (1 / 448), 2^-126),  code = e4m3(a * (1 / scale)), nearest, ties to even
+ *     scale = max(max|a| * (1 / 448), 2^-126),  code = e4m3(a * (1 / scale))
  * and a sqrt(v) above 0 has at least the code of 2^-9, so that no element is divided by eps
  * alone. The step itself uses the new m and v before they are rounded to codes. A block with
  * an infinity or NaN gets scale NaN and codes 0. All-zero codes and scales are the state
  * before the first step.
+ *   MOE_DITHER   a code's mean is the value: one of the two codes around it, by 16 random bits, a
+ *                hash of the element's index in its tensor and the number of the step (the same
+ *                inputs give the same codes). Over many steps the states follow their averages; the
+ *                held sqrt(v) is within about 15 % of its average (one standard deviation).
+ *   MOE_NEAREST  the nearest code, ties to even: each code is nearer its value, but a state that falls
+ *                by less than half a code (3 to 6 %) in a step does not fall at all. sqrt(v) falls by
+ *                1 - sqrt(beta2) at most, so it stays too large where gradients fade next to a
+ *                block's largest element, and m where beta1 is above 0.94. For single steps and
+ *                states that are quantised from fp32 again and again.
  * Tensors are dense, of any length (0 included), aligned to their elements only. */
 #define MOE_STATE_BLOCK 128
 typedef enum { MOE_STATE_F32 = 0, MOE_STATE_E4M3 = 1 } moe_state;
+typedef enum { MOE_NEAREST = 0, MOE_DITHER = 1 } moe_rounding;
 
 typedef struct {
   void* param;              /* [numel] param_dt, written (read without a master) */
@@ -581,6 +591,7 @@ typedef struct {
   const float* norm;             /* [1] DEVICE fp32, e.g. from moe_grad_norm; or NULL: no clipping */
   float max_norm;                /* >= 0, finite; with norm only */
   moe_state state;
+  moe_rounding rounding;         /* of 8-bit states; not looked at for others */
 } moe_adamw_args;
 
 /* MOE_EINVAL if a written tensor overlaps another tensor of the list (of any entry), or

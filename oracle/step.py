@@ -158,16 +158,50 @@ def to_e4m3(a):
     return (code | np.where(np.signbit(a), 0x80, 0)).astype(np.uint8)
 
 
-def encode_state(a, root=False):
+def mix(h):
+    """The finaliser of MurmurHash3, of uint32 arrays."""
+    h = np.asarray(h, dtype=np.uint32)
+    with np.errstate(over="ignore"):
+        h = (h ^ h >> np.uint32(16)) * np.uint32(0x85EBCA6B)
+        h = (h ^ h >> np.uint32(13)) * np.uint32(0xC2B2AE35)
+    return h ^ h >> np.uint32(16)
+
+
+def dither_bits(index, step):
+    """32 random bits for each element of a tensor (int64 indices) in a step: the lower 16 for the first
+    state, the upper for the second."""
+    index = np.asarray(index, dtype=np.uint64)
+    low, high = (index & np.uint64(0xFFFFFFFF)).astype(np.uint32), (index >> np.uint64(32)).astype(np.uint32)
+    key = mix(np.uint32(step & 0xFFFFFFFF) ^ mix(np.uint32(step >> 32)))
+    with np.errstate(over="ignore"):
+        return mix(low ^ mix(high + key))
+
+
+def to_e4m3_dithered(a, bits):
+    """One of the two codes around each fp32 value of at most 448, by 16 random bits: up where the share
+    of the way there and the bits (as a fraction, half a unit more) add up to one."""
+    mag, bits = np.abs(np.asarray(a, dtype=np.float32)), np.asarray(bits, dtype=np.uint32)
+    # below 2^-6 codes are 2^-9 apart, as they are for another 2^-6 on top
+    shift = np.where(mag < np.float32(2.0 ** -6), np.float32(2.0 ** -6), np.float32(0))
+    up = (((mag + shift).view(np.uint32) + (bits << np.uint32(4) | np.uint32(8))) & np.uint32(0xFFF00000)).view(np.float32) - shift
+    return to_e4m3(np.copysign(np.minimum(up, np.float32(448)), a))
+
+
+def encode_state(a, root=False, bits=None):
     """Codes and scales of an fp32 array, step by step in fp32 as the operator defines
-    them; a root above 0 has at least the code 1."""
+    them; a root above 0 has at least the code 1. bits: dither_bits of its elements."""
     a = np.asarray(a, dtype=np.float32)
     n = a.size
     b = np.pad(a.reshape(-1), (0, -n % BLOCK)).reshape(-1, BLOCK)
     finite = np.isfinite(b).all(axis=1)
     safe = np.where(finite[:, None], b, np.float32(0))
     scale = np.maximum(np.abs(safe).max(axis=1) * (np.float32(1) / np.float32(448)), np.float32(2.0 ** -126))
-    codes = to_e4m3(safe * (np.float32(1) / scale)[:, None])
+    scaled = safe * (np.float32(1) / scale)[:, None]
+    if bits is None:
+        codes = to_e4m3(scaled)
+    else:
+        half = np.asarray(bits).reshape(-1) >> np.uint32(16) if root else np.asarray(bits).reshape(-1) & np.uint32(0xFFFF)
+        codes = to_e4m3_dithered(scaled, np.pad(half, (0, -n % BLOCK)).reshape(-1, BLOCK))
     codes = np.where(finite[:, None], codes, 0).astype(np.uint8)
     if root:
         codes = np.where((safe > 0) & (codes == 0), 1, codes).astype(np.uint8)

@@ -37,6 +37,7 @@ MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP = 0, 1, 2, 3
 MOE_F32, MOE_BF16 = 0, 1
 MOE_SOFTMAX, MOE_SIGMOID = 0, 1
 MOE_STATE_F32, MOE_STATE_E4M3, MOE_STATE_BLOCK = 0, 1, 128
+MOE_NEAREST, MOE_DITHER = 0, 1
 
 
 class MoeError(RuntimeError):
@@ -106,6 +107,7 @@ class moe_adamw_args(ctypes.Structure):
         ("norm", ctypes.c_void_p),
         ("max_norm", ctypes.c_float),
         ("state", ctypes.c_int),
+        ("rounding", ctypes.c_int),
     ]
 
 
@@ -1505,14 +1507,20 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm=None, workspace=None, 
 class Float8State:
     """A tensor's AdamW state in 8 bits: codes (float8_e4m3fn) of the tensor's shape and
     scale [ceil(numel / 128)] fp32. Element i stands for codes[i] * scale[i // 128]; the
-    second state holds the square root of the mean square."""
+    second state holds the square root of the mean square. How adamw rounds to codes:
+    "dither" (what adamw_states makes) to one of the two around a value, by a hash of the
+    element's index and the step, so that a code's mean is the value and the states follow
+    their averages; "nearest", which does not let a state fall by less than half a code (3 to
+    6 %) a step. None, of a state built without saying: "dither" where a beta is above 0.95,
+    else "nearest"; say "dither" for a run of steps on states that were stored."""
     codes: object
     scale: object
+    rounding: str | None = None
 
 
 def adamw_states(params, bits: int = 32):
     """(exp_avg, exp_avg_sq) of a list of parameters before the first step: zeros, as
-    fp32 tensors or (bits = 8) Float8State."""
+    fp32 tensors or (bits = 8) Float8State with rounding "dither"."""
     torch = _torch()
     if bits not in (8, 32):
         raise ValueError(f"bits must be 8 or 32, got {bits}")
@@ -1521,12 +1529,16 @@ def adamw_states(params, bits: int = 32):
         if bits == 32:
             return torch.zeros(p.shape, dtype=torch.float32, device=p.device)
         codes = torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(torch.float8_e4m3fn)
-        return Float8State(codes, torch.zeros(-(-p.numel() // MOE_STATE_BLOCK), dtype=torch.float32, device=p.device))
+        return Float8State(codes, torch.zeros(-(-p.numel() // MOE_STATE_BLOCK), dtype=torch.float32, device=p.device),
+                           "dither")
 
     return [one(p) for p in params], [one(p) for p in params]
 
 
 _dtype_of = operator.attrgetter("dtype")
+_rounding_of = operator.attrgetter("rounding")
+_ROUNDINGS = {"nearest": MOE_NEAREST, "dither": MOE_DITHER}
+_NEAREST_BETA = 0.95  # states built without a rounding: the nearest code up to this beta
 
 
 def _same_list(ts, name: str, params, sizes, dtypes):
@@ -1546,25 +1558,34 @@ def _same_list(ts, name: str, params, sizes, dtypes):
 
 
 def _state_list(ts, name: str, params, sizes, numels):
-    """(tensors, scales or None) of a list of states."""
+    """(tensors, scales or None, the roundings asked for) of a list of states."""
     torch = _torch()
     ts = list(ts)
     kinds = set(map(type, ts))
     if Float8State not in kinds:
-        return _same_list(ts, name, params, sizes, {torch.float32}), None
+        return _same_list(ts, name, params, sizes, {torch.float32}), None, set()
     if len(kinds) > 1:
         raise TypeError(f"{name} must hold fp32 tensors or Float8State, not both")
     codes = _same_list([t.codes for t in ts], name, params, sizes, {torch.float8_e4m3fn})
-    scales = [t.scale for t in ts]
+    scales, rounding = [t.scale for t in ts], set(map(_rounding_of, ts))
     blocks = [(-(-n // MOE_STATE_BLOCK),) for n in numels]
     try:
         if {torch.float32}.issuperset(map(_dtype_of, scales)) and list(map(torch.Tensor.size, scales)) == blocks:
-            return codes, scales
+            return codes, scales, rounding
     except (AttributeError, TypeError):  # something else than tensors
         pass
     for i, (t, n) in enumerate(zip(scales, blocks)):
         _want(t, f"{name}[{i}].scale", torch.float32, n)
-    return codes, scales
+    return codes, scales, rounding
+
+
+def _rounding(asked, betas) -> int:
+    """The one rounding of a step's 8-bit states."""
+    if None in asked:
+        asked = (asked - {None}) | {"dither" if max(betas) > _NEAREST_BETA else "nearest"}
+    if len(asked) != 1 or not asked <= set(_ROUNDINGS):
+        raise ValueError(f"the states of a step must have one rounding of {sorted(_ROUNDINGS)}, got {sorted(map(str, asked))}")
+    return _ROUNDINGS[asked.pop()]
 
 
 def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -1580,8 +1601,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps:
     params, numels, kinds = _tensor_list(params, "params")
     sizes = list(map(torch.Tensor.size, params))
     grads = _same_list(grads, "grads", params, sizes, set(_CODES))
-    m, m_scale = _state_list(exp_avg, "exp_avg", params, sizes, numels)
-    v, v_scale = _state_list(exp_avg_sq, "exp_avg_sq", params, sizes, numels)
+    m, m_scale, m_rounding = _state_list(exp_avg, "exp_avg", params, sizes, numels)
+    v, v_scale, v_rounding = _state_list(exp_avg_sq, "exp_avg_sq", params, sizes, numels)
     if (m_scale is None) != (v_scale is None):
         raise TypeError("exp_avg and exp_avg_sq must both be fp32 or both Float8State")
     n = len(params)
@@ -1595,6 +1616,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps:
             if t.dtype is not torch.float32 or t.shape != p.shape:
                 _want(t, f"masters[{i}]", torch.float32, tuple(p.shape))
     args = moe_adamw_args(beta1=betas[0], beta2=betas[1], eps=eps, state=MOE_STATE_F32 if m_scale is None else MOE_STATE_E4M3)
+    if m_scale is not None:
+        args.rounding = _rounding(m_rounding | v_rounding, betas)
     scalars = []
     for name, value, dtype in (("step", step, torch.int64), ("lr", lr, torch.float32)):
         if torch.is_tensor(value):

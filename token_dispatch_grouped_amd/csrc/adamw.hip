@@ -16,6 +16,14 @@
 // largest, where codes of equal steps would lose all small elements. sqrt(v) > 0 never
 // becomes 0 (m / eps would be the step); its smallest code, 2^-9 / 448 of the largest, is
 // too large then, which makes the step smaller. The step itself uses m and v before the rounding.
+//
+// A step lowers m and sqrt(v) by (1 - b1) and (1 - b2) / 2 of themselves at most, and the nearest code
+// is that of the step before where this is less than half a code (3 to 6 %): a state whose gradients
+// fade stays where it is (b2 = 0.999, gradients down to a tenth: sqrt(v) 7 to 12 times too large for good).
+// Dithered codes go up or down with the probabilities that make their mean the value; the noise that
+// stays is about a code (15 % of sqrt(v), whatever b2). Its random bits are a hash of the element's
+// index and the step's number: the same inputs give the same codes, however a list is cut. (398M elements
+// 1243 us, with the nearest codes 1156: two 32-bit products a hash.)
 #include <math.h>
 
 #include "row_group.h"
@@ -35,6 +43,7 @@ constexpr int64_t kBlocks = int64_t{1} << 23;  // a launch holds fewer than 2^32
 constexpr int kStateBlock = MOE_STATE_BLOCK;
 constexpr float kClipEps = 1e-6f;
 constexpr float kCodeStep = 1.f / 448.f;  // of the largest code
+enum class Hold { kF32, kNearest, kDither };  // of the states: fp32, or 8 bits with codes rounded like this
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
 
 struct Entry {
@@ -59,22 +68,32 @@ struct Scalars {
   const float* d_lr;
   const int64_t* d_step;
   const float* norm;
-  double lr, step, log_b1, log_b2;
+  int64_t step;
+  double lr, log_b1, log_b2;
   float b1, b2, one_b1, one_b2;  // 1 - b from the fp64 b
   float eps, max_norm;
 };
 
-// Of one call: the rate over the first bias correction, the root's factor, the clip factor.
+// The finaliser of MurmurHash3 (Appleby): every bit of h changes about half of the result's.
+__device__ __forceinline__ uint32_t mix(uint32_t h) {
+  h = (h ^ h >> 16) * 0x85EBCA6Bu;
+  h = (h ^ h >> 13) * 0xC2B2AE35u;
+  return h ^ h >> 16;
+}
+
+// Of one call: the rate over the first bias correction, the root's factor, the clip factor, the step's hash.
 struct Step {
   double lr;
   float rate, root, coef;
+  uint32_t key;
 };
 
 __device__ __forceinline__ Step step_of(const Scalars& a) {
   Step s;
   const double lr = a.d_lr != nullptr ? static_cast<double>(*a.d_lr) : a.lr;
-  double t = a.step;
-  if (a.d_step != nullptr) t = static_cast<double>(*a.d_step < 1 ? 1 : *a.d_step);
+  const int64_t step = a.d_step == nullptr ? a.step : *a.d_step < 1 ? 1 : *a.d_step;
+  const double t = static_cast<double>(step);
+  s.key = mix(static_cast<uint32_t>(step) ^ mix(static_cast<uint32_t>(static_cast<uint64_t>(step) >> 32)));
   s.lr = lr;
   s.rate = static_cast<float>(lr / -expm1(t * a.log_b1));
   s.root = static_cast<float>(1.0 / sqrt(-expm1(t * a.log_b2)));
@@ -195,9 +214,21 @@ __device__ __forceinline__ void values4(const uint8_t (&c)[4], float* f) {
   f[3] = __builtin_amdgcn_cvt_f32_fp8(w, 3);
 }
 
-// The block's scale from its 16 lanes' values, and this lane's codes.
-template <bool ROOT>
-__device__ __forceinline__ float encode(const float (&f)[8], uint8_t (&codes)[2][4]) {
+// a (at most 448, but for a rounding) as one of the two e4m3 values around it, the larger with the probability of
+// a's share of the way there. bits: 16 random ones, the upper of the 20 below a code's own, so that a code's value
+// always stays. Below 2^-6 codes are 2^-9 apart, as they are for another 2^-6 on top.
+template <bool POSITIVE>
+__device__ __forceinline__ float dithered(float a, uint32_t bits) {
+  const float mag = POSITIVE ? a : fabsf(a), shift = mag < 0x1p-6f ? 0x1p-6f : 0.f;
+  const float up = __uint_as_float((__float_as_uint(mag + shift) + (bits << 4 | 8u)) & 0xFFF00000u) - shift;
+  return POSITIVE ? fminf(up, 448.f) : copysignf(fminf(up, 448.f), a);
+}
+
+// The block's scale from its 16 lanes' values, and this lane's codes. With DITHER, the upper (ROOT) or lower half of
+// an element's 32 random bits.
+template <bool ROOT, bool DITHER>
+__device__ __forceinline__ float encode(const float (&f)[8], const uint32_t (&random)[DITHER ? 8 : 1],
+                                        uint8_t (&codes)[2][4]) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max_u32(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
@@ -209,7 +240,10 @@ __device__ __forceinline__ float encode(const float (&f)[8], uint8_t (&codes)[2]
   for (int h = 0; h < 2; ++h) {
     float a[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = finite ? f[4 * h + i] * inv : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      a[i] = finite ? f[4 * h + i] * inv : 0.f;
+      if constexpr (DITHER) a[i] = dithered<ROOT>(a[i], ROOT ? random[4 * h + i] >> 16 : random[4 * h + i] & 0xFFFFu);
+    }
     const uint32_t w = codes4(a);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -255,7 +289,7 @@ __device__ __forceinline__ void piece_f32(const Entry& e, int64_t first, const S
 
 // A piece with 8-bit states: a block of 128 elements is in 16 lanes, four elements of each of
 // its halves in a lane, so that a load of fp32 values is one run as well.
-template <int PIECE, bool P_BF16, bool G_BF16, bool MASTER, bool STREAM, bool FULL>
+template <bool DITHER, int PIECE, bool P_BF16, bool G_BF16, bool MASTER, bool STREAM, bool FULL>
 __device__ __forceinline__ void piece_e4m3(const Entry& e, int64_t first, const Scalars& a, const Step& s, float decay) {
   constexpr int N = 4, kHalves = 2, kLanes = kStateBlock / (N * kHalves), kU = PIECE / (kThreads * N * kHalves);
   const int block = static_cast<int>(threadIdx.x) / kLanes, lane = static_cast<int>(threadIdx.x) % kLanes;
@@ -299,7 +333,14 @@ __device__ __forceinline__ void piece_e4m3(const Entry& e, int64_t first, const 
         if (!FULL && j >= n[q][h]) mj = rj = 0.f;  // past the last element: not in the block's largest
       }
     }
-    const float m_scale = encode<false>(m, mc[q]), v_scale = encode<true>(root, vc[q]);
+    uint32_t random[DITHER ? kHalves * N : 1];
+    if constexpr (DITHER) {
+      const uint32_t high = mix(static_cast<uint32_t>(static_cast<uint64_t>(i0) >> 32) + s.key);  // the block's
+#pragma unroll
+      for (int j = 0; j < kHalves * N; ++j)
+        random[j] = mix((static_cast<uint32_t>(i0) + j / N * (kStateBlock / kHalves) + lane * N + j % N) ^ high);
+    }
+    const float m_scale = encode<false, DITHER>(m, random, mc[q]), v_scale = encode<true, DITHER>(root, random, vc[q]);
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const int64_t i = i0 + h * (kStateBlock / kHalves) + lane * N;
@@ -315,19 +356,20 @@ __device__ __forceinline__ void piece_e4m3(const Entry& e, int64_t first, const 
   }
 }
 
-template <bool E4M3, int PIECE, bool STREAM, bool P_BF16, bool G_BF16, bool MASTER>
+template <Hold HOLD, int PIECE, bool STREAM, bool P_BF16, bool G_BF16, bool MASTER>
 __device__ __forceinline__ void piece(const Entry& e, int64_t first, const Scalars& a, const Step& s, float decay) {
+  constexpr bool kE4m3 = HOLD != Hold::kF32, kDither = HOLD == Hold::kDither;
   // only a tensor's last piece looks where the tensor ends
   if (first + PIECE <= e.numel) {
-    if constexpr (E4M3) piece_e4m3<PIECE, P_BF16, G_BF16, MASTER, STREAM, true>(e, first, a, s, decay);
+    if constexpr (kE4m3) piece_e4m3<kDither, PIECE, P_BF16, G_BF16, MASTER, STREAM, true>(e, first, a, s, decay);
     else piece_f32<PIECE, P_BF16, G_BF16, MASTER, STREAM, true>(e, first, a, s, decay);
   } else {
-    if constexpr (E4M3) piece_e4m3<PIECE, P_BF16, G_BF16, MASTER, STREAM, false>(e, first, a, s, decay);
+    if constexpr (kE4m3) piece_e4m3<kDither, PIECE, P_BF16, G_BF16, MASTER, STREAM, false>(e, first, a, s, decay);
     else piece_f32<PIECE, P_BF16, G_BF16, MASTER, STREAM, false>(e, first, a, s, decay);
   }
 }
 
-template <bool E4M3, int PIECE, bool STREAM>
+template <Hold HOLD, int PIECE, bool STREAM>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const List l, const Scalars a) {
   const Step s = step_of(a);
   const int64_t total = l.piece0[l.n];
@@ -338,25 +380,25 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const List l, const Sca
     const int64_t first = (at - l.piece0[i]) * PIECE;
     const float decay = static_cast<float>(1.0 - s.lr * e.decay);
     if (!e.p_bf16) {
-      if (e.g_bf16) piece<E4M3, PIECE, STREAM, false, true, false>(e, first, a, s, decay);
-      else piece<E4M3, PIECE, STREAM, false, false, false>(e, first, a, s, decay);
+      if (e.g_bf16) piece<HOLD, PIECE, STREAM, false, true, false>(e, first, a, s, decay);
+      else piece<HOLD, PIECE, STREAM, false, false, false>(e, first, a, s, decay);
     } else if (e.w != nullptr) {
-      if (e.g_bf16) piece<E4M3, PIECE, STREAM, true, true, true>(e, first, a, s, decay);
-      else piece<E4M3, PIECE, STREAM, true, false, true>(e, first, a, s, decay);
+      if (e.g_bf16) piece<HOLD, PIECE, STREAM, true, true, true>(e, first, a, s, decay);
+      else piece<HOLD, PIECE, STREAM, true, false, true>(e, first, a, s, decay);
     } else {
-      if (e.g_bf16) piece<E4M3, PIECE, STREAM, true, true, false>(e, first, a, s, decay);
-      else piece<E4M3, PIECE, STREAM, true, false, false>(e, first, a, s, decay);
+      if (e.g_bf16) piece<HOLD, PIECE, STREAM, true, true, false>(e, first, a, s, decay);
+      else piece<HOLD, PIECE, STREAM, true, false, false>(e, first, a, s, decay);
     }
   }
 }
 
-template <bool E4M3>
+template <Hold HOLD>
 hipError_t launch_list(const List& l, const Scalars& a, bool small, bool big, hipStream_t stream) {
   const int64_t pieces = l.piece0[l.n];
   const dim3 grid(static_cast<unsigned>(pieces < kBlocks ? pieces : kBlocks));
-  if (small) hipLaunchKernelGGL((adamw_kernel<E4M3, kSmallPiece, false>), grid, dim3(kThreads), 0, stream, l, a);
-  else if (big) hipLaunchKernelGGL((adamw_kernel<E4M3, kPiece, true>), grid, dim3(kThreads), 0, stream, l, a);
-  else hipLaunchKernelGGL((adamw_kernel<E4M3, kPiece, false>), grid, dim3(kThreads), 0, stream, l, a);
+  if (small) hipLaunchKernelGGL((adamw_kernel<HOLD, kSmallPiece, false>), grid, dim3(kThreads), 0, stream, l, a);
+  else if (big) hipLaunchKernelGGL((adamw_kernel<HOLD, kPiece, true>), grid, dim3(kThreads), 0, stream, l, a);
+  else hipLaunchKernelGGL((adamw_kernel<HOLD, kPiece, false>), grid, dim3(kThreads), 0, stream, l, a);
   return hipGetLastError();
 }
 
@@ -375,7 +417,7 @@ hipError_t launch_adamw(const moe_adamw_tensor* t, int n, const moe_adamw_args& 
   a.d_step = args.d_step;
   a.norm = args.norm;
   a.lr = args.lr;
-  a.step = static_cast<double>(args.step);
+  a.step = args.step;
   a.log_b1 = log(args.beta1);
   a.log_b2 = log(args.beta2);
   a.b1 = static_cast<float>(args.beta1);
@@ -417,7 +459,9 @@ hipError_t launch_adamw(const moe_adamw_tensor* t, int n, const moe_adamw_args& 
       ++l.n;
     }
     if (l.n == 0) break;
-    const hipError_t err = e4m3 ? launch_list<true>(l, a, small, big, stream) : launch_list<false>(l, a, small, big, stream);
+    const hipError_t err = !e4m3 ? launch_list<Hold::kF32>(l, a, small, big, stream)
+                           : args.rounding == MOE_DITHER ? launch_list<Hold::kDither>(l, a, small, big, stream)
+                                                         : launch_list<Hold::kNearest>(l, a, small, big, stream);
     if (err != hipSuccess) return err;
   }
   return hipSuccess;

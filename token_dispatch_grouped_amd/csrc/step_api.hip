@@ -54,6 +54,7 @@ struct Range {
 moe_status check_adamw(const moe_adamw_tensor* t, int32_t n, const moe_adamw_args* a) {
   if (a == nullptr || n < 0 || (n > 0 && t == nullptr)) return MOE_EINVAL;
   if (a->state != MOE_STATE_F32 && a->state != MOE_STATE_E4M3) return MOE_EINVAL;
+  if (a->state == MOE_STATE_E4M3 && a->rounding != MOE_NEAREST && a->rounding != MOE_DITHER) return MOE_EINVAL;
   if (!isfinite(a->lr) || !(a->beta1 >= 0 && a->beta1 < 1) || !(a->beta2 >= 0 && a->beta2 < 1)) return MOE_EINVAL;
   if (!(a->eps >= 1e-30) || !isfinite(static_cast<float>(a->eps)) || !isfinite(a->weight_decay)) return MOE_EINVAL;
   if (a->d_step == nullptr && a->step < 1) return MOE_EINVAL;
