@@ -1589,14 +1589,14 @@ def _rounding(asked, betas) -> int:
 
 
 def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
-          weight_decay=0.0, masters=None, norm=None, max_norm: float = 0.0, stream=None) -> None:
+          weight_decay=0.0, masters=None, norm=None, max_norm: float | None = None, stream=None) -> None:
     """One AdamW step, in place, over lists of params (bf16 or fp32), grads (bf16 or
     fp32) and states (fp32 or Float8State, from adamw_states). masters: fp32 copies of
     bf16 params, which the step then reads and writes (None for the list or for single
     entries; an fp32 param has none). weight_decay: a number, or one for each param.
     step (the number of this step, from 1) and lr are numbers, or tensors [1] (int64,
     fp32) that a captured graph reads at each replay. With norm [1] fp32 (grad_norm), the
-    gradients are clipped to max_norm on the way, without being written."""
+    gradients are clipped to max_norm on the way, without being written; one needs the other."""
     torch = _torch()
     params, numels, kinds = _tensor_list(params, "params")
     sizes = list(map(torch.Tensor.size, params))
@@ -1637,6 +1637,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps:
         args.weight_decays = decays.buffer_info()[0]
     if norm is not None:
         _want(norm, "norm", torch.float32, (1,))
+        if max_norm is None:
+            raise ValueError("norm needs max_norm, what to clip to")
         args.norm, args.max_norm = norm.data_ptr(), max_norm
         scalars.append(norm)
     elif max_norm:
