@@ -764,7 +764,7 @@ def layer(x, logits, w_gate_up, w_down, k: int, e_begin: int, e_end: int, stream
         h, y = grouped_gemm(disp.x_perm, disp.offsets, w_gate_up, w_down, T, k, E, e_begin, e_end, stream=stream)
     out = combine(y, disp.pair_pos, w, T, k, E, e_begin, e_end, stream=stream)
     res = dict(idx=idx, w=w, counts=disp.counts, offsets=disp.offsets, perm=disp.perm,
-               pair_pos=disp.pair_pos, x_perm=disp.x_perm, h=h, y=y, out=out, gu=gu)
+               pair_pos=disp.pair_pos, x_perm=disp.x_perm, h=h, y=y, out=out, gu=gu, router=router)
     if router is not None:
         res["logits"] = logits
     return _with_norm(res, x if residual is None else residual, norm, stream)
@@ -984,7 +984,9 @@ def layer_backward(x, w_gate_up, w_down, fwd: dict, d_out, k: int, e_begin: int,
     the gradient through the experts alone; the residual's gradient (x's, unless
     the forward was given another) adds d_sum, and x's what comes through the logits.
     `router` is the forward's."""
-    if (router is None) != ("logits" not in fwd):
+    # a dict that layer() did not make says by its logits whether a router chose
+    scored = fwd["router"] is not None if "router" in fwd else "logits" in fwd
+    if (router is not None) != scored:
         raise ValueError("router must be the forward's")
     T = x.shape[0]
     E = fwd["counts"].shape[0]
