@@ -48,3 +48,48 @@ def test_the_forwards_router_is_needed():
     got = moe.layer_backward(x, wgu, wdn, hand, up, K, 0, E, router=router)
     torch.cuda.synchronize()
     assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+def test_overwritten_logits_are_refused():
+    x, logits, wgu, wdn, up = _inputs()
+    router = moe.Router("sigmoid", renormalize=False)
+    want = moe.layer_backward(x, wgu, wdn, moe.layer(x, logits.clone(), wgu, wdn, K, 0, E, fused=True, router=router), up, K,
+                              0, E, router=router)
+    fwd = moe.layer(x, logits, wgu, wdn, K, 0, E, fused=True, router=router)
+    for _ in range(2):
+        got = moe.layer_backward(x, wgu, wdn, fwd, up, K, 0, E, router=router)
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], want[k]) for k in want)
+    logits.copy_(_normal((T, E), 1.0, 6, torch.float32))  # the next batch's, in the same buffer
+    with pytest.raises(ValueError, match="overwritten"):
+        moe.layer_backward(x, wgu, wdn, fwd, up, K, 0, E, router=router)
+    fwd = moe.layer(x, logits, wgu, wdn, K, 0, E, fused=True, router=router)
+    moe.layer_backward(x, wgu, wdn, fwd, up, K, 0, E, router=router)
+    torch.cuda.synchronize()
+
+
+def test_logits_in_a_buffer_of_several():
+    """Views count the changes of each other: filling one after the other's forward is no change of it."""
+    x, logits, wgu, wdn, up = _inputs()
+    router = moe.Router("sigmoid")
+    both = torch.empty((2, T, E), device=dev)
+    both[0].copy_(logits)
+    first = moe.layer(x, both[0], wgu, wdn, K, 0, E, fused=True, router=router)
+    both[1].copy_(_normal((T, E), 1.0, 6, torch.float32))
+    second = moe.layer(x, both[1], wgu, wdn, K, 0, E, fused=True, router=router)
+    for fwd, z in ((first, both[0]), (second, both[1])):
+        want = moe.layer_backward(x, wgu, wdn, moe.layer(x, z.clone(), wgu, wdn, K, 0, E, fused=True, router=router), up, K,
+                                  0, E, router=router)
+        got = moe.layer_backward(x, wgu, wdn, fwd, up, K, 0, E, router=router)
+        torch.cuda.synchronize()
+        assert torch.equal(got["d_logits"], want["d_logits"])
+
+
+def test_inference_tensors_have_no_count():
+    x, logits, wgu, wdn, up = _inputs()
+    router = moe.Router("sigmoid")
+    with torch.inference_mode():
+        z = logits.clone()
+        fwd = moe.layer(x, z, wgu, wdn, K, 0, E, fused=True, router=router)
+        moe.layer_backward(x, wgu, wdn, fwd, up, K, 0, E, router=router)
+    torch.cuda.synchronize()

@@ -739,7 +739,10 @@ def layer(x, logits, w_gate_up, w_down, k: int, e_begin: int, e_end: int, stream
     "normed", "mean" and "rstd" as well. With `norm` an RmsNorm, by rms_norm ("mean"
     is None). On a rank that holds a share of the experts, out is a partial sum over
     ranks: join the ranks' first and normalise then.
-    With `router`, the experts are chosen by route_experts instead of route_topk."""
+    With `router`, the experts are chosen by route_experts instead of route_topk, and
+    the result has "logits", the tensor given, which layer_backward reads: it must
+    not be overwritten before (torch's changes in place are found out and refused,
+    unless logits is a view of another tensor)."""
     torch = _torch()
     T = x.shape[0]
     if logits.dim() != 2 or logits.shape[0] != T:
@@ -766,8 +769,14 @@ def layer(x, logits, w_gate_up, w_down, k: int, e_begin: int, e_end: int, stream
     res = dict(idx=idx, w=w, counts=disp.counts, offsets=disp.offsets, perm=disp.perm,
                pair_pos=disp.pair_pos, x_perm=disp.x_perm, h=h, y=y, out=out, gu=gu, router=router)
     if router is not None:
-        res["logits"] = logits
+        res["logits"], res["logits_version"] = logits, _version(logits)
     return _with_norm(res, x if residual is None else residual, norm, stream)
+
+
+def _version(t):
+    """torch's count of the changes of a tensor in place; None where there is none, or it
+    counts those of other tensors too (views)."""
+    return None if t.is_inference() or t._base is not None else t._version
 
 
 @dataclass(frozen=True)
@@ -988,6 +997,8 @@ def layer_backward(x, w_gate_up, w_down, fwd: dict, d_out, k: int, e_begin: int,
     scored = fwd["router"] is not None if "router" in fwd else "logits" in fwd
     if (router is not None) != scored:
         raise ValueError("router must be the forward's")
+    if router is not None and fwd.get("logits_version") is not None and fwd["logits_version"] != fwd["logits"]._version:
+        raise ValueError("the forward's logits were overwritten since: give layer() a copy of them")
     T = x.shape[0]
     E = fwd["counts"].shape[0]
     extra = {}
