@@ -7,7 +7,7 @@
 //
 // Which experts a token gets hangs on the order of values that may be close, so c is
 // computed in fp64 and rounded to fp32 once: two ways to compute it then agree but for
-// a value within 2^-52 of the middle between two fp32 numbers. Equal c go to the
+// a value within 2^-50 (of itself) of the middle between two fp32 numbers. Equal c go to the
 // lower id. Without a bias the scores rise with the logits, and these are compared.
 // A logit of -infinity masks its expert: c is -infinity then, whatever the bias.
 #include <float.h>
@@ -40,19 +40,20 @@ __device__ __forceinline__ float from_orderable(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
-// e^x in fp64, to about 2^-52: x = n ln 2 + r with |r| <= ln 2 / 2, and e^r by its power series
+// e^x in fp64, to 2^-51: x = n ln 2 + r with |r| <= ln 2 / 2, and e^r by its power series
 // (the term r^13 / 13! is below 2^-52). x is held to +-700, so that 1 + e^x and its inverse are
 // finite; a NaN stays one. A few instructions fewer than the library's, made for any argument, and its
 // division (131072 x 256 softmax scores, all in fp64: 105 us against 111).
 __device__ __forceinline__ double exp64(double x) {
   const double y = fmin(fmax(x, -700.0), 700.0);
   const double n = rint(y * 1.4426950408889634);
-  const double r = fma(n, -0.6931471805599453, y);
+  double r = fma(n, -0.6931471805599453, y);
   // coefficients from scalar registers: as part of the fused operation, not moved to its result first
   auto scalar = [](double c) {
     asm("" : "+s"(c));
     return c;
   };
+  r = fma(n, scalar(-2.3190468138462996e-17), r);  // one double of ln 2 is off by 12 * 2^-52 for |x| of 80
   double p = fma(scalar(1.0 / 479001600), r, scalar(1.0 / 39916800));
   p = fma(p, r, scalar(1.0 / 3628800));
   p = fma(p, r, scalar(1.0 / 362880));
