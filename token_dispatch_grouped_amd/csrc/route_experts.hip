@@ -21,9 +21,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWavesPerBlock = kThreads / kWave;
-// Few lanes a token (many values each) are less work in all, and used where the tokens fill the chip's
-// 1024 SIMDs with two waves each all the same: 16384 x 256 sigmoids 11.2 us with 8 lanes, 13.5 with 16;
-// 8192 x 256 softmax scores 14.2 with 8, 12.0 with 16.
+// Lanes of a token. A call of few tokens takes as many as hold 8 values each (16 from 16 lanes on): short chains.
+// Fewer lanes with more values are less work in all, and taken where the tokens fill the chip's 1024 SIMDs with two waves
+// each all the same. us of 8 experts a token by the first rule and by the second (logits; sigmoids with a bias; softmax
+// scores with one):
+//   128 experts, 1000 tokens 3.8 4.9 6.6 and 5.8 11.2 13.7; 16384 6.5 9.1 11.9 and 5.1 6.9 11.2; 65536 18.2 28.3 35.8 and 11.7 28.0 33.0
+//   512, 1000 tokens 4.9 6.4 9.5 and 6.2 8.1 10.5; 8192 8.7 12.3 20.4 and 7.7 10.4 14.7; 65536 48 75 133 and 37 54 71
 constexpr int64_t kFewLanes = 2 * 1024 * kWave;
 constexpr int kTop = 16;  // chosen experts that are kept in registers
 
@@ -1061,9 +1064,14 @@ hipError_t launch_route_experts(const moe_router& r, const float* logits, int32_
     int blocks = 1;  // groups rounded up to a power of two
     while (blocks < r.groups) blocks *= 2;
     const int size = E / r.groups;
-#define MOE_ROUTE(LANES, VALUES)                                                                              \
-  if (T * LANES >= least && blocks <= LANES && (size + LANES / blocks - 1) / (LANES / blocks) <= VALUES)      \
-    return launch_route_top<LANES, VALUES>(a, LANES / blocks, (size + LANES / blocks - 1) / (LANES / blocks), stream)
+    auto per = [&](int lanes) { return (size + lanes / blocks - 1) / (lanes / blocks); };  // values of a lane
+    auto fits = [&](int lanes, int values) { return blocks <= lanes && per(lanes) <= values; };
+    int few = 1;  // lanes of a call of few tokens
+    while (few < kWave && !fits(few, few < 16 ? 8 : 16)) few *= 2;
+    // more tokens never take more lanes (2048 x 64 6.5 us with 64, 3.6 with 8; 4096 x 256 sigmoids in groups 9.6 with 32, 6.5 with 16)
+#define MOE_ROUTE(LANES, VALUES)                                                                  \
+  if (fits(LANES, VALUES) && (least == 0 || (T * LANES >= least && LANES < few)))                 \
+    return launch_route_top<LANES, VALUES>(a, LANES / blocks, per(LANES), stream)
     for (const int64_t least : {kFewLanes, int64_t{0}}) {
       MOE_ROUTE(1, 8);
       MOE_ROUTE(2, 8);
