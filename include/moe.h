@@ -120,6 +120,9 @@ typedef struct {
  *   topk_w = scale * s                             without renormalize
  *          = scale * softmax over the k logits     MOE_SOFTMAX with renormalize
  *          = scale * s / (sum of the k s + 1e-20)  MOE_SIGMOID with renormalize
+ * s and topk_w are computed in fp64 and rounded once, but for the sum over all E experts that
+ * topk_w of MOE_SOFTMAX without renormalize goes by: that is fp32, and such weights are within
+ * 50 * 2^-24 of themselves (2^-22 as a rule), with last bits that may differ with s->T.
  * Equal values go to the lower id; -0.0 equals +0.0; a NaN comes after every number.
  * Any logits and biases give k distinct ids of groups that stay. -infinity (of a logit or
  * a bias) puts an expert behind those without. A token with a NaN or +infinity among its
@@ -437,7 +440,8 @@ moe_status moe_layer_norm_backward(const moe_shape* s, moe_dtype dt, const void*
  *            both NULL: the rows in 8 bits, as the experts below take them: codes and scale
  *            of the fp32 y, before its rounding to dt (MOE_EUNSUPPORTED unless dt = MOE_BF16).
  * A row with a NaN gets NaN, a row of zeros with eps 0 as well; an infinity gives rstd 0 and
- * so NaN for itself, 0 for the others, and a scale of NaN. Uses s->T and s->d only. Errors as moe_layer_norm. */
+ * so NaN for itself, 0 for the others, and a scale of NaN. With eps 0, rstd of a row whose root
+ * mean square is below 2^-128 is infinite, and so is y. Uses s->T and s->d only. Errors as moe_layer_norm. */
 moe_status moe_rms_norm(const moe_shape* s, moe_dtype dt, const void* x, const void* residual,
                         moe_dtype wdt, const void* weight, float eps, void* y, void* sum, float* rstd,
                         void* q, float* q_scale, hipStream_t stream);
@@ -557,8 +561,9 @@ moe_status moe_clip_grad_norm(const moe_tensor* grads, const moe_tensor* out, in
  * before the first step.
  *   MOE_DITHER   a code's mean is the value: one of the two codes around it, by 16 random bits, a
  *                hash of the element's index in its tensor and the number of the step (the same
- *                inputs give the same codes). Over many steps the states follow their averages; the
- *                held sqrt(v) is within about 15 % of its average (one standard deviation).
+ *                inputs give the same codes; a graph that replays one number replays its bits). Over
+ *                many steps the states follow their averages; the held sqrt(v) is within about
+ *                15 % of its average (one standard deviation).
  *   MOE_NEAREST  the nearest code, ties to even: each code is nearer its value, but a state that falls
  *                by less than half a code (3 to 6 %) in a step does not fall at all. sqrt(v) falls by
  *                1 - sqrt(beta2) at most, so it stays too large where gradients fade next to a

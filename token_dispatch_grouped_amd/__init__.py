@@ -1522,8 +1522,8 @@ class Float8State:
     scale [ceil(numel / 128)] fp32. Element i stands for codes[i] * scale[i // 128]; the
     second state holds the square root of the mean square. How adamw rounds to codes:
     "dither" (what adamw_states makes) to one of the two around a value, by a hash of the
-    element's index and the step, so that a code's mean is the value and the states follow
-    their averages; "nearest", which does not let a state fall by less than half a code (3 to
+    element's index and the step's number, so that a code's mean is the value and the states
+    follow their averages as the number changes; "nearest", which does not let a state fall by less than half a code (3 to
     6 %) a step. None, of a state built without saying: "dither" where a beta is above 0.95,
     else "nearest"; say "dither" for a run of steps on states that were stored."""
     codes: object

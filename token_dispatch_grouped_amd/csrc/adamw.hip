@@ -6,7 +6,7 @@
 //
 // Bound by HBM: every array is read and written once (28 bytes an element for bf16
 // weights with masters and fp32 states, 16 with 8-bit states: 398M elements in 1975 us
-// and 1121 us, 5.6 and 5.7 TB/s). The tensors of a list are cut into pieces, numbered
+// and 1160 us, 5.6 and 5.5 TB/s). The tensors of a list are cut into pieces, numbered
 // through, a workgroup each (2048 workgroups that take turns: 2180 us for 398M weights
 // against 1975). A launch carries its tensors' addresses in the kernel arguments (no table
 // to copy, so a captured graph keeps them), up to kList of them.
@@ -23,7 +23,7 @@
 // Dithered codes go up or down with the probabilities that make their mean the value; the noise that
 // stays is about a code (15 % of sqrt(v), whatever b2). Its random bits are a hash of the element's
 // index and the step's number: the same inputs give the same codes, however a list is cut. (398M elements
-// 1243 us, with the nearest codes 1156: two 32-bit products a hash.)
+// 1230 us, with the nearest codes 1160: two 32-bit products a hash.)
 #include <math.h>
 
 #include "row_group.h"
@@ -433,7 +433,7 @@ hipError_t launch_adamw(const moe_adamw_tensor* t, int n, const moe_adamw_args& 
     pieces += (t[i].numel + kPiece - 1) / kPiece;
   }
   // A list that does not fit the memory-side cache passes it by (398M bf16 weights with masters: 1975 us, and 2080
-  // through the cache; with 8-bit states 1121 and 1160). One that fits is found there by the next call (157 MB: 57 us, and 64 past it).
+  // through the cache; with 8-bit states 1160 and 1214). One that fits is found there by the next call (157 MB: 57 us, and 64 past it).
   const bool big = bytes > kStreamBytes;
   // (60 fp32 tensors of 1 to 368641 elements, 1.5M in all: 14.5 us, and 18.7 with the large pieces)
   const bool small = !big && pieces <= kFewPieces;

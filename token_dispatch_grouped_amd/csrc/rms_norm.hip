@@ -13,7 +13,8 @@
 // directions are bound by HBM: a row is read once and held in registers through its
 // reductions. 16384 x 7168 bf16 with a residual 153 us (6.1 TB/s); 8192 x 2880 bf16 18.1 us,
 // with 8-bit rows 26.5; 32 x 2880 3.4 and 4.3, one launch's latency. The gradient of 4096 x
-// 4096 bf16 with ds 23.6 us (5.7 TB/s), and 3.9 for the join of the column sums.
+// 4096 bf16 with ds 23.6 us (5.7 TB/s), and 3.9 for the join of the column sums; of 1024 x 32768 bf16
+// 63 us (3.2 TB/s: rows of 1024 threads spill 11 to 14 registers).
 #include <limits.h>
 
 #include "int8_code.h"

@@ -140,7 +140,8 @@ RouteArgs make_args(const moe_router& r, const float* logits, int32_t* idx, floa
 }
 
 // Any sizes (more than kTop experts a token, more than 64 groups): one wave per token, the choice values in LDS and, as keys (value, then lower
-// id), in registers; k rounds of a maximum over the wave.
+// id), in registers; k rounds of a maximum over the wave, each waiting for the one before (16384 tokens, 17, 24 and 32 of
+// 256: 82, 105 and 133 us).
 __global__ __launch_bounds__(kThreads) void route_any_kernel(const RouteArgs a) {
   constexpr int kPer = kMaxExperts / kWave;
   __shared__ uint32_t values[kWavesPerBlock][kMaxExperts];
