@@ -115,7 +115,8 @@ typedef struct {
  *   c_e    = s_e + bias_e, computed in fp64 and rounded to fp32 once, and -infinity where
  *            the logit is; the logit itself where there is no bias and groups or group_top is 1
  *   groups   ranked by their largest c, or the fp32 sum of their two largest (of the
- *            only one where a group has one expert); the first top_groups stay
+ *            only one where a group has one expert; sums of -infinity, of groups with fewer
+ *            than two experts that are not masked, by the largest); the first top_groups stay
  *   topk_idx the k largest c of the groups that stay, in descending order
  *   topk_w = scale * s                             without renormalize
  *          = scale * softmax over the k logits     MOE_SOFTMAX with renormalize

@@ -57,9 +57,11 @@ def route_experts(logits, k, score="softmax", bias=None, groups=1, top_groups=1,
             value = []
             for g in range(groups):
                 best = sorted(c[t, g * size:(g + 1) * size], key=_place)
-                with np.errstate(invalid="ignore"):
-                    value.append(best[0] + best[1] if group_top == 2 and size > 1 else best[0])  # fp32
-            stay = sorted(range(groups), key=lambda g: (*_place(value[g]), g))[:top_groups]
+                with np.errstate(invalid="ignore", over="ignore"):
+                    v = best[0] + best[1] if group_top == 2 and size > 1 else best[0]  # fp32
+                # sums of -infinity go by the largest
+                value.append((*_place(v), *(_place(best[0]) if v == -np.inf else (0, 0.0))))
+            stay = sorted(range(groups), key=lambda g: (*value[g], g))[:top_groups]
         from_ = [e for g in stay for e in range(g * size, (g + 1) * size)]
         idx[t] = sorted(from_, key=lambda e: (*_place(c[t, e]), e))[:k]
         x = logits[t, idx[t]]

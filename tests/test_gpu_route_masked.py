@@ -107,3 +107,43 @@ def test_a_masked_expert_passes_no_gradient_under_a_bias():
                 torch.cuda.synchronize()
                 assert not ((idx == 5) | (idx == 20)).any()
                 assert torch.isfinite(w).all() and torch.isfinite(g).all() and not g[:, [5, 20]].any()
+
+
+# as SHAPES, and more than 64 groups
+GROUPS = [(37, 32, 8, 3, 9), (203, 60, 6, 2, 4), (120, 64, 32, 3, 6), (1000, 256, 8, 4, 8), (500, 1024, 128, 9, 12), (16391, 256, 8, 2, 8),
+          (16391, 256, 4, 1, 4), (16391, 128, 2, 1, 8), (8209, 512, 16, 4, 8), (8209, 1024, 8, 3, 16), (32771, 128, 4, 2, 8)]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("by", ["logit", "bias"])
+@pytest.mark.parametrize("T,E,groups,top_groups,k", GROUPS)
+def test_groups_with_few_experts_left(T, E, groups, top_groups, k, by, score):
+    """Groups with none, one or two experts that are not masked: one with any comes before one with none, and the
+    groups that stay hold as many of them as there are, up to top_groups."""
+    rng, x, bias = _inputs(T, E, seed=T + E + 2)
+    size = E // groups
+    left = rng.choice([0, 0, 1, 1, 1, 2], (T, groups) if by == "logit" else (1, groups))
+    order = rng.random((left.shape[0], groups, size)).argsort(axis=2).argsort(axis=2)
+    out = (order >= left[:, :, None]).reshape(left.shape[0], E)
+    if by == "logit":
+        x[out] = -np.inf
+    else:
+        bias[out[0]] = -np.inf
+    left, out = np.broadcast_to(left, (T, groups)), np.broadcast_to(out, (T, E))
+    for b in (bias, None) if by == "logit" else (bias,):
+        print(f"case T={T} E={E} groups={groups} of which {top_groups} k={k} {score} by {by} bias={b is not None}", flush=True)
+        if b is None:
+            router = moe.Router(score, None, groups, top_groups, "top2", True, 1.0)
+            idx, _ = moe.route_experts(_gpu(x), k, router)
+            torch.cuda.synchronize()
+            ids = idx.cpu().numpy()
+            with np.errstate(invalid="ignore"):
+                want, _ = st.route_experts(x[:64], k, score, None, groups, top_groups, 2)
+            np.testing.assert_array_equal(ids[:64], want)
+        else:
+            ids, _ = _route(x, b, k, score, groups, top_groups, "top2")
+        if k >= 2 * top_groups:  # every expert that is left in the groups that stay is chosen
+            chosen = (~np.take_along_axis(out, ids, 1)).sum(axis=1)
+            twos, ones = (left == 2).sum(axis=1), (left == 1).sum(axis=1)
+            best = 2 * np.minimum(twos, top_groups) + np.minimum(ones, np.maximum(top_groups - twos, 0))
+            np.testing.assert_array_equal(chosen, best)

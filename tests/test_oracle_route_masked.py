@@ -46,3 +46,22 @@ def test_values_that_are_not_masked_are_untouched(score):
     bias = rng.standard_normal(8).astype(np.float32)
     s = st.sigmoid(x) if score == "sigmoid" else st.softmax(x)
     np.testing.assert_array_equal(st.choice_values(x, score, bias), (s + bias.astype(np.float64)).astype(np.float32))
+
+
+def test_groups_with_one_expert_left():
+    """Groups whose sum of two is -infinity are ranked by their largest value: one with an expert that is not masked
+    comes before one without."""
+    x = np.array([[-INF, -INF, -INF, 2.0, 1.0, -INF]], dtype=np.float32)
+    for score in ("sigmoid", "softmax"):
+        for bias in (None, np.zeros(6, dtype=np.float32), np.array([9, 9, 0, 0, 0, 0], dtype=np.float32)):
+            assert st.route_experts(x, 2, score, bias, 3, 1, 2)[0].tolist() == [[3, 2]]
+            assert st.route_experts(x, 2, score, bias, 3, 2, 2)[0].tolist() == [[3, 4]]
+    # and after every group with two
+    x[0, 0:2] = -20.0
+    assert st.route_experts(x, 2, "sigmoid", np.zeros(6, dtype=np.float32), 3, 1, 2)[0].tolist() == [[0, 1]]
+    # equal ones by their ids; by a bias of -infinity as by a mask
+    x = np.array([[1.0, 0.0, 1.0, 0.0]], dtype=np.float32)
+    bias = np.array([0, -INF, 0, -INF], dtype=np.float32)
+    assert st.route_experts(x, 1, "sigmoid", bias, 2, 1, 2)[0].tolist() == [[0]]
+    x[0, 2] = 1.5
+    assert st.route_experts(x, 1, "sigmoid", bias, 2, 1, 2)[0].tolist() == [[2]]

@@ -38,6 +38,8 @@ __device__ __forceinline__ uint32_t orderable(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+constexpr uint32_t kMinusInfinity = 0x007FFFFFu;  // orderable(-INFINITY)
+
 __device__ __forceinline__ float from_orderable(uint32_t o) {
   if (o == 1u) return __uint_as_float(0x7FC00000u);
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
@@ -174,6 +176,7 @@ __global__ __launch_bounds__(kThreads) void route_any_kernel(const RouteArgs a) 
     }
     wave_sync();
     if (a.top_groups < a.groups) {
+      bool minus = false;  // a sum of -infinity
       for (int g = lane; g < a.groups; g += kWave) {
         uint32_t first = 0, second = 0;
         for (int i = g * size; i < (g + 1) * size; ++i) {
@@ -182,15 +185,34 @@ __global__ __launch_bounds__(kThreads) void route_any_kernel(const RouteArgs a) 
           first = v > first ? v : first;
         }
         gv[g] = a.group_top == 2 && size > 1 ? orderable(from_orderable(first) + from_orderable(second)) : first;
+        minus = minus || gv[g] == kMinusInfinity;
       }
+      minus = __any(minus);
       wave_sync();
-      for (int g = lane; g < a.groups; g += kWave) {
+      auto largest = [&](int g) {
+        uint32_t top = 0;
+        for (int i = g * size; i < (g + 1) * size; ++i) top = c[i] > top ? c[i] : top;
+        return top;
+      };
+      uint32_t leaves = 0;  // of this lane's groups
+      for (int g = lane, n = 0; g < a.groups; g += kWave, ++n) {
         const uint32_t mine = gv[g];
         int before = 0;
-        for (int i = 0; i < a.groups; ++i) before += gv[i] > mine || (gv[i] == mine && i < g);
-        if (before >= a.top_groups)
-          for (int i = g * size; i < (g + 1) * size; ++i) c[i] = 0;
+        if (!minus)
+          for (int i = 0; i < a.groups; ++i) before += gv[i] > mine || (gv[i] == mine && i < g);
+        else {
+          const uint32_t top = mine == kMinusInfinity ? largest(g) : 0;
+          for (int i = 0; i < a.groups; ++i) {
+            const uint32_t other = gv[i] == mine && mine == kMinusInfinity ? largest(i) : top;
+            before += gv[i] > mine || (gv[i] == mine && (other > top || (other == top && i < g)));
+          }
+        }
+        leaves |= static_cast<uint32_t>(before >= a.top_groups) << n;
       }
+      wave_sync();
+      for (int g = lane, n = 0; g < a.groups; g += kWave, ++n)
+        if (leaves >> n & 1)
+          for (int i = g * size; i < (g + 1) * size; ++i) c[i] = 0;
       wave_sync();
     }
     uint64_t key[kPer];
@@ -342,6 +364,28 @@ __device__ __forceinline__ void other_lanes(int v, int g, int log_p, F&& f) {
   }
 }
 
+// Lanes of the groups before this one, by their values `mine`, those of -infinity (SUMS of two) by their largest,
+// `top`; then the lower group. OFTEN: where nearly every wave asks, and hardly any has a sum of -infinity.
+template <int G, bool SUMS, bool OFTEN>
+__device__ __forceinline__ int lanes_before(uint32_t mine, uint32_t top, int g, int log_p) {
+  const int group = g >> log_p;
+  int before = 0;
+  if (SUMS && (!OFTEN || __any(mine == kMinusInfinity))) {
+    top = mine == kMinusInfinity ? top : 0;
+#pragma unroll 1
+    for (int m = 1; m < G; ++m) {
+      const uint32_t other = __shfl_xor(mine, m), its_top = __shfl_xor(top, m);
+      before += other > mine || (other == mine && (its_top > top || (its_top == top && (g ^ m) >> log_p < group)));
+    }
+  } else {
+    other_lanes<G>(static_cast<int>(mine), g, log_p, [&](int value, int of) {
+      const uint32_t other = static_cast<uint32_t>(value);
+      before += other > mine || (other == mine && of < group);
+    });
+  }
+  return before;
+}
+
 template <int G, int OFF = 1, typename T>
 __device__ __forceinline__ T group_sum(T v) {
   if constexpr (OFF < G) return group_sum<G, 2 * OFF>(v + __shfl_xor(v, OFF));
@@ -456,8 +500,8 @@ struct Candidates {
   uint16_t id[kWave / G][kMost];
 };
 
-// The wave's tokens, with every score in fp64.
-template <int G, int VPL, int L, Route MODE>
+// The wave's tokens, with every score in fp64. BEHIND the search below: for few waves.
+template <int G, int VPL, int L, Route MODE, bool BEHIND>
 __device__ __forceinline__ void route_exact(const RouteArgs& a, const Rows<G, VPL>& in, int P) {
   constexpr int kSlots = (L + G - 1) / G;
   constexpr int kRun = VPL < L ? VPL : L;
@@ -527,12 +571,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, const Rows<G, VP
     uint32_t one = key_ord(best[0]), two = L > 1 ? key_ord(best[1]) : 0;
     merge_two<G>(one, two, P);
     const uint32_t mine = a.group_top == 2 && size > 1 ? orderable(from_orderable(one) + from_orderable(two)) : one;
-    int before = 0;  // lanes of groups before this one
-    other_lanes<G>(static_cast<int>(mine), g, __ffs(P) - 1, [&](int value, int of) {
-      const uint32_t other = static_cast<uint32_t>(value);
-      before += other > mine || (other == mine && of < group);
-    });
-    if (before >= a.top_groups * P)
+    if (lanes_before<G, kScores, !BEHIND>(mine, one, g, __ffs(P) - 1) >= a.top_groups * P)
 #pragma unroll
       for (int i = 0; i < L; ++i) best[i] = 1.0;
   }
@@ -722,11 +761,7 @@ __device__ __forceinline__ bool route_quick(const RouteArgs& a, const Rows<G, VP
                                : a.group_top == 2 && size > 1
                                    ? orderable(from_orderable(first_ord) + from_orderable(second_ord))
                                    : first_ord;
-      int before = 0;
-      other_lanes<G>(static_cast<int>(rank_by), g, __ffs(P) - 1, [&](int value, int of) {
-        const uint32_t other = static_cast<uint32_t>(value);
-        before += other > rank_by || (other == rank_by && of < in.group);
-      });
+      const int before = lanes_before<G, true, false>(rank_by, first_ord, g, __ffs(P) - 1);
       above = close ? before : above;
     }
     if (above >= a.top_groups * P) {
@@ -870,7 +905,7 @@ __global__ __launch_bounds__(kThreads, (route_waves<G, MODE>())) void route_kern
       __shared__ Candidates<G, L> room[kWavesPerBlock];
       if (route_quick<G, VPL, L, MODE>(a, in, P, room[wv])) continue;
     }
-    route_exact<G, VPL, L, MODE>(a, in, P);
+    route_exact<G, VPL, L, MODE, QUICK>(a, in, P);
   }
 }
 
