@@ -1549,7 +1549,6 @@ def adamw_states(params, bits: int = 32):
 
 
 _dtype_of = operator.attrgetter("dtype")
-_rounding_of = operator.attrgetter("rounding")
 _ROUNDINGS = {"nearest": MOE_NEAREST, "dither": MOE_DITHER}
 _NEAREST_BETA = 0.95  # states built without a rounding: the nearest code up to this beta
 
@@ -1580,7 +1579,7 @@ def _state_list(ts, name: str, params, sizes, numels):
     if len(kinds) > 1:
         raise TypeError(f"{name} must hold fp32 tensors or Float8State, not both")
     codes = _same_list([t.codes for t in ts], name, params, sizes, {torch.float8_e4m3fn})
-    scales, rounding = [t.scale for t in ts], set(map(_rounding_of, ts))
+    scales, rounding = [t.scale for t in ts], {t.rounding for t in ts}
     blocks = [(-(-n // MOE_STATE_BLOCK),) for n in numels]
     try:
         if {torch.float32}.issuperset(map(_dtype_of, scales)) and list(map(torch.Tensor.size, scales)) == blocks:
@@ -1594,11 +1593,11 @@ def _state_list(ts, name: str, params, sizes, numels):
 
 def _rounding(asked, betas) -> int:
     """The one rounding of a step's 8-bit states."""
-    if None in asked:
-        asked = (asked - {None}) | {"dither" if max(betas) > _NEAREST_BETA else "nearest"}
-    if len(asked) != 1 or not asked <= set(_ROUNDINGS):
+    default = "dither" if max(betas) > _NEAREST_BETA else "nearest"
+    codes = {_ROUNDINGS.get(default if r is None else r) for r in asked}
+    if len(codes) != 1 or None in codes:
         raise ValueError(f"the states of a step must have one rounding of {sorted(_ROUNDINGS)}, got {sorted(map(str, asked))}")
-    return _ROUNDINGS[asked.pop()]
+    return codes.pop()
 
 
 def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
